@@ -4,7 +4,7 @@ Four operators: writing a matrix in MXFP4 (blocks of 32 values, E2M1 elements, o
 each) and reading it back, the product of two MXFP4 matrices, the product of a few bf16 rows with an
 MXFP4 matrix, and a whole mixture-of-experts layer for a few tokens with bf16 or MXFP4 experts.
 
-Layout of an MXFP4 matrix [rows, K]: codes uint8 [rows, ceil(K/32)*16], two codes a byte, the even k in the
+Layout of an MXFP4 matrix [rows, K]: codes uint8 [rows, ceil(K/128)*64], two codes a byte, the even k in the
 low half; scales uint8 [rows, ceil(K/32) rounded up to 16], 2^(byte - 127); padding is zero.
 """
 import math
@@ -78,13 +78,12 @@ def _normal(g, shape, scale=1.0, dtype=torch.float32):
 
 
 def _pitches(K):
-    blocks = -(-K // 32)
-    return blocks * 16, -(-blocks // 16) * 16
+    return -(-K // 128) * 64, -(-K // 512) * 16
 
 
 def _blocks(v):
-    """[..., K] -> fp32 [..., ceil(K/32), 32], zeros past K."""
-    pad = -v.shape[-1] % 32
+    """[..., K] -> fp32 [..., 4 ceil(K/128), 32], zeros past K."""
+    pad = -v.shape[-1] % 128
     v = torch.nn.functional.pad(v.float(), (0, pad)) if pad else v.float()
     return v.reshape(*v.shape[:-1], -1, 32)
 
@@ -104,7 +103,7 @@ def _pack(v):
     """MXFP4 codes and scales of [rows, K] (or [E, rows, K]) values."""
     code, s = _encode(_blocks(v))
     byte = code[..., 0::2] | (code[..., 1::2] << 4)
-    scales = torch.nn.functional.pad((s + 127).to(torch.uint8), (0, -s.shape[-1] % 16))
+    scales = torch.nn.functional.pad((s + 127).to(torch.uint8), (0, -s.shape[-1] % 16))  # an empty block's byte is 0
     return byte.flatten(-2).contiguous(), scales.contiguous()
 
 
