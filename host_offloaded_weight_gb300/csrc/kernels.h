@@ -1,5 +1,6 @@
 // Internal kernel launchers of the layer-streaming library (not part of the C ABI).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -129,5 +130,29 @@ cudaError_t launch_canary(void* base, int64_t stride, int count, bool check, uin
 // 0..T*k-1. Reads only inside those arrays. Raises DERR_BOUNDS | (region0 + layer) << 8.
 cudaError_t launch_moe_check(const int* sel, const int* row_table, const int* bounds, int n_layers, int T,
                              int k, int E, uint32_t* err_word, uint32_t region0, cudaStream_t s);
+
+// ---------------------------------------------------------------- MXFP4
+// Row pitches in bytes: codes are padded to 128 values (64 bytes: the tensor copies' 4-bit
+// form wants whole runs of 128), scales to 16 bytes (512 values).
+inline int64_t mx_code_pitch(int64_t K) { return (K + 127) / 128 * 64; }
+inline int64_t mx_scale_pitch(int64_t K) { return (K + 511) / 512 * 16; }
+cudaError_t launch_mx_quantize(const void* src, bool f32, int64_t rows, int K, int64_t ld, void* codes, void* scales,
+                               cudaStream_t s);
+cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t rows, int K, void* dst, bool f32,
+                                 int64_t ld, cudaStream_t s);
+typedef CUresult (*MxEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+MxEncodeFn mx_encode_fn();  // the driver's tensor map encoder; NULL without a driver
+cudaError_t launch_gemm_mx(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales, void* C,
+                           bool c_f32, int M, int N, int K, uint32_t* err, cudaStream_t s);
+// bf16 x MXFP4: ws holds the split rows, the tickets and the partial sums (act_mx_ws_bytes, 256-byte aligned).
+int64_t act_mx_ws_bytes(int M, int N, int K);
+cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, const void* b_scales, void* C, bool c_f32,
+                               int M, int N, int K, void* ws, uint32_t* err, cudaStream_t s);
+
+// ---------------------------------------------------------------- shared by the standalone entry points
+uint32_t* entry_error_word();       // device address of the word behind lsk_device_error
+cudaMemPool_t entry_scratch_pool();  // the current device's pool for short-lived scratch; NULL if refused
 
 }  // namespace ls

@@ -143,6 +143,12 @@ _sig = {
     "lsk_moe_check": (_I32, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P]),
     "lsk_moe_group_masked": (_I32, [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "lsk_moe_rows_copy": (_I32, [_P, _P, _P, _P, _I32, _I32, _P, _P, _U32, _I32, _P]),
+    "lsk_mxfp4_code_pitch": (_I64, [_I32]),
+    "lsk_mxfp4_scale_pitch": (_I64, [_I32]),
+    "lsk_mxfp4_quantize": (_I32, [_P, _I32, _I64, _I32, _I64, _P, _P, _P]),
+    "lsk_mxfp4_dequantize": (_I32, [_P, _P, _I64, _I32, _P, _I32, _I64, _P]),
+    "lsk_gemm_mxfp4": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
+    "lsk_gemm_bf16_mxfp4": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "ls_helper_share": (C.c_double, [_I64]),
     "ls_host_alloc": (_I32, [_U64, C.POINTER(_P)]),
     "ls_host_free": (_I32, [_P]),
@@ -535,3 +541,43 @@ def ls_helper_split(routed, share: float):
 def lsk_moe_combine(x, y, T, k, H, out, out32=None, stream=None) -> int:
     xf32 = int("float32" in str(getattr(x, "dtype", "")))
     return _check(_lib.lsk_moe_combine(_ptr(x), xf32, _ptr(y), T, k, H, _ptr(out), _ptr(out32), _stream(stream)))
+
+
+# ------------------------------------------------------------------ MXFP4
+def _is_f32(t) -> int:
+    return int("float32" in str(getattr(t, "dtype", "")))
+
+
+def lsk_mxfp4_code_pitch(K: int) -> int:
+    """Bytes of a row of K 4-bit codes."""
+    return _lib.lsk_mxfp4_code_pitch(K)
+
+
+def lsk_mxfp4_scale_pitch(K: int) -> int:
+    """Bytes of a row's block scales."""
+    return _lib.lsk_mxfp4_scale_pitch(K)
+
+
+def lsk_mxfp4_quantize(src, rows: int, K: int, codes, scales, ld: int | None = None, stream=None) -> int:
+    """src [rows, K] bf16 or float32, ld elements between rows (None = K)."""
+    return _check(_lib.lsk_mxfp4_quantize(_ptr(src), _is_f32(src), rows, K, K if ld is None else ld, _ptr(codes),
+                                          _ptr(scales), _stream(stream)))
+
+
+def lsk_mxfp4_dequantize(codes, scales, rows: int, K: int, dst, ld: int | None = None, stream=None) -> int:
+    """dst [rows, K] bf16 or float32, ld elements between rows (None = K)."""
+    return _check(_lib.lsk_mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, K, _ptr(dst), _is_f32(dst),
+                                            K if ld is None else ld, _stream(stream)))
+
+
+def lsk_gemm_mxfp4(A_codes, A_scales, B_codes, B_scales, C_out, M: int, N: int, K: int, stream=None) -> int:
+    """C_out [M, N] bf16 or float32."""
+    return _check(_lib.lsk_gemm_mxfp4(_ptr(A_codes), _ptr(A_scales), _ptr(B_codes), _ptr(B_scales), _ptr(C_out),
+                                      _is_f32(C_out), M, N, K, _stream(stream)))
+
+
+def lsk_gemm_bf16_mxfp4(A, B_codes, B_scales, C_out, M: int, N: int, K: int, lda: int | None = None,
+                        stream=None) -> int:
+    """A [M, K] bf16, lda elements between rows (None = K); C_out [M, N] bf16 or float32."""
+    return _check(_lib.lsk_gemm_bf16_mxfp4(_ptr(A), K if lda is None else lda, _ptr(B_codes), _ptr(B_scales),
+                                           _ptr(C_out), _is_f32(C_out), M, N, K, _stream(stream)))

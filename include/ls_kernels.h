@@ -182,6 +182,45 @@ ls_status lsk_moe_combine(const void* x_dev, int32_t x_f32, const float* y_dev, 
 ls_status lsk_moe_check(const int32_t* sel_dev, const int32_t* row_table_dev, const int32_t* group_bounds_dev,
                         int32_t n_layers, int32_t T, int32_t k, int32_t E, uint32_t* err_host, void* stream);
 
+/* ---- MXFP4: microscaled 4-bit floats (OCP Microscaling Formats 1.0) -------------------
+ * A row of K values in blocks of 32. Block scale 2^s as one byte s + 127 (E8M0),
+ * s = floor(log2 max|v|) - 2, at least -127; elements E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives), v 2^-s rounded to the nearest, ties to the even code, saturating at 6. An all-zero
+ * block has scale byte 0. A block with a NaN or an infinity has scale byte 255 and reads back as
+ * NaN. Weights in this form take 17/64 of their bf16 bytes (of a slot, and of the host link).
+ *
+ * A matrix [rows, K]: codes, two a byte (even k in the low half), lsk_mxfp4_code_pitch(K) =
+ * 64 ceil(K/128) bytes a row; scales, lsk_mxfp4_scale_pitch(K) = 16 ceil(K/512) bytes a row.
+ * Both are dense in rows, and zero past K: the products read the padding, so a caller that writes
+ * the format itself has to write those zeros. codes 32-byte aligned, scales 16-byte aligned
+ * everywhere. 1 <= K <= 2^24. */
+int64_t lsk_mxfp4_code_pitch(int32_t K);   /* 0 for K < 1 */
+int64_t lsk_mxfp4_scale_pitch(int32_t K);
+
+/* src_dev [rows, K] bf16 (fp32 when src_f32 != 0), ld >= K elements between rows -> codes_dev,
+ * scales_dev. Any row alignment (16-byte aligned rows are read 16 bytes at a time). */
+ls_status lsk_mxfp4_quantize(const void* src_dev, int32_t src_f32, int64_t rows, int32_t K, int64_t ld,
+                             void* codes_dev, void* scales_dev, void* stream);
+
+/* The values that the codes stand for, bf16 or fp32 (both exact), ld >= K elements between rows. */
+ls_status lsk_mxfp4_dequantize(const void* codes_dev, const void* scales_dev, int64_t rows, int32_t K,
+                               void* dst_dev, int32_t dst_f32, int64_t ld, void* stream);
+
+/* C[M,N] = A[M,K] B[N,K]^T with both operands in MXFP4, fp32 sums, C dense bf16 (fp32 when
+ * c_f32 != 0), any M, N and K. The activations' side is written by lsk_mxfp4_quantize. */
+ls_status lsk_gemm_mxfp4(const void* a_codes_dev, const void* a_scales_dev, const void* b_codes_dev,
+                         const void* b_scales_dev, void* C_dev, int32_t c_f32, int32_t M, int32_t N, int32_t K,
+                         void* stream);
+
+/* C[M,N] = A[M,K] B[N,K]^T with A bf16 (lda >= K elements between rows) and B in MXFP4, fp32
+ * sums, C dense bf16 (fp32 when c_f32 != 0). Any M; made for few tokens (M = 1 upwards), where it streams the
+ * weights once at 17/32 byte a value. A keeps its eight bits: values down to 2^-13 of the
+ * largest of their block of 32 enter exactly, smaller ones within 2^-22 of that largest. A NaN or an
+ * infinity in a row of A makes that row of C NaN. Takes scratch on `stream` from the library's
+ * pool, as lsk_gemm_bf16 does (LS_ERR_OOM if refused). */
+ls_status lsk_gemm_bf16_mxfp4(const void* A_dev, int64_t lda, const void* b_codes_dev, const void* b_scales_dev,
+                              void* C_dev, int32_t c_f32, int32_t M, int32_t N, int32_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
