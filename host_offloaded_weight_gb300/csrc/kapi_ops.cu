@@ -87,4 +87,56 @@ ls_status lsk_gemm_bf16_mxfp4(const void* A, int64_t lda, const void* b_codes, c
                                         (cudaStream_t)stream));
 }
 
+ls_status lsk_moe_few(const void* x, const float* resid, const float* logits, const lsk_moe_experts* w, int32_t T,
+                      int32_t E, int32_t k, int32_t H, int32_t F, void* out, float* out32, void* stream) {
+    if (!w || T < 0 || E < 1 || k < 1 || k > E || H < 8 || F < 8 || (H % 8) || (F % 8) || H > MX_MAX_K || F > MX_MAX_K)
+        return LS_ERR_INVALID_ARG;
+    if (T > 64 || E > 256 || k > 8) return LS_ERR_UNSUPPORTED;
+    if (T == 0) return LS_OK;
+    const bool mx = w->mxfp4 != 0;
+    const uintptr_t al = mx ? 32 : 16;
+    if (!x || !logits || !out || !w->gate || !w->up || !w->down || !aligned(x, 16) || !aligned(resid, 4) ||
+        !aligned(logits, 4) || !aligned(out, 2) || !aligned(out32, 4) || !aligned(w->gate, al) || !aligned(w->up, al) ||
+        !aligned(w->down, al))
+        return LS_ERR_INVALID_ARG;
+    const int64_t up_bytes = (int64_t)F * (mx ? mx_code_pitch(H) : 2ll * H);
+    const int64_t down_bytes = (int64_t)H * (mx ? mx_code_pitch(F) : 2ll * F);
+    // a stride may be anything with one expert; the tensor copies want multiples of 16 bytes below 2^40
+    const int64_t gs = E == 1 ? up_bytes : w->gate_stride, ds = E == 1 ? down_bytes : w->down_stride;
+    if (gs < up_bytes || ds < down_bytes || (gs % 16) || (ds % 16) || gs >= (1ll << 40) || ds >= (1ll << 40))
+        return LS_ERR_INVALID_ARG;
+    MoeFewDesc d;
+    if (mx) {
+        const int64_t ub = F * mx_scale_pitch(H), db = H * mx_scale_pitch(F);
+        d.gate_scale_stride = E == 1 ? ub : w->gate_scale_stride;
+        d.down_scale_stride = E == 1 ? db : w->down_scale_stride;
+        if (!w->gate_scales || !w->up_scales || !w->down_scales || !aligned(w->gate_scales, 16) ||
+            !aligned(w->up_scales, 16) || !aligned(w->down_scales, 16) || d.gate_scale_stride < ub ||
+            d.down_scale_stride < db || (d.gate_scale_stride % 16) || (d.down_scale_stride % 16))
+            return LS_ERR_INVALID_ARG;
+    }
+    d.x = x;
+    d.resid = resid;
+    d.logits = logits;
+    d.mx = mx;
+    d.gate = w->gate;
+    d.up = w->up;
+    d.down = w->down;
+    d.gate_stride = gs;
+    d.down_stride = ds;
+    d.gate_scales = w->gate_scales;
+    d.up_scales = w->up_scales;
+    d.down_scales = w->down_scales;
+    d.T = T;
+    d.E = E;
+    d.k = k;
+    d.H = H;
+    d.F = F;
+    d.out = out;
+    d.out32 = out32;
+    Scratch ws((cudaStream_t)stream);
+    if (!ws.take(moe_few_ws_bytes(T, k, F))) return LS_ERR_OOM;
+    return status_of(launch_moe_few(d, ws.p, entry_error_word(), (cudaStream_t)stream));
+}
+
 }  // extern "C"

@@ -151,6 +151,27 @@ int64_t act_mx_ws_bytes(int M, int N, int K);
 cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, const void* b_scales, void* C, bool c_f32,
                                int M, int N, int K, void* ws, uint32_t* err, cudaStream_t s);
 
+// ---------------------------------------------------------------- MoE layer for a few tokens
+struct MoeFewDesc {
+    const void* x = nullptr;        // [T, H] bf16
+    const float* resid = nullptr;   // [T, H], or NULL: x
+    const float* logits = nullptr;  // [T, E]
+    bool mx = false;                // experts in MXFP4 (codes and scales), else bf16
+    const void* gate = nullptr;
+    const void* up = nullptr;
+    const void* down = nullptr;
+    int64_t gate_stride = 0, down_stride = 0;              // bytes between experts (gate and up alike)
+    const void* gate_scales = nullptr;
+    const void* up_scales = nullptr;
+    const void* down_scales = nullptr;
+    int64_t gate_scale_stride = 0, down_scale_stride = 0;
+    int T = 0, E = 0, k = 0, H = 0, F = 0;
+    void* out = nullptr;            // [T, H] bf16
+    float* out32 = nullptr;         // [T, H], or NULL
+};
+int64_t moe_few_ws_bytes(int T, int k, int F);
+cudaError_t launch_moe_few(const MoeFewDesc& d, void* ws, uint32_t* err, cudaStream_t s);
+
 // ---------------------------------------------------------------- shared by the standalone entry points
 uint32_t* entry_error_word();       // device address of the word behind lsk_device_error
 cudaMemPool_t entry_scratch_pool();  // the current device's pool for short-lived scratch; NULL if refused

@@ -67,6 +67,13 @@ class ls_moe_routing(C.Structure):
     _fields_ = [("logits", C.c_void_p), ("top_k", C.c_int32)]
 
 
+class lsk_moe_experts(C.Structure):
+    _fields_ = [("mxfp4", C.c_int32), ("reserved", C.c_int32), ("gate", C.c_void_p), ("up", C.c_void_p),
+                ("down", C.c_void_p), ("gate_stride", C.c_int64), ("down_stride", C.c_int64),
+                ("gate_scales", C.c_void_p), ("up_scales", C.c_void_p), ("down_scales", C.c_void_p),
+                ("gate_scale_stride", C.c_int64), ("down_scale_stride", C.c_int64)]
+
+
 class ls_kernel_time(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("launches", C.c_int64), ("total_ms", C.c_double)]
 
@@ -149,6 +156,7 @@ _sig = {
     "lsk_mxfp4_dequantize": (_I32, [_P, _P, _I64, _I32, _P, _I32, _I64, _P]),
     "lsk_gemm_mxfp4": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "lsk_gemm_bf16_mxfp4": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
+    "lsk_moe_few": (_I32, [_P, _P, _P, C.POINTER(lsk_moe_experts), _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "ls_helper_share": (C.c_double, [_I64]),
     "ls_host_alloc": (_I32, [_U64, C.POINTER(_P)]),
     "ls_host_free": (_I32, [_P]),
@@ -581,3 +589,22 @@ def lsk_gemm_bf16_mxfp4(A, B_codes, B_scales, C_out, M: int, N: int, K: int, lda
     """A [M, K] bf16, lda elements between rows (None = K); C_out [M, N] bf16 or float32."""
     return _check(_lib.lsk_gemm_bf16_mxfp4(_ptr(A), K if lda is None else lda, _ptr(B_codes), _ptr(B_scales),
                                            _ptr(C_out), _is_f32(C_out), M, N, K, _stream(stream)))
+
+
+def _stride_bytes(t) -> int:
+    """Bytes between the experts of a stacked tensor."""
+    return t.stride(0) * t.element_size()
+
+
+def lsk_moe_few(x, logits, gate, up, down, T: int, E: int, k: int, H: int, F: int, out, gate_scales=None,
+                up_scales=None, down_scales=None, resid=None, out32=None, stream=None) -> int:
+    """One MoE layer for T <= 64 tokens. gate, up [E, F, H] and down [E, H, F] bf16, or MXFP4 codes
+    [E, rows, code pitch] with their scales [E, rows, scale pitch]; an expert's rows are dense."""
+    w = lsk_moe_experts(int(gate_scales is not None), 0, _ptr(gate), _ptr(up), _ptr(down), _stride_bytes(gate),
+                        _stride_bytes(down), _ptr(gate_scales), _ptr(up_scales), _ptr(down_scales),
+                        0 if gate_scales is None else _stride_bytes(gate_scales),
+                        0 if down_scales is None else _stride_bytes(down_scales))
+    if _stride_bytes(up) != w.gate_stride or (w.mxfp4 and _stride_bytes(up_scales) != w.gate_scale_stride):
+        raise ValueError("gate and up need the same distance between experts")
+    return _check(_lib.lsk_moe_few(_ptr(x), _ptr(resid), _ptr(logits), C.byref(w), T, E, k, H, F, _ptr(out),
+                                   _ptr(out32), _stream(stream)))

@@ -221,6 +221,41 @@ ls_status lsk_gemm_mxfp4(const void* a_codes_dev, const void* a_scales_dev, cons
 ls_status lsk_gemm_bf16_mxfp4(const void* A_dev, int64_t lda, const void* b_codes_dev, const void* b_scales_dev,
                               void* C_dev, int32_t c_f32, int32_t M, int32_t N, int32_t K, void* stream);
 
+/* The experts of one MoE layer: gate and up [F, H] and down [H, F] of each, row-major, an
+ * expert's matrix a fixed number of bytes after the one before (the gate and up matrices
+ * alike), so that stacked tensors [E, F, H] and expert-major blobs both fit. bf16, or MXFP4
+ * (mxfp4 != 0: the pointers are codes, with the scales beside them). Strides are multiples of 16
+ * bytes; matrices 16-byte aligned (32 for MXFP4 codes). */
+typedef struct lsk_moe_experts {
+    int32_t mxfp4;
+    int32_t reserved;
+    const void* gate;
+    const void* up;
+    const void* down;
+    int64_t gate_stride;
+    int64_t down_stride;
+    const void* gate_scales;
+    const void* up_scales;
+    const void* down_scales;
+    int64_t gate_scale_stride;
+    int64_t down_scale_stride;
+} lsk_moe_experts;
+
+/* A whole MoE layer for a few tokens, in two launches:
+ *   out[t] = r[t] + sum_{j<k} w[t,j] D_e (SiLU(G_e x[t]) * (U_e x[t])),  e = sel[t,j]
+ * with sel and w as lsk_moe_route gives them from logits_dev [T, E] fp32 (the k largest, ties to the
+ * lower expert, softmax over the chosen), r = resid_dev [T, H] fp32, or x_dev when that is NULL.
+ * x_dev [T, H] bf16 (16-byte aligned), out_dev [T, H] bf16; out32_dev (may be NULL) gets the fp32
+ * result. A NaN logit counts as the lowest one and makes its token NaN if it is chosen; a token
+ * whose logits are all -infinity gets no expert (out = r). Sums are fp32 in a fixed order; the
+ * hidden activation is rounded once (to bf16, or with MXFP4 experts to f16 times a power of two
+ * for each 32, as x is for each row). T <= 64, E <= 256, k <= 8 (LS_ERR_UNSUPPORTED above:
+ * lsk_moe_route to lsk_moe_combine serve more tokens), H and F multiples of 8. Takes scratch on
+ * `stream` from the library's pool (LS_ERR_OOM if refused). */
+ls_status lsk_moe_few(const void* x_dev, const float* resid_dev, const float* logits_dev,
+                      const lsk_moe_experts* experts, int32_t T, int32_t E, int32_t k, int32_t H, int32_t F,
+                      void* out_dev, float* out32_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
