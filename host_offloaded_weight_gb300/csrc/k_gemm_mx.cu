@@ -19,7 +19,8 @@
 // products; the others write the results. The scales' TMEM columns belong to the stage, so
 // the barrier that frees a stage orders their reuse too.
 //
-// Sums are fp32 and each output is written by one thread from a fixed order of sums.
+// Few tiles (bf16 x 4-bit) are shared along K by a cluster of CTAs, whose sums meet in the first one's shared
+// memory. Sums are fp32 and each output is written by one thread from a fixed order of sums.
 #include <algorithm>
 #include <mutex>
 
@@ -31,25 +32,40 @@ namespace {
 
 using namespace tc;
 
-enum { MX_MX = 0, ACT_MX = 1 };
+// MX_MX: both operands MXFP4. ACT: the right operand is the split rows in memory.
+// ACT_IN: up to 16 bf16 rows, split by the scale warps on their way into each stage.
+enum { MX_MX = 0, ACT = 1, ACT_IN = 2 };
 
 constexpr int TILE_P = 128;               // rows of the left operand in a tile
 constexpr int P_BYTES = TILE_P * 128;     // a stage of it
 
 template <int MODE, int BQ>
 struct Cfg {
+    static constexpr int TN = BQ / 2;                          // ACT: tokens of a tile (two terms each)
     static constexpr int QUADS = MODE == MX_MX ? 2 : 1;        // words of four blocks (128 values of K) in a stage
+    static constexpr int PER = 4 / QUADS;                      // stages of one 16-byte load of scales
     static constexpr int PARTS = (BQ + 127) / 128;             // 128-row parts of the right operand's scales
     static constexpr int Q_BYTES = BQ * 128;
     static constexpr int SCALE_BYTES = QUADS * (1 + PARTS) * 512;
     static constexpr int STAGE = (P_BYTES + Q_BYTES + SCALE_BYTES + 1023) / 1024 * 1024;
     static constexpr int EPI_WARPS = MODE == MX_MX ? 8 : 4;
-    static constexpr int EPI_BYTES = MODE == MX_MX ? EPI_WARPS * 32 * 33 * 4 : 0;
+    // CTAs that may share a tile along K, and the room for the others' sums in the first one's memory
+    static constexpr int MAX_SPLIT = MODE == MX_MX ? 1 : TN == 8 ? 8 : TN <= 32 ? 4 : TN == 64 ? 2 : 1;
+    static constexpr int RED_BYTES = (MAX_SPLIT - 1) * TN * TILE_P * 4;
+    static constexpr int EPI_BYTES = MODE == MX_MX ? EPI_WARPS * 4096 : RED_BYTES;
     static constexpr int FIT = (232448 - 1024 - 512 - EPI_BYTES) / STAGE;
     static constexpr int STAGES = FIT < 10 ? FIT : 10;
     static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024 + 512;
-    static constexpr int THREADS = 32 * (6 + EPI_WARPS);
+    static constexpr int FIRST_EPI = MODE == ACT_IN ? 10 : 6;   // the first warp of the epilogue
+    static constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
     static constexpr int ACCS = 2 * BQ + STAGES * QUADS * 4 * (1 + PARTS) <= 512 ? 2 : 1;
+    // The scale warps work in teams that take turns of RUN stages. A turn begins at most a round of the
+    // ring after the team's last one: a wait by parity cannot tell a phase from the one two before it.
+    static constexpr int SCALE_WARPS = MODE == ACT_IN ? 8 : 4;
+    static constexpr int TEAM = MODE == ACT_IN ? 1 : 2;         // warps of a team
+    static constexpr int TEAMS = SCALE_WARPS / TEAM;
+    static constexpr int RUN = MODE == ACT_IN ? 1 : 2;
+    static_assert(TEAMS * RUN <= STAGES, "a team's turns are within a round of the ring");
     static constexpr int SCALE_COLS = QUADS * 4 * (1 + PARTS);  // TMEM columns of a stage's scales
     static_assert(ACCS * BQ + STAGES * SCALE_COLS <= 512, "tensor memory");
     static_assert(BQ % 16 == 0 && BQ <= 256, "columns of a product");
@@ -60,60 +76,47 @@ struct MxParams {
     const uint8_t* scale_p;
     const uint8_t* scale_q;
     int scale_pitch;
-    int rows_p, rows_q;   // rows of the operands (ACT_MX: rows_q = tokens)
-    int q_term_rows;      // ACT_MX: rows between the two terms
+    int rows_p, rows_q;   // rows of the operands (ACT: rows_q = tokens)
+    int q_term_rows;      // ACT: rows between the two terms
     int k_stages;         // stages along K
     int tiles_p, tiles_q, tiles;
+    int splits;           // CTAs (a cluster) that share a tile along K
+    const __nv_bfloat16* a;  // ACT_IN: the rows themselves
+    int64_t lda;
+    int K, vec;
     void* C;
     int64_t ldc;
-    int c_f32;
-    float* partial;       // ACT_MX: [2 * grid][BQ / 2][128] sums of tiles that several CTAs share
-    uint32_t* tickets;    // ACT_MX: [tiles][4], zero before the launch
+    int c_f32, c_vec;     // c_vec: groups of four columns are whole and aligned
     uint32_t* err;
 };
 
-// The pieces of work of a CTA, in order. 4-bit x 4-bit: whole tiles. bf16 x 4-bit: the tiles'
-// stages in one line, cut evenly over the CTAs, so that every SM streams the same share of
-// the weights whatever the number of tiles; a tile that is cut is summed by its last CTA.
-template <int MODE>
+// The tiles of a CTA, in order, and its stages of each: with splits > 1 a cluster has one tile,
+// and its CTAs a run of whole scale groups each.
+template <int PER>
 struct Work {
-    int64_t pos, end;
-    int k_stages, tile, k0, k1;
-    __device__ __forceinline__ Work(const MxParams& p) : k_stages(p.k_stages), tile(0), k0(0), k1(0) {
-        if (MODE == MX_MX) {
-            pos = blockIdx.x;
-            end = p.tiles;
-        } else {
-            const int64_t total = (int64_t)p.tiles * p.k_stages;
-            pos = blockIdx.x * total / gridDim.x;
-            end = (blockIdx.x + 1) * total / gridDim.x;
-        }
+    int tile, step, tiles, k0, k1;
+    __device__ __forceinline__ Work(const MxParams& p) {
+        const int slice = (int)blockIdx.x % p.splits, groups = (p.k_stages + PER - 1) / PER;
+        step = (int)gridDim.x / p.splits;
+        tile = (int)blockIdx.x / p.splits - step;
+        tiles = p.tiles;
+        k0 = (int)((int64_t)slice * groups / p.splits) * PER;
+        k1 = min(p.k_stages, (int)((int64_t)(slice + 1) * groups / p.splits) * PER);
     }
     __device__ __forceinline__ bool next() {
-        if (pos >= end) return false;
-        if (MODE == MX_MX) {
-            tile = (int)pos;
-            k0 = 0;
-            k1 = k_stages;
-            pos += gridDim.x;
-        } else {
-            tile = (int)(pos / k_stages);
-            k0 = (int)(pos - (int64_t)tile * k_stages);
-            k1 = (int)min((int64_t)k_stages, k0 + (end - pos));
-            pos += k1 - k0;
-        }
-        return true;
+        tile += step;
+        return tile < tiles;
     }
 };
 
-template <int MODE>
-__device__ __forceinline__ void tile_at(const MxParams& p, int tile, int bq, int& row_p, int& row_q) {
+template <int MODE, int BQ>
+__device__ __forceinline__ void tile_at(const MxParams& p, int tile, int& row_p, int& row_q) {
     if (MODE == MX_MX) {
         row_p = tile % p.tiles_p * TILE_P;
-        row_q = tile / p.tiles_p * bq;
+        row_q = tile / p.tiles_p * BQ;
     } else {  // the token tiles of one weight tile follow one another
         row_p = tile / p.tiles_q * TILE_P;
-        row_q = tile % p.tiles_q * (bq / 2);
+        row_q = tile % p.tiles_q * (BQ / 2);
     }
 }
 
@@ -122,10 +125,111 @@ __device__ __forceinline__ void store_c(const MxParams& p, int64_t at, float v) 
     else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
 }
 
+// Eight values of a bf16 row from k on, zeros past K.
+__device__ __forceinline__ uint4 row8(const __nv_bfloat16* row, int k, int K, int vec) {
+    if (vec && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+    uint32_t w[4] = {0, 0, 0, 0};
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (k + j < K) w[j >> 1] |= (uint32_t)s[k + j] << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The two E4M3 terms of eight values and the scale bytes of their block (see the top). Four
+// neighbouring lanes hold a block; every lane of the warp takes part.
+__device__ __forceinline__ void split8(uint4 raw, uint2& o1, uint2& o2, uint32_t& b1, uint32_t& b2) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // s1 = e - 127 - 7 and s2 = s1 - 5 as bytes, not below 0; a block with a NaN or an infinity reads as NaN
+    const uint32_t e = m >> 7;
+    b1 = e == 255 ? 255 : e < 7 ? 0 : e - 7;
+    b2 = e == 255 ? 255 : e < 12 ? 0 : e - 12;
+    const float f1 = __uint_as_float((254 - min(b1, 253u)) << 23), u1 = e8m0_to_float(min(b1, 254u));
+    const float f2 = __uint_as_float((254 - min(b2, 253u)) << 23);
+    uint16_t t1[4], t2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float x = __uint_as_float(w[j] << 16), y = __uint_as_float(w[j] & 0xffff0000u);
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t1[j]) : "f"(y * f1), "f"(x * f1));
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(t1[j]));
+        const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        const float rx = x - d.x * u1, ry = y - d.y * u1;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t2[j]) : "f"(ry * f2), "f"(rx * f2));
+    }
+    o1 = make_uint2(t1[0] | (uint32_t)t1[1] << 16, t1[2] | (uint32_t)t1[3] << 16);
+    o2 = make_uint2(t2[0] | (uint32_t)t2[1] << 16, t2[2] | (uint32_t)t2[3] << 16);
+    if (e == 255) o1 = o2 = make_uint2(0, 0);
+}
+
+__device__ __forceinline__ void st_shared2(uint32_t at, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
+__device__ __forceinline__ void load_words(const uint8_t* p, bool in, uint4& v) {
+    v = in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
+__device__ __forceinline__ void load_words(const uint8_t* p, bool in, uint2& v) {
+    v = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+}
+__device__ __forceinline__ void load_words(const uint8_t* p, bool in, uint32_t& v) {
+    v = in ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+}
+template <int BYTES> struct Words;
+template <> struct Words<4> { typedef uint32_t type; };
+template <> struct Words<8> { typedef uint2 type; };
+template <> struct Words<16> { typedef uint4 type; };
+
+// A warp's 32 x 32 of the result, lane l with row r0 + l: turned through shared memory (float4
+// columns, exclusive-or swizzled by the row) so that eight lanes write a row's 32 columns.
+__device__ __forceinline__ void store_chunk(const MxParams& p, float4* buf, const uint32_t (&v)[32], int r0, int col0) {
+    const int lane = threadIdx.x & 31;
+    if (col0 >= p.rows_q || r0 >= p.rows_p) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        buf[lane * 8 + (j ^ (lane & 7))] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                                       __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+    __syncwarp();
+    const int c4 = lane & 7, col = col0 + 4 * c4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3), row = r0 + r;
+        const float4 o = buf[r * 8 + (c4 ^ (r & 7))];
+        if (row >= p.rows_p || col >= p.rows_q) continue;
+        const int64_t at = (int64_t)row * p.ldc + col;
+        if (p.c_vec) {  // rows of whole, aligned groups of four
+            if (p.c_f32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.C) + at) = o;
+            } else {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.C) + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            }
+        } else {
+            store_c(p, at, o.x);
+            if (col + 1 < p.rows_q) store_c(p, at + 1, o.y);
+            if (col + 2 < p.rows_q) store_c(p, at + 2, o.z);
+            if (col + 3 < p.rows_q) store_c(p, at + 3, o.w);
+        }
+    }
+    __syncwarp();
+}
+
 template <int MODE, int BQ>
 __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(const __grid_constant__ MxParams p) {
     using C = Cfg<MODE, BQ>;
-    constexpr int S = C::STAGES;
+    constexpr int S = C::STAGES, PER = C::PER;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -138,12 +242,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
     const uint32_t done = bars + 8u * (2 * S + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (2 * S + 5));
     __shared__ volatile int stop;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         stop = 0;
         for (int s = 0; s < S; ++s) {
-            bar_init(full(s), 1 + 4);  // the TMA thread and the four scale warps
+            bar_init(full(s), 1 + C::TEAM);  // the TMA thread and a team of scale warps
             bar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -152,76 +256,103 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         }
         bar_init(done, 1);
         bar_init_fence();
+        tma_desc_prefetch(&p.map_p);
+        if (MODE != ACT_IN) tma_desc_prefetch(&p.map_q);
     }
     if (warp == 1) tmem_get(smem_addr(tmem_slot), 512);
     fence_before_sync();
-    __syncthreads();
+    __syncwarp();
+    if (MODE != MX_MX && p.splits > 1) cluster_barrier();
+    else __syncthreads();
     fence_after_sync();
-    grid_wait();
+    // ACT: the kernel before this one, which splits the rows, began after everything earlier was
+    // complete, so only the split rows have to be waited for; the weights start at once
+    if (MODE != ACT) grid_wait();
     const uint32_t tmem = *tmem_slot;
-    Work<MODE> w(p);
+    Work<PER> w(p);
 
     if (warp == 0) {
         // ------------------------------------------------------------ operand tiles
-        if (lane == 0) {
-            tma_desc_prefetch(&p.map_p);
-            tma_desc_prefetch(&p.map_q);
-            int it = 0;
-            bool ok = true;
-            while (ok && w.next()) {
-                int row_p, row_q;
-                tile_at<MODE>(p, w.tile, BQ, row_p, row_q);
-                for (int k = w.k0; k < w.k1; ++k, ++it) {
-                    const int s = it % S;
-                    if (!bar_wait(empty(s), (uint32_t)(it / S + 1) & 1u, p.err, 1)) {
-                        ok = false;
-                        stop = 1;
-                        break;
+        const bool one = elect_one();
+        int s = 0, it = 0;
+        uint32_t phase = 1;  // a new barrier's preceding phase counts as complete
+        bool ok = true;
+        // an unpacking copy counts the packed bytes (it leaves every second 8 bytes alone)
+        constexpr uint32_t BYTES = MODE == MX_MX ? P_BYTES + C::Q_BYTES : MODE == ACT ? P_BYTES / 2 + C::Q_BYTES : P_BYTES / 2;
+        auto load_q = [&](int st, int k, int row_q) {
+            const uint32_t at = base + st * C::STAGE + P_BYTES;
+            if (MODE != ACT_IN) tma_2d(at, &p.map_q, full(st), k * 128, row_q);
+            if (MODE == ACT) tma_2d(at + C::Q_BYTES / 2, &p.map_q, full(st), k * 128, row_q + p.q_term_rows);
+        };
+        while (ok && w.next()) {
+            int row_p, row_q, k = w.k0;
+            tile_at<MODE, BQ>(p, w.tile, row_p, row_q);
+            if (MODE == ACT && it == 0) {
+                const int ahead = min(S, w.k1 - w.k0);
+                if (one)
+                    for (int i = 0; i < ahead; ++i) {
+                        bar_expect(full(i), BYTES);
+                        tma_2d(base + i * C::STAGE, &p.map_p, full(i), (k + i) * 128, row_p);
                     }
-                    const uint32_t at = base + s * C::STAGE;
-                    // an unpacking copy counts the packed bytes (it leaves every second 8 bytes alone)
-                    bar_expect(full(s), (MODE == MX_MX ? P_BYTES : P_BYTES / 2) + C::Q_BYTES);
-                    tma_2d(at, &p.map_p, full(s), k * 128, row_p);
-                    if (MODE == MX_MX) {
-                        tma_2d(at + P_BYTES, &p.map_q, full(s), k * 128, row_q);
-                    } else {
-                        tma_2d(at + P_BYTES, &p.map_q, full(s), k * 128, row_q);
-                        tma_2d(at + P_BYTES + C::Q_BYTES / 2, &p.map_q, full(s), k * 128, row_q + p.q_term_rows);
-                    }
+                grid_wait();
+                if (one)
+                    for (int i = 0; i < ahead; ++i) load_q(i, k + i, row_q);
+                __syncwarp();
+                it = ahead;
+                k += ahead;
+                s = ahead % S;
+                phase ^= ahead == S ? 1u : 0u;
+            }
+            for (; k < w.k1; ++k, ++it) {
+                if (!bar_wait_warp(empty(s), phase, p.err, 1)) {
+                    ok = false;
+                    stop = 1;
+                    break;
+                }
+                if (one) {
+                    bar_expect(full(s), BYTES);
+                    tma_2d(base + s * C::STAGE, &p.map_p, full(s), k * 128, row_p);
+                    load_q(s, k, row_q);
+                }
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
-            grid_release();
-            // an aborted CTA waits for its own copies before it exits
-            if (stop)
-                for (int s = 0; s < S && s < it; ++s) {
-                    const int last = it - 1 - (it - 1 - s) % S;
-                    bar_wait(full(s), (uint32_t)(last / S) & 1u, p.err, 5);
-                }
         }
+        grid_release();
+        // an aborted CTA waits for its own copies before it exits
+        if (stop)
+            for (int i = 0; i < S && i < it; ++i) {
+                const int last = it - 1 - (it - 1 - i) % S;
+                bar_wait(full(i), (uint32_t)(last / S) & 1u, p.err, 5);
+            }
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            constexpr uint32_t IDESC = MODE == MX_MX ? mx_idesc(1, 1, TILE_P, BQ) : mx_idesc(5, 0, TILE_P, BQ);
-            int it = 0, n = 0;
-            bool ok = true;
-            while (ok && w.next()) {
-                const int b = n % C::ACCS;
-                if (!bar_wait(acc_empty(b), (uint32_t)(n / C::ACCS + 1) & 1u, p.err, 2) || stop) {
+        constexpr uint32_t IDESC = MODE == MX_MX ? mx_idesc(1, 1, TILE_P, BQ) : mx_idesc(5, 0, TILE_P, BQ);
+        const bool one = elect_one();
+        int s = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && w.next()) {
+            const int b = n % C::ACCS;
+            if (!bar_wait_warp(acc_empty(b), (uint32_t)(n / C::ACCS + 1) & 1u, p.err, 2) || stop) {
+                stop = 1;
+                break;
+            }
+            fence_after_sync();
+            const uint32_t d = tmem + (uint32_t)(b * BQ);
+            for (int k = w.k0; k < w.k1; ++k) {
+                if (!bar_wait_warp(full(s), phase, p.err, 3)) {
+                    ok = false;
                     stop = 1;
                     break;
                 }
                 fence_after_sync();
-                const uint32_t d = tmem + (uint32_t)(b * BQ);
-                for (int k = w.k0; k < w.k1; ++k, ++it) {
-                    const int s = it % S;
-                    if (!bar_wait(full(s), (uint32_t)(it / S) & 1u, p.err, 3)) {
-                        ok = false;
-                        stop = 1;
-                        break;
-                    }
-                    fence_after_sync();
-                    const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
-                    const uint32_t tp = tmem + (uint32_t)(C::ACCS * BQ + s * C::SCALE_COLS), tq = tp + 4 * C::QUADS;
+                const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
+                const uint32_t tp = tmem + (uint32_t)(C::ACCS * BQ + s * C::SCALE_COLS), tq = tp + 4 * C::QUADS;
+                if (one) {
 #pragma unroll
                     for (int q = 0; q < C::QUADS; ++q) {
                         scale_copy(tp + 4 * q, scale_desc(sc + 512 * q));
@@ -241,76 +372,138 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                     }
                     mma_commit(empty(s));
                 }
-                if (ok) mma_commit(acc_full(b));
-                ++n;
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
-            mma_commit(done);
-            bar_wait(done, 0, p.err, 6);
+            if (ok && one) mma_commit(acc_full(b));
+            __syncwarp();
+            ++n;
         }
-    } else if (warp < 6) {
-        // ------------------------------------------------------------ scales
-        // lane l of warp w takes row 32 (l % 4) + 8 w + l / 4 of each 128: its word's place in the
-        // 512 bytes is then 128 w + 4 l, free of bank conflicts
-        const int r = 32 * (lane & 3) + 8 * (warp - 2) + (lane >> 2);
-        const uint32_t off = (uint32_t)((warp - 2) * 128 + lane * 4);
-        int it = 0;
-        bool ok = true;
-        while (ok && w.next()) {
-            int row_p, row_q;
-            tile_at<MODE>(p, w.tile, BQ, row_p, row_q);
-            const uint8_t* src[1 + C::PARTS];
-            src[0] = row_p + r < p.rows_p ? p.scale_p + (int64_t)(row_p + r) * p.scale_pitch : nullptr;
+        if (one) mma_commit(done);
+        __syncwarp();
+        bar_wait(done, 0, p.err, 6);
+    } else if (warp < C::FIRST_EPI) {
+        // ------------------------------------------------------------ scales (and ACT_IN: the rows)
+        // Teams take turns, so that the latencies of several stages' waits, stores and fences
+        // overlap; a team requests its next turn's scales (ACT_IN: of two turns) before it starts one. A
+        // team's warps share the rows: of each 128, lane l has rows l + 32 j, whose words lie side by
+        // side at 16 l in the order that the tensor core reads.
+        constexpr int RUN = C::RUN, TEAMS = C::TEAMS, RPW = 4 / C::TEAM;   // rows of a warp, of each 128
+        constexpr int NR = RPW * (MODE == ACT_IN ? 1 : 1 + C::PARTS);
+        constexpr int AHEAD = MODE == ACT_IN ? 2 : 1;
+        constexpr int U = MODE == ACT_IN ? C::TN / 2 : 1;                  // ACT_IN: units of 8 values a lane
+        typedef typename Words<4 * C::QUADS * RUN>::type V;
+        const int team = (warp - 2) / C::TEAM, first = RPW * ((warp - 2) % C::TEAM);
+        w.next();
+        const int stages = w.k1 - w.k0, turns = (stages + RUN - 1) / RUN;
+        int tile = w.tile, u = 0, it0 = 0;                             // the turn at hand
+        int f_tile = w.tile, f_u = 0;                                  // the turn to request next
+        auto step = [&](int& t, int& v, int& it, int by) {
+            for (v += by; v >= turns; v -= turns, t += w.step, it += stages) {}
+        };
+        V v[AHEAD + 1][NR];
+        uint4 x[AHEAD + 1][U];
+        const int xg = lane & 15;
+        auto fetch = [&](V (&to)[NR], uint4 (&xto)[U], int t, int turn, int j0, int j1) {
+            const bool on = t < p.tiles;
+            const int k = w.k0 + turn * RUN;
+            int row_p = 0, row_q = 0;
+            if (on) tile_at<MODE, BQ>(p, t, row_p, row_q);
+            const int64_t at = (int64_t)k * (4 * C::QUADS);
 #pragma unroll
-            for (int j = 0; j < C::PARTS; ++j) {
-                const int rq = r + 128 * j;
-                int64_t at = -1;
-                if (rq < BQ) {
-                    if (MODE == MX_MX) at = row_q + rq < p.rows_q ? row_q + rq : -1;
-                    else at = rq < BQ / 2 ? row_q + rq : row_q + rq - BQ / 2 + p.q_term_rows;
+            for (int j = 0; j < NR; ++j) {
+                if (j < j0 || j >= j1) continue;
+                if (j < RPW) {
+                    const int row = row_p + lane + 32 * (first + j);
+                    load_words(p.scale_p + (int64_t)row * p.scale_pitch + at, on && row < p.rows_p, to[j]);
+                } else {
+                    const int rq = lane + 128 * (j / RPW - 1) + 32 * (first + j % RPW);
+                    const int64_t row = MODE == MX_MX ? row_q + rq
+                                        : rq < BQ / 2 ? row_q + rq : (int64_t)row_q + rq - BQ / 2 + p.q_term_rows;
+                    load_words(p.scale_q + row * p.scale_pitch + at, on && rq < BQ && (MODE != MX_MX || row < p.rows_q), to[j]);
                 }
-                src[1 + j] = at >= 0 ? p.scale_q + at * p.scale_pitch : nullptr;
             }
-            uint4 cur[1 + C::PARTS], nxt[1 + C::PARTS];
-            auto load = [&](uint4(&v)[1 + C::PARTS], int group) {
+            if (MODE == ACT_IN && j0 == 0) {
 #pragma unroll
-                for (int j = 0; j < 1 + C::PARTS; ++j)
-                    v[j] = src[j] && group * 16 < p.scale_pitch
-                               ? __ldg(reinterpret_cast<const uint4*>(src[j] + group * 16))
-                               : make_uint4(0, 0, 0, 0);
-            };
-            constexpr int PER = 4 / C::QUADS;  // stages of one 16-byte load
-            load(nxt, w.k0 / PER);
-            for (int k = w.k0; k < w.k1; ++k, ++it) {
-                if (k == w.k0 || k % PER == 0) {
-#pragma unroll
-                    for (int j = 0; j < 1 + C::PARTS; ++j) cur[j] = nxt[j];
-                    load(nxt, k / PER + 1);
+                for (int i = 0; i < U; ++i) {
+                    if (2 * i >= p.rows_q) continue;  // columns of tokens that do not exist hold anything
+                    const int tok = (lane >> 4) + 2 * i;
+                    xto[i] = on && tok < p.rows_q ? row8(p.a + (int64_t)tok * p.lda, k * 128 + 8 * xg, p.K, p.vec)
+                                                  : make_uint4(0, 0, 0, 0);
                 }
-                const int s = it % S;
+            }
+        };
+        int none = 0;
+        step(tile, u, it0, team);
+        step(f_tile, f_u, none, team);
+        if (MODE == ACT) {
+            fetch(v[0], x[0], f_tile, f_u, 0, RPW);
+            grid_wait();
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            fetch(v[i], x[i], f_tile, f_u, MODE == ACT ? RPW : 0, NR);
+            step(f_tile, f_u, none, TEAMS);
+        }
+        bool ok = true;
+        while (ok && tile < p.tiles) {
+            fetch(v[AHEAD], x[AHEAD], f_tile, f_u, 0, NR);
+            step(f_tile, f_u, none, TEAMS);
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                if (!ok || u * RUN + i >= stages) continue;
+                const int it = it0 + u * RUN + i, s = it % S;
                 if (!__all_sync(0xffffffffu, bar_wait(empty(s), (uint32_t)(it / S + 1) & 1u, p.err, 7))) {
                     ok = false;
                     stop = 1;
-                    break;
+                    continue;
                 }
-                const uint32_t sc = base + s * C::STAGE + P_BYTES + C::Q_BYTES + off;
+                const uint32_t sq = base + s * C::STAGE + P_BYTES, sc = sq + C::Q_BYTES, at = sc + lane * 16 + 4 * first;
 #pragma unroll
-                for (int j = 0; j < 1 + C::PARTS; ++j) {
-                    const uint4 v = cur[j];
-                    if (MODE == MX_MX) {
-                        const uint32_t a = k & 1 ? v.z : v.x, b = k & 1 ? v.w : v.y;
-                        // the left operand's two words, then (word, part) of the right one
-                        const uint32_t w0 = j == 0 ? 0 : 2 + (j - 1), w1 = j == 0 ? 1 : 2 + C::PARTS + (j - 1);
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 512 * w0), "r"(a) : "memory");
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 512 * w1), "r"(b) : "memory");
-                    } else {
-                        const uint32_t a = k & 2 ? (k & 1 ? v.w : v.z) : (k & 1 ? v.y : v.x);
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 512 * j), "r"(a) : "memory");
+                for (int q = 0; q < C::QUADS; ++q)
+#pragma unroll
+                    for (int j = 0; j < NR / RPW; ++j) {  // the left operand's chunk, then the right one's parts
+                        const uint32_t to = at + 512 * (j == 0 ? q : C::QUADS + q * C::PARTS + j - 1);
+                        const int wi = i * C::QUADS + q;
+                        if (RPW == 4)
+                            st_shared4(to, word_of(v[0][RPW * j], wi), word_of(v[0][RPW * j + 1], wi),
+                                       word_of(v[0][RPW * j + 2 % RPW], wi), word_of(v[0][RPW * j + 3 % RPW], wi));
+                        else
+                            st_shared2(to, word_of(v[0][RPW * j], wi), word_of(v[0][RPW * j + 1], wi));
+                    }
+                if (MODE == ACT_IN) {
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        if (2 * j >= p.rows_q) continue;
+                        uint2 o1, o2;
+                        uint32_t b1, b2;
+                        split8(x[0][j], o1, o2, b1, b2);
+                        const int r1 = (lane >> 4) + 2 * j, r2 = r1 + C::TN;  // rows of the stage, swizzled 16 bytes
+                        const uint32_t col = (uint32_t)((((xg >> 1) ^ (r1 & 7)) << 4) + (xg & 1) * 8);
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sq + r1 * 128 + col), "r"(o1.x), "r"(o1.y) : "memory");
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sq + r2 * 128 + col), "r"(o2.x), "r"(o2.y) : "memory");
+                        if ((xg & 3) == 0) {
+                            const uint32_t to = sc + 512 + (uint32_t)(xg >> 2);
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + r1 * 16), "r"(b1) : "memory");
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + r2 * 16), "r"(b2) : "memory");
+                        }
                     }
                 }
                 fence_smem_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive(full(s));
             }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+#pragma unroll
+                for (int j = 0; j < NR; ++j) v[i][j] = v[i + 1][j];
+#pragma unroll
+                for (int j = 0; j < U; ++j) x[i][j] = x[i + 1][j];
+            }
+            step(tile, u, it0, TEAMS);
         }
     } else {
         // ------------------------------------------------------------ results
@@ -318,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         int n = 0;
         while (w.next()) {
             int row_p, row_q;
-            tile_at<MODE>(p, w.tile, BQ, row_p, row_q);
+            tile_at<MODE, BQ>(p, w.tile, row_p, row_q);
             const int b = n % C::ACCS;
             if (!__all_sync(0xffffffffu, bar_wait(acc_full(b), (uint32_t)(n / C::ACCS) & 1u, p.err, 4) && !stop)) {
                 stop = 1;
@@ -327,72 +520,68 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             fence_after_sync();
             const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BQ);
             if (MODE == MX_MX) {
-                float* buf = reinterpret_cast<float*>(gbase + S * C::STAGE) + (warp - 6) * 32 * 33;
+                float4* buf = reinterpret_cast<float4*>(gbase + S * C::STAGE) + (warp - C::FIRST_EPI) * 256;
                 const int r0 = row_p + q * 32;
-                const int half = (warp - 6) >> 2;
+                const int half = (warp - C::FIRST_EPI) >> 2;
 #pragma unroll 1
                 for (int c = half; c < BQ / 32; c += 2) {
                     uint32_t v[32];
                     tmem_load32(t + 32 * c, v);
                     tmem_load_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) buf[lane * 33 + j] = __uint_as_float(v[j]);
-                    __syncwarp();
-                    const int col = row_q + 32 * c + lane;
-                    if (col < p.rows_q)
-                        for (int i = 0; i < 32 && r0 + i < p.rows_p; ++i)
-                            store_c(p, (int64_t)(r0 + i) * p.ldc + col, buf[i * 33 + lane]);
-                    __syncwarp();
+                    store_chunk(p, buf, v, r0, row_q + 32 * c);
                 }
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) bar_arrive(acc_empty(b));
             } else {
-                constexpr int TN = BQ / 2;
-                const int row = q * 32 + lane;
-                const int col = row_p + row;                   // the weight row is the output column
-                const int tokens = min(TN, p.rows_q - row_q);
-                const bool whole = w.k0 == 0 && w.k1 == p.k_stages;
-                float* mine = p.partial + ((int64_t)(2 * blockIdx.x + (w.k0 > 0 ? 0 : 1)) * TN) * 128 + row;
+                const int row = q * 32 + lane, col = row_p + row;  // the weight row is the output column
+                const int tokens = min(C::TN, p.rows_q - row_q);
+                const uint32_t slice = blockIdx.x % p.splits;
+                // a cluster's later CTAs leave their sums in the first one's memory
+                const uint32_t red = slice ? cluster_addr(base + S * C::STAGE + (slice - 1) * C::TN * TILE_P * 4, 0) : 0u;
+                if (p.splits == 1 || slice) {
 #pragma unroll 1
-                for (int j0 = 0; j0 < tokens; j0 += 8) {
-                    uint32_t x[8], y[8];
-                    tmem_load8(t + j0, x);
-                    tmem_load8(t + TN + j0, y);
-                    tmem_load_wait();
+                    for (int j0 = 0; j0 < tokens; j0 += 8) {
+                        uint32_t x[8], y[8];
+                        tmem_load8(t + j0, x);
+                        tmem_load8(t + C::TN + j0, y);
+                        tmem_load_wait();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float v = __uint_as_float(x[j]) + __uint_as_float(y[j]);
-                        if (j0 + j >= tokens) continue;
-                        if (!whole) mine[(j0 + j) * 128] = v;
-                        else if (col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
-                    }
-                }
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) bar_arrive(acc_empty(b));
-                if (!whole) {
-                    // CTA b holds the line [b total / grid, (b + 1) total / grid)
-                    const int64_t total = (int64_t)p.tiles * p.k_stages, first = (int64_t)w.tile * p.k_stages;
-                    const int b0 = (int)(((first + 1) * gridDim.x - 1) / total);
-                    const int b1 = (int)(((first + p.k_stages) * gridDim.x - 1) / total);
-                    __threadfence();
-                    __syncwarp();
-                    uint32_t seen = 0;
-                    if (lane == 0) seen = atomicAdd(p.tickets + 4 * w.tile + q, 1u);
-                    seen = __shfl_sync(0xffffffffu, seen, 0);
-                    if (seen == (uint32_t)(b1 - b0)) {  // the last of the tile's CTAs: all sums, in order
-                        __threadfence();
-                        for (int j = 0; j < tokens; ++j) {
-                            float v = 0.f;
-                            for (int i = b0; i <= b1; ++i)
-                                v += __ldcg(p.partial + ((int64_t)(2 * i + (i == b0 ? 1 : 0)) * TN + j) * 128 + row);
-                            if (col < p.rows_p) store_c(p, (int64_t)(row_q + j) * p.ldc + col, v);
+                        for (int j = 0; j < 8; ++j) {
+                            const float v = __uint_as_float(x[j]) + __uint_as_float(y[j]);
+                            if (slice) st_cluster(red + ((j0 + j) * TILE_P + row) * 4, v);
+                            else if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
                         }
                     }
                 }
             }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) bar_arrive(acc_empty(b));
             ++n;
+        }
+    }
+    if (MODE != MX_MX && p.splits > 1) {
+        __syncwarp();
+        cluster_barrier();  // every CTA's sums are in the first one's memory; the sum runs in CTA order
+        if (blockIdx.x % p.splits == 0 && warp >= C::FIRST_EPI) {
+            fence_after_sync();
+            int row_p, row_q;
+            tile_at<MODE, BQ>(p, blockIdx.x / p.splits, row_p, row_q);
+            const int q = warp & 3, row = q * 32 + lane, col = row_p + row;
+            const int tokens = min(C::TN, p.rows_q - row_q);
+            const float* red = reinterpret_cast<const float*>(gbase + S * C::STAGE) + row;
+            const uint32_t t = tmem + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+            for (int j0 = 0; j0 < tokens; j0 += 8) {
+                uint32_t x[8], y[8];
+                tmem_load8(t + j0, x);
+                tmem_load8(t + C::TN + j0, y);
+                tmem_load_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float v = __uint_as_float(x[j]) + __uint_as_float(y[j]);
+                    for (int i = 0; i < p.splits - 1; ++i) v += red[(i * C::TN + j0 + j) * TILE_P];
+                    if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
+                }
+            }
         }
     }
     fence_before_sync();
@@ -403,62 +592,21 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
     }
 }
 
-// The two E4M3 terms of bf16 rows (see the top) and the tickets' zeros. Terms: [2][pad rows]
-// [pitch] bytes, scales likewise; rows past M are zero. A thread takes 8 values, four lanes a block.
+// The two terms of more rows than a stage's warps split on the way: [2][pad rows][pitch] bytes
+// and their scales likewise; rows past M are zero. A thread takes 8 values, four lanes a block.
 __global__ void __launch_bounds__(256)
 split_rows_kernel(const __nv_bfloat16* __restrict__ a, int64_t lda, int M, int K, int vec, int pad_rows, uint32_t per_row,
-                  uint8_t* __restrict__ terms, uint8_t* __restrict__ scales, int scale_pitch, uint32_t* __restrict__ tickets,
-                  int n_tickets) {
-    grid_release();
+                  uint8_t* __restrict__ terms, uint8_t* __restrict__ scales, int scale_pitch) {
+    grid_wait();
+    grid_release();  // everything earlier is complete: the product may start on the weights
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t total = (int64_t)pad_rows * per_row;
-    if (i < n_tickets) tickets[i] = 0;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const int row = (int)(i / per_row);
     const uint32_t g = (uint32_t)(i % per_row);
-    if (i < total && row < M) {
-        const int k = (int)g * 8;
-        const __nv_bfloat16* s = a + row * lda + k;
-        if (vec && k + 8 <= K) {
-            const uint4 q = *reinterpret_cast<const uint4*>(s);
-            const uint32_t x[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(x[j] << 16);
-                v[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (k + j < K) v[j] = __bfloat162float(s[j]);
-        }
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    uint2 o1, o2;
+    uint32_t b1, b2;
+    split8(i < total && row < M ? row8(a + row * lda, (int)g * 8, K, vec) : make_uint4(0, 0, 0, 0), o1, o2, b1, b2);
     if (i >= total) return;
-    // s1 = e - 127 - 7 and s2 = s1 - 5 as bytes, not below 0; a block with a NaN or an infinity reads as NaN
-    const uint32_t e = m >> 23;
-    const uint32_t b1 = e == 255 ? 255 : e < 7 ? 0 : e - 7, b2 = e == 255 ? 255 : e < 12 ? 0 : e - 12;
-    const float f1 = __uint_as_float((254 - min(b1, 253u)) << 23), u1 = e8m0_to_float(min(b1, 254u));
-    const float f2 = __uint_as_float((254 - min(b2, 253u)) << 23);
-    uint16_t t1[4], t2[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float x = v[2 * j], y = v[2 * j + 1];
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t1[j]) : "f"(y * f1), "f"(x * f1));
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(t1[j]));
-        const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        const float rx = x - d.x * u1, ry = y - d.y * u1;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t2[j]) : "f"(ry * f2), "f"(rx * f2));
-    }
-    const bool bad = e == 255;
-    uint2 o1 = make_uint2(t1[0] | (uint32_t)t1[1] << 16, t1[2] | (uint32_t)t1[3] << 16);
-    uint2 o2 = make_uint2(t2[0] | (uint32_t)t2[1] << 16, t2[2] | (uint32_t)t2[3] << 16);
-    if (bad) o1 = o2 = make_uint2(0, 0);
     reinterpret_cast<uint2*>(terms)[i] = o1;
     reinterpret_cast<uint2*>(terms)[i + total] = o2;
     if ((g & 3) == 0) {
@@ -472,8 +620,8 @@ split_rows_kernel(const __nv_bfloat16* __restrict__ a, int64_t lda, int M, int K
 }
 
 // ------------------------------------------------------------------ host side
-// View of `rows` rows of `pitch` bytes in boxes of 128 x box_rows, 128-byte swizzle. codes:
-// packed 4-bit values unpacked to a byte each (128 values a row of the box).
+// View of `rows` rows of `pitch` bytes in boxes of 128 x box_rows, 128-byte swizzle. unpack:
+// packed 4-bit values to a byte each (128 values a row of the box).
 bool map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows, bool unpack) {
     const MxEncodeFn fn = mx_encode_fn();
     if (!fn) return false;
@@ -487,21 +635,25 @@ bool map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int 
 }
 
 template <int MODE, int BQ>
-cudaError_t launch(const MxParams& p, int grid, bool pdl, cudaStream_t s) {
+cudaError_t launch(const MxParams& p, cudaStream_t s) {
     auto kern = gemm_mx_kernel<MODE, BQ>;
     using C = Cfg<MODE, BQ>;
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(p.splits > 1 ? p.tiles * p.splits : std::min(p.tiles, gemm_num_sms()));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = p.splits;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -509,6 +661,28 @@ int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 // Tokens of a tile: the fewest columns that hold M, at most 128.
 int act_tile(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// CTAs that share a tile along K (a cluster): few tiles leave SMs idle, and each further CTA costs
+// a pass of the sums through shared memory. In units of a scale group (512 values of K, about 0.7 us of an
+// SM's share of the memory): a CTA's groups, one to start, and three to join the sums.
+int act_splits(int tiles, int groups, int max_split) {
+    int best = 1;
+    double least = groups + 1.0;
+    for (int n = 2; n <= max_split && n <= groups && tiles * n <= gemm_num_sms(); ++n) {
+        const double cost = (groups + n - 1) / n + 1.0 + 3.0;
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
+template <int MODE, int BQ>
+cudaError_t launch_act(MxParams& p, cudaStream_t s) {
+    p.splits = act_splits(p.tiles, (p.k_stages + 3) / 4, Cfg<MODE, BQ>::MAX_SPLIT);
+    return launch<MODE, BQ>(p, s);
+}
 
 }  // namespace
 
@@ -540,28 +714,22 @@ cudaError_t launch_gemm_mx(const void* a_codes, const void* a_scales, const void
     p.rows_p = M;
     p.rows_q = N;
     p.k_stages = (K + 255) / 256;
-    p.tiles_p = (M + TILE_P - 1) / TILE_P;
-    p.tiles_q = (N + BQ - 1) / BQ;
-    if ((int64_t)p.tiles_p * p.tiles_q > 0x7fffffffll) return cudaErrorInvalidValue;
+    p.tiles_p = (int)(up(M, TILE_P) / TILE_P);
+    p.tiles_q = (int)(up(N, BQ) / BQ);
+    if ((int64_t)p.tiles_p * p.tiles_q > 0x3fffffffll) return cudaErrorInvalidValue;
     p.tiles = p.tiles_p * p.tiles_q;
+    p.splits = 1;
     p.C = C;
     p.ldc = N;
     p.c_f32 = c_f32;
+    p.c_vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(C) & (c_f32 ? 15 : 7)) == 0;
     p.err = err;
-    return launch<MX_MX, BQ>(p, std::min(p.tiles, gemm_num_sms()), false, s);
+    return launch<MX_MX, BQ>(p, s);
 }
 
-static int act_grid(int M, int N, int K) {
+int64_t act_mx_ws_bytes(int M, int K) {
     const int tn = act_tile(M);
-    const int64_t stages = up(N, TILE_P) / TILE_P * (up(M, tn) / tn) * (up(K, 128) / 128);
-    return (int)std::min<int64_t>(stages, gemm_num_sms());
-}
-
-int64_t act_mx_ws_bytes(int M, int N, int K) {
-    const int tn = act_tile(M);
-    const int64_t rows = up(M, tn), tiles = up(N, TILE_P) / TILE_P * (rows / tn);
-    return 2 * rows * (up(K, 128) + mx_scale_pitch(K)) + up(16 * tiles, 256) +
-           2ll * act_grid(M, N, K) * tn * 128 * (int64_t)sizeof(float) + 1024;
+    return tn <= 16 ? 0 : 2 * up(M, tn) * (up(K, 128) + mx_scale_pitch(K));
 }
 
 cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, const void* b_scales, void* C, bool c_f32,
@@ -574,45 +742,47 @@ cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, 
     p.scale_pitch = (int)mx_scale_pitch(K);
     p.tiles_p = (int)(up(N, TILE_P) / TILE_P);
     p.tiles_q = (int)(rows / tn);
-    if ((int64_t)p.tiles_p * p.tiles_q > 0x7fffffffll / 4 || 2 * rows > 0x7fffffffll) return cudaErrorInvalidValue;
+    if ((int64_t)p.tiles_p * p.tiles_q > 0x3fffffffll || 2 * rows > 0x7fffffffll) return cudaErrorInvalidValue;
     p.tiles = p.tiles_p * p.tiles_q;
-    uint8_t* w = static_cast<uint8_t*>(ws);
-    uint8_t* terms = w;
-    w += 2 * rows * kp;
-    uint8_t* scales = w;
-    w += 2 * rows * p.scale_pitch;
-    w = reinterpret_cast<uint8_t*>(up(reinterpret_cast<intptr_t>(w), 256));
-    p.tickets = reinterpret_cast<uint32_t*>(w);
-    w += up(16ll * p.tiles, 256);
-    p.partial = reinterpret_cast<float*>(w);
-    if (!map_rows(&p.map_p, b_codes, N, mx_code_pitch(K), TILE_P, true) || !map_rows(&p.map_q, terms, 2 * rows, kp, tn, false))
-        return cudaErrorInvalidValue;
+    if (!map_rows(&p.map_p, b_codes, N, mx_code_pitch(K), TILE_P, true)) return cudaErrorInvalidValue;
     p.scale_p = static_cast<const uint8_t*>(b_scales);
-    p.scale_q = scales;
     p.rows_p = N;
     p.rows_q = M;
-    p.q_term_rows = (int)rows;
     p.k_stages = (int)(kp / 128);
+    p.a = static_cast<const __nv_bfloat16*>(a);
+    p.lda = lda;
+    p.K = K;
+    p.vec = (reinterpret_cast<uintptr_t>(a) & 15) == 0 && lda % 8 == 0;
     p.C = C;
     p.ldc = N;
     p.c_f32 = c_f32;
     p.err = err;
-    const int vec = (reinterpret_cast<uintptr_t>(a) & 15) == 0 && lda % 8 == 0;
+    if (tn == 8) return launch_act<ACT_IN, 16>(p, s);
+    if (tn == 16) return launch_act<ACT_IN, 32>(p, s);
+    uint8_t* terms = static_cast<uint8_t*>(ws);
+    uint8_t* scales = terms + 2 * rows * kp;
+    if (!map_rows(&p.map_q, terms, 2 * rows, kp, tn, false)) return cudaErrorInvalidValue;
+    p.scale_q = scales;
+    p.q_term_rows = (int)rows;
     const uint32_t per_row = (uint32_t)(kp / 8);
-    const int64_t work = std::max<int64_t>(rows * per_row, 4ll * p.tiles);
-    if ((work + 255) / 256 > 0x7fffffffll) return cudaErrorInvalidValue;
-    split_rows_kernel<<<(unsigned)((work + 255) / 256), 256, 0, s>>>(static_cast<const __nv_bfloat16*>(a), lda, M, K, vec,
-                                                                     (int)rows, per_row, terms, scales, p.scale_pitch,
-                                                                     p.tickets, 4 * p.tiles);
-    cudaError_t e = cudaGetLastError();
+    const int64_t blocks = (rows * per_row + 255) / 256;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, split_rows_kernel, p.a, lda, M, K, p.vec, (int)rows, per_row, terms, scales,
+                                             p.scale_pitch);
     if (e != cudaSuccess) return e;
-    const int grid = act_grid(M, N, K);
     switch (tn) {
-        case 8: return launch<ACT_MX, 16>(p, grid, true, s);
-        case 16: return launch<ACT_MX, 32>(p, grid, true, s);
-        case 32: return launch<ACT_MX, 64>(p, grid, true, s);
-        case 64: return launch<ACT_MX, 128>(p, grid, true, s);
-        default: return launch<ACT_MX, 256>(p, grid, true, s);
+        case 32: return launch_act<ACT, 64>(p, s);
+        case 64: return launch_act<ACT, 128>(p, s);
+        default: return launch_act<ACT, 256>(p, s);
     }
 }
 

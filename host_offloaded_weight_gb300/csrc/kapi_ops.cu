@@ -82,7 +82,8 @@ ls_status lsk_gemm_bf16_mxfp4(const void* A, int64_t lda, const void* b_codes, c
         !aligned(C, c_f32 ? 4 : 2))
         return LS_ERR_INVALID_ARG;
     Scratch ws((cudaStream_t)stream);
-    if (!ws.take(act_mx_ws_bytes(M, N, K))) return LS_ERR_OOM;
+    const int64_t need = act_mx_ws_bytes(M, K);
+    if (need > 0 && !ws.take(need)) return LS_ERR_OOM;
     return status_of(launch_gemm_act_mx(A, lda, b_codes, b_scales, C, c_f32 != 0, M, N, K, ws.p, entry_error_word(),
                                         (cudaStream_t)stream));
 }
