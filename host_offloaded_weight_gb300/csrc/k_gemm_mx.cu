@@ -125,55 +125,6 @@ __device__ __forceinline__ void store_c(const MxParams& p, int64_t at, float v) 
     else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
 }
 
-// Eight values of a bf16 row from k on, zeros past K.
-__device__ __forceinline__ uint4 row8(const __nv_bfloat16* row, int k, int K, int vec) {
-    if (vec && k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
-    uint32_t w[4] = {0, 0, 0, 0};
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(row);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (k + j < K) w[j >> 1] |= (uint32_t)s[k + j] << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The two E4M3 terms of eight values and the scale bytes of their block (see the top). Four
-// neighbouring lanes hold a block; every lane of the warp takes part.
-__device__ __forceinline__ void split8(uint4 raw, uint2& o1, uint2& o2, uint32_t& b1, uint32_t& b2) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
-    m = max(m & 0xffffu, m >> 16);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // s1 = e - 127 - 7 and s2 = s1 - 5 as bytes, not below 0; a block with a NaN or an infinity reads as NaN
-    const uint32_t e = m >> 7;
-    b1 = e == 255 ? 255 : e < 7 ? 0 : e - 7;
-    b2 = e == 255 ? 255 : e < 12 ? 0 : e - 12;
-    const float f1 = __uint_as_float((254 - min(b1, 253u)) << 23), u1 = e8m0_to_float(min(b1, 254u));
-    const float f2 = __uint_as_float((254 - min(b2, 253u)) << 23);
-    uint16_t t1[4], t2[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float x = __uint_as_float(w[j] << 16), y = __uint_as_float(w[j] & 0xffff0000u);
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t1[j]) : "f"(y * f1), "f"(x * f1));
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(t1[j]));
-        const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        const float rx = x - d.x * u1, ry = y - d.y * u1;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t2[j]) : "f"(ry * f2), "f"(rx * f2));
-    }
-    o1 = make_uint2(t1[0] | (uint32_t)t1[1] << 16, t1[2] | (uint32_t)t1[3] << 16);
-    o2 = make_uint2(t2[0] | (uint32_t)t2[1] << 16, t2[2] | (uint32_t)t2[3] << 16);
-    if (e == 255) o1 = o2 = make_uint2(0, 0);
-}
-
-__device__ __forceinline__ void st_shared2(uint32_t at, uint32_t a, uint32_t b) {
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(a), "r"(b) : "memory");
-}
-__device__ __forceinline__ void st_shared4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
 __device__ __forceinline__ void load_words(const uint8_t* p, bool in, uint4& v) {
@@ -334,7 +285,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         const bool one = elect_one();
         int s = 0, n = 0;
         uint32_t phase = 0;
-        bool ok = true;
+        bool ok = true, ready = false;  // ready: the next stage's barrier, asked before this stage's products
         while (ok && w.next()) {
             const int b = n % C::ACCS;
             if (!bar_wait_warp(acc_empty(b), (uint32_t)(n / C::ACCS + 1) & 1u, p.err, 2) || stop) {
@@ -344,14 +295,19 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             fence_after_sync();
             const uint32_t d = tmem + (uint32_t)(b * BQ);
             for (int k = w.k0; k < w.k1; ++k) {
-                if (!bar_wait_warp(full(s), phase, p.err, 3)) {
+                if (!__all_sync(0xffffffffu, ready) && !bar_wait_warp(full(s), phase, p.err, 3)) {
                     ok = false;
                     stop = 1;
                     break;
                 }
                 fence_after_sync();
-                const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
+                const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES, freed = empty(s);
                 const uint32_t tp = tmem + (uint32_t)(C::ACCS * BQ + s * C::SCALE_COLS), tq = tp + 4 * C::QUADS;
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+                ready = bar_test(full(s), phase);
                 if (one) {
 #pragma unroll
                     for (int q = 0; q < C::QUADS; ++q) {
@@ -370,13 +326,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                         else
                             mma_mxf8(d, dp, dq, idesc_at(IDESC, i), tp, tq, acc);
                     }
-                    mma_commit(empty(s));
+                    mma_commit(freed);
                 }
                 __syncwarp();
-                if (++s == S) {
-                    s = 0;
-                    phase ^= 1u;
-                }
             }
             if (ok && one) mma_commit(acc_full(b));
             __syncwarp();
