@@ -1,7 +1,7 @@
-// A whole mixture-of-experts layer for a few tokens, in two kernels:
+// A whole mixture-of-experts layer for a few tokens, in one launch:
 //
-//   up     h[i] = SiLU(G_e x_t) * (U_e x_t)   for every routed pair i = (t, e)
-//   down   out[t] = r[t] + sum_j w[t,j] D_e h[i],  w = softmax over the token's k largest logits
+//   h[i]   = SiLU(G_e x_t) * (U_e x_t)   for every routed pair i = (t, e)                 ("up")
+//   out[t] = r[t] + sum_j w[t,j] D_e h[i],  w = softmax over the token's k largest logits ("down")
 //
 // Experts in bf16 or MXFP4. The bound is the bytes of the experts that are routed: each is read
 // once (for up to 8 of its tokens), and nothing else of that size is touched.
@@ -11,16 +11,19 @@
 // as E4M3 terms with a power of two for each block of 32 (see k_gemm_mx.cu): two for x, which
 // holds a bf16's 8 bits, and three for h, 12 bits. So the weights go from memory to the tensor core as they
 // are, with no instruction spent on a value, and a product (about 60 clocks for 4 KB of the stage)
-// stays under the memory's time. A tile takes 64 gate rows and the 64 up rows of the same columns of h.
+// stays under the memory's time. A tile of up takes 64 gate rows and the 64 up rows of the same columns of h.
 //
-// Routing is done by every CTA of both kernels for itself (a warp a token): that costs less than a
-// launch, and lets the down kernel request its first weights while the up kernel runs.
+// The grid is resident as a whole (a cooperative launch): every CTA routes for itself, takes tiles of
+// up, meets the others once, and takes a tile of 128 output rows for its share of the experts. Across the
+// meeting the ring of stages goes on: the first weights of down are requested before it. (As two
+// launches the second one's start, routing and first loads cost 8 us of 18 at one token.) The CTAs of a tile add
+// their sums through memory, the last one to finish in the order of the CTAs: the same bits
+// every time, and no atomics on data.
 //
-// Both kernels: warp 0 loads the weights by TMA into a ring of stages, warps 2-9 take turns at
-// the stages and add the block scales and (up) the tokens' rows, warp 1 issues the products,
-// warps 10-13 write the results. Down: a cluster has 128 output rows; its CTAs share the experts,
-// keep the weighted sums [token][row] in shared memory and add one another's in CTA order. The
-// same bits every time, and no atomics on data.
+// Warp 0 loads the weights by TMA into the ring, warps 2-9 take turns at the stages and add the
+// block scales and (up) the tokens' rows, warp 1 issues the products, warps 10-13 take the results.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kernels.h"
@@ -36,42 +39,41 @@ constexpr int MAX_ROWS = MAX_T * MAX_K;
 constexpr int TOK = 8;            // tokens of an expert that one pass over its weights serves
 constexpr int TILE = 128;         // weight rows of a tile
 constexpr int UP_F = TILE / 2;    // columns of h of a tile of the up kernel
-constexpr int P_BYTES = TILE * 128;
-constexpr int H_TERMS = 3;        // E4M3 terms of h (MXFP4 experts)
-
-template <bool MX, bool UP>
-struct Cfg {
-    static constexpr int TERMS = !MX ? 1 : UP ? 2 : H_TERMS;
-    static constexpr int BQ = TERMS <= 2 ? 16 : 32;                    // columns of a product
-    static constexpr int Q_BYTES = BQ * 128;
-    static constexpr int STAGE = P_BYTES + Q_BYTES + 1024;             // and 1 KB of scales
-    static constexpr int STAGES = BQ == 16 ? 9 : 8;
-    static constexpr int TMEM_COLS = BQ == 16 ? 128 : 256;             // two accumulators, and each stage's scales
-    static_assert(2 * BQ + STAGES * 8 <= TMEM_COLS, "tensor memory");
-};
-constexpr int MAX_STAGES = 9;
 constexpr int FEED_WARPS = 8, FIRST_EPI = 2 + FEED_WARPS;
 constexpr int THREADS = 32 * (FIRST_EPI + 4);
-constexpr int MAX_CLUSTER = 8;
-// a wait by parity cannot tell a phase from the one two before it
-static_assert(FEED_WARPS <= Cfg<true, false>::STAGES, "a feed warp's turns are within a round of the ring");
+constexpr int P_BYTES = TILE * 128;
+constexpr int X_TERMS = 2, H_TERMS = 3;  // E4M3 terms of x and of h (MXFP4 experts)
 
-struct Routing;
+template <bool MX>
+struct Cfg {
+    static constexpr int Q_ROWS = MX ? 32 : 16;                        // columns of the widest product
+    static constexpr int Q_BYTES = Q_ROWS * 128;
+    static constexpr int STAGE = P_BYTES + Q_BYTES + 1024;             // and 1 KB of scales
+    static constexpr int STAGES = MX ? 8 : 9;
+    static_assert(2 * Q_ROWS + STAGES * 8 <= 128, "tensor memory: two accumulators, and each stage's scales");
+    // a wait by parity cannot tell a phase from the one two before it
+    static_assert(FEED_WARPS <= STAGES, "a feed warp's turns are within a round of the ring");
+};
+constexpr int MAX_STAGES = 9, TMEM_COLS = 128;
+constexpr int MAX_SHARES = 32;    // CTAs that share an output tile
+
 struct FewParams {
-    CUtensorMap map_p, map_p2;  // up: gate, up; down: down, h
-    const uint8_t* scale_p;     // MXFP4: block scales of gate and up, or of down
-    const uint8_t* scale_p2;
-    int64_t scale_stride;       // bytes between experts
-    int scale_pitch;
+    CUtensorMap gate, up, down, map_h;
+    const uint8_t* gate_scale;  // MXFP4: block scales
+    const uint8_t* up_scale;
+    const uint8_t* down_scale;
+    int64_t up_scale_stride, down_scale_stride;  // bytes between experts
+    int up_scale_pitch, down_scale_pitch;
     const __nv_bfloat16* x;     // [T, H]
     const float* resid;         // [T, H], or NULL: x
     const float* logits;        // [T, E]
     uint8_t* h;                 // [T k][h_cols] bf16, or [H_TERMS][T k][h_cols] E4M3 terms
     uint8_t* h_scale;           // [H_TERMS][T k][h_scale_pitch]
-    Routing* tables;            // the up kernel's, for the down kernel (unless small_routing)
+    float* partial;             // [output tile][share][T][TILE]
+    uint32_t* tickets;          // [output tile]
     int h_cols, h_scale_pitch;
     int T, E, k, H, F;
-    int splits;                 // CTAs of a cluster: up shares K, down the experts
+    int tiles, shares;          // output tiles, and the CTAs that share one
     __nv_bfloat16* out;
     float* out32;
     uint32_t* err;
@@ -99,10 +101,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
-
-// Whether both kernels route for themselves. Beyond that the up kernel leaves its tables in memory, and the down
-// kernel, whose CTAs mostly start when the up kernel's end, reads them: 1 us instead of 5 at 32 tokens.
-__host__ __device__ __forceinline__ bool small_routing(int T, int k) { return T <= TOK && T * k <= 64; }
 
 // Per token the k largest logits (ties to the lower expert), weights exp(l - l_max) / sum in fp32; all
 // zero when every logit is -infinity. W lanes a token, PER of its logits each.
@@ -314,34 +312,22 @@ __device__ __forceinline__ void route(Routing& r, const FewParams& p, int warp, 
         else route_tokens<16, 16>(r, p, warp, lane);
     }
     __syncthreads();
-    if (small_routing(p.T, p.k)) small_tables(r, p);
+    if (p.T <= TOK && p.T * p.k <= 64) small_tables(r, p);
     else large_tables(r, p, warp, lane);
 }
 
-// ------------------------------------------------------------------ the two kernels
-struct Bars {
+// ------------------------------------------------------------------ the kernel
+struct alignas(16) Smem {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], done;
-    uint32_t tmem;
-};
-static_assert(sizeof(Routing) % 16 == 0, "copied in 16-byte pieces");
-struct UpSmem {
-    Bars b;
-    Routing r;
-    float turn[UP_F][TOK + 1];                    // the up rows' sums, on their way to the gate rows' threads
-    float red[MAX_CLUSTER - 1][TOK][TILE];        // the other CTAs' sums
-};
-struct alignas(16) DownSmem {
-    Bars b;
+    uint32_t tmem, last;
+    float turn[TILE][TOK + 1];  // a tile's sums, on their way to the threads that make h
     Routing r;
 };
-template <bool MX, bool UP>
+template <bool MX>
 constexpr int smem_bytes(int T) {
-    return 1024 + Cfg<MX, UP>::STAGES * Cfg<MX, UP>::STAGE +
-           (UP ? (int)sizeof(UpSmem) : (int)sizeof(DownSmem) + T * TILE * (int)sizeof(float));
+    return 1024 + Cfg<MX>::STAGES * Cfg<MX>::STAGE + (int)sizeof(Smem) + T * TILE * (int)sizeof(float);
 }
-static_assert(smem_bytes<true, true>(MAX_T) <= 232448 - 64 && smem_bytes<true, false>(MAX_T) <= 232448 - 64 &&
-                  smem_bytes<false, false>(MAX_T) <= 232448 - 64,
-              "shared memory");
+static_assert(smem_bytes<true>(MAX_T) <= 232448 - 64 && smem_bytes<false>(MAX_T) <= 232448 - 64, "shared memory");
 
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -354,73 +340,63 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 __host__ __device__ constexpr uint32_t bf16_idesc(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ float4 ld_cluster(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-    return v;
-}
 
-// The columns f0 to f0 + 63 of h for n tokens, from a tile's sums: warps q = 0 and 1 have the gate
-// rows, 2 and 3 the up rows. All four warps of the epilogue.
+// The columns f0 to f0 + 63 of h for n tokens, from the sums in sm.turn. The epilogue's 128 threads.
 template <bool MX>
-__device__ __forceinline__ void write_h(const FewParams& p, UpSmem& sm, const float (&v)[TOK], int q, int lane, int row0, int n,
-                                        int f0) {
-    if (q >= 2)
+__device__ __forceinline__ void write_h(const FewParams& p, const Smem& sm, int tid, int row0, int n, int f0) {
+    const int c = tid & 63, f = f0 + c;
+    const int64_t R = (int64_t)p.T * p.k;
+#pragma unroll 1
+    for (int j = tid >> 6; j < n; j += 2) {
+        const float g = sm.turn[c][j], h = g / (1.f + __expf(-g)) * sm.turn[UP_F + c][j];
+        if (MX) {  // a warp has one block of 32: each term takes four bits of what the ones before leave
+            const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu) >> 23;
+            float rest = h;
 #pragma unroll
-        for (int j = 0; j < TOK; ++j) sm.turn[(q - 2) * 32 + lane][j] = v[j];
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (q < 2) {
-        const int f = f0 + q * 32 + lane;
-        const int64_t R = (int64_t)p.T * p.k;
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            if (j >= n) continue;
-            const float g = v[j], h = g / (1.f + __expf(-g)) * sm.turn[q * 32 + lane][j];
-            if (MX) {  // one block of 32: each term takes four bits of what the ones before leave
-                const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu), e = m >> 23;
-                float rest = h;
-#pragma unroll
-                for (int i = 0; i < H_TERMS; ++i) {
-                    const uint32_t low = 7 + 5 * i, b = e == 255 ? 255 : e < low ? 0 : e - low;
-                    uint16_t t;
-                    uint32_t back;
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t) : "f"(0.f), "f"(rest * __uint_as_float((254 - min(b, 253u)) << 23)));
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(t));
-                    rest -= __half2float(__ushort_as_half((unsigned short)(back & 0xffffu))) * e8m0_to_float(min(b, 254u));
-                    p.h[(i * R + row0 + j) * p.h_cols + f] = e == 255 ? 0 : (uint8_t)t;
-                    if (lane == 0) p.h_scale[(i * R + row0 + j) * p.h_scale_pitch + (f0 + q * 32) / 32] = (uint8_t)b;
-                }
-            } else {
-                reinterpret_cast<__nv_bfloat16*>(p.h)[(int64_t)(row0 + j) * p.h_cols + f] = __float2bfloat16_rn(h);
+            for (int i = 0; i < H_TERMS; ++i) {
+                const uint32_t low = 7 + 5 * i, b = e == 255 ? 255 : e < low ? 0 : e - low;
+                uint16_t t;
+                uint32_t back;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t) : "f"(0.f), "f"(rest * __uint_as_float((254 - min(b, 253u)) << 23)));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(t));
+                rest -= __half2float(__ushort_as_half((unsigned short)(back & 0xffffu))) * e8m0_to_float(min(b, 254u));
+                p.h[(i * R + row0 + j) * p.h_cols + f] = e == 255 ? 0 : (uint8_t)t;
+                if ((c & 31) == 0) p.h_scale[(i * R + row0 + j) * p.h_scale_pitch + f / 32] = (uint8_t)b;
             }
+        } else {
+            reinterpret_cast<__nv_bfloat16*>(p.h)[(int64_t)(row0 + j) * p.h_cols + f] = __float2bfloat16_rn(h);
         }
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-// A CTA's line of work: units of ks stages (stages k0 to k0 + ks of the unit's K) each. Up: a unit is a
-// (chunk, tile of h); down: a chunk.
-template <bool MX, bool UP>
+// A CTA's line of work of a phase: units of ks stages each. Up: a unit is a (chunk, tile of h); down: a
+// (output tile, chunk).
+struct Line {
+    int first, step, units, ks;
+    __device__ __forceinline__ int unit(int u) const { return first + u * step; }
+    __device__ __forceinline__ int stages() const { return units * ks; }
+};
+
+template <bool MX>
 __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_constant__ FewParams p) {
-    using C = Cfg<MX, UP>;
+    using C = Cfg<MX>;
     constexpr int KV = MX ? 128 : 64;  // values of K in a stage
-    constexpr int BQ = C::BQ, Q_BYTES = C::Q_BYTES, STAGE = C::STAGE, STAGES = C::STAGES;
+    constexpr int STAGE = C::STAGE, STAGES = C::STAGES;
     extern __shared__ uint8_t raw_smem[];
     const uint32_t raw = smem_addr(raw_smem), base = (raw + 1023u) & ~1023u;
     uint8_t* gen = raw_smem + (base - raw) + STAGES * STAGE;
-    Bars& bars = *reinterpret_cast<Bars*>(gen);
-    Routing& rt = UP ? reinterpret_cast<UpSmem*>(gen)->r : reinterpret_cast<DownSmem*>(gen)->r;
-    float* sums = reinterpret_cast<float*>(gen + sizeof(DownSmem));  // down: [T][TILE]
-    const uint32_t full0 = smem_addr(bars.full), empty0 = smem_addr(bars.empty), acc_full0 = smem_addr(bars.acc_full),
-                   acc_empty0 = smem_addr(bars.acc_empty), done = smem_addr(&bars.done);
+    Smem& sm = *reinterpret_cast<Smem*>(gen);
+    Routing& rt = sm.r;
+    float* sums = reinterpret_cast<float*>(gen + sizeof(Smem));  // down: [T][TILE]
+    const uint32_t full0 = smem_addr(sm.full), empty0 = smem_addr(sm.empty), acc_full0 = smem_addr(sm.acc_full),
+                   acc_empty0 = smem_addr(sm.acc_empty), done = smem_addr(&sm.done);
     __shared__ volatile int stop;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
-    constexpr bool FEED = MX || UP;  // down with bf16 weights has nothing to add to a stage
 
     if (threadIdx.x == 0) {
         stop = 0;
         for (int s = 0; s < STAGES; ++s) {
-            bar_init(full0 + 8 * s, FEED ? 2 : 1);  // the TMA thread and the stage's feed warp
+            bar_init(full0 + 8 * s, 2);  // the TMA thread and the stage's feed warp
             bar_init(empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -429,159 +405,106 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
         }
         bar_init(done, 1);
         bar_init_fence();
-        tma_desc_prefetch(&p.map_p);
-        tma_desc_prefetch(&p.map_p2);
+        tma_desc_prefetch(&p.gate);
+        tma_desc_prefetch(&p.up);
+        tma_desc_prefetch(&p.down);
+        tma_desc_prefetch(&p.map_h);
     }
-    if (warp == 1) tmem_get(smem_addr(&bars.tmem), C::TMEM_COLS);
-    if (!UP)
-        for (int i = threadIdx.x; i < p.T * TILE; i += THREADS) sums[i] = 0.f;
+    if (warp == 1) tmem_get(smem_addr(&sm.tmem), TMEM_COLS);
+    for (int i = threadIdx.x; i < p.T * TILE; i += THREADS) sums[i] = 0.f;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < p.tiles; i += THREADS) p.tickets[i] = 0;
     fence_before_sync();
-    // up: everything earlier is complete after the wait, so the down kernel, which may be placed from here on, can
-    // read the logits and the weights at once; only h has to wait for this kernel
-    if (UP) {
-        grid_wait();
-        grid_release();
-    }
-    if (UP || small_routing(p.T, p.k)) {
-        route(rt, p, warp, lane);  // ends with a barrier of the CTA
-    } else {
-        grid_wait();
-        const uint4* from = reinterpret_cast<const uint4*>(p.tables);
-        for (int i = threadIdx.x; i < (int)(sizeof(Routing) / 16); i += THREADS) reinterpret_cast<uint4*>(&rt)[i] = __ldcg(from + i);
-        __syncthreads();
-    }
-    if (UP && blockIdx.x == 0 && !small_routing(p.T, p.k))
-        for (int i = threadIdx.x; i < (int)(sizeof(Routing) / 16); i += THREADS)
-            reinterpret_cast<uint4*>(p.tables)[i] = reinterpret_cast<const uint4*>(&rt)[i];
-    if (p.splits > 1) {
-        __syncwarp();
-        cluster_barrier();
-    }
+    grid_wait();
+    route(rt, p, warp, lane);  // begins and ends with a barrier of the CTA
     fence_after_sync();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = sm.tmem;
 
-    const int rank = (int)blockIdx.x % p.splits, cluster = (int)blockIdx.x / p.splits;
-    const int stages = ((UP ? p.H : p.F) + KV - 1) / KV;
-    int unit0, unit_step, n_units, k0 = 0, ks = stages;
-    const int n_f = (p.h_cols + UP_F - 1) / UP_F;
-    if (UP) {
-        k0 = rank * stages / p.splits;
-        ks = (rank + 1) * stages / p.splits - k0;
-        unit0 = cluster;
-        unit_step = (int)gridDim.x / p.splits;
-        const int units = rt.n_chunks * n_f;
-        n_units = unit0 < units ? (units - 1 - unit0) / unit_step + 1 : 0;
-    } else {
-        unit0 = rank * rt.n_chunks / p.splits;
-        unit_step = 1;
-        n_units = (rank + 1) * rt.n_chunks / p.splits - unit0;
-    }
-    const int row_p = UP ? 0 : cluster * TILE;  // down: the tile's rows
-    auto chunk_of = [&](int u) { return UP ? u / n_f : u; };
-    auto f_of = [&](int u) { return UP ? u % n_f * UP_F : 0; };
-    const int R = p.T * p.k;
+    const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
+    const int n_f = (p.h_cols + UP_F - 1) / UP_F, n_chunks = rt.n_chunks;
+    Line up, down;
+    up.first = cta;
+    up.step = grid;
+    up.ks = (p.H + KV - 1) / KV;
+    up.units = cta < n_chunks * n_f ? (n_chunks * n_f - 1 - cta) / grid + 1 : 0;
+    // down: CTA b has share b / tiles of tile b % tiles, or (more tiles than CTAs) whole tiles b, b + grid, ...
+    const int share = p.shares > 1 ? cta / p.tiles : 0;
+    const int c0 = share * n_chunks / p.shares, own = share < p.shares ? (share + 1) * n_chunks / p.shares - c0 : 0;
+    const int out_tiles = p.shares > 1 ? 1 : cta < p.tiles ? (p.tiles - 1 - cta) / grid + 1 : 0;
+    down.first = 0;
+    down.step = 1;
+    down.ks = (p.F + KV - 1) / KV;
+    down.units = out_tiles * own;
+    auto down_chunk = [&](int u) { return c0 + u % own; };
+    auto down_tile = [&](int u) { return p.shares > 1 ? cta % p.tiles : cta + u / own * grid; };
+    const int R = p.T * p.k, base_it = up.stages();
+    const bool one = elect_one();
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ weights (down: and h)
-        const bool one = elect_one();
-        constexpr uint32_t BYTES = (MX ? P_BYTES / 2 : P_BYTES) + (UP ? 0 : C::TERMS * TOK * 128);
-        auto load_p = [&](int s, int chunk, int f0, int k) {
-            const uint32_t at = base + s * STAGE, bar = full0 + 8 * s;
-            const int e = rt.chunk_e[chunk], x = k * KV;
-            bar_expect(bar, BYTES);
-            if (UP) {
-                tma_3d(at, &p.map_p, bar, x, f0, e);
-                tma_3d(at + P_BYTES / 2, &p.map_p2, bar, x, f0, e);
-            } else {
-                tma_3d(at, &p.map_p, bar, x, row_p, e);
-            }
-        };
-        auto load_h = [&](int s, int chunk, int k) {
-            if (MX) tma_3d(base + s * STAGE + P_BYTES, &p.map_p2, full0 + 8 * s, k * KV, rt.chunk_row[chunk], 0);
-            else tma_2d(base + s * STAGE + P_BYTES, &p.map_p2, full0 + 8 * s, k * KV, rt.chunk_row[chunk]);
-        };
-        int s = 0, it = 0, u = 0, k = 0;
-        uint32_t phase = 1;
-        bool ok = true;
-        if (!UP) {  // the first round's weights before h is complete
-            const int ahead = min(STAGES, n_units * ks);
-            if (one)
-                for (int i = 0, v = 0, q = 0; i < ahead; ++i) {
-                    load_p(i, unit0 + v, 0, q);
-                    if (++q == ks) {
-                        q = 0;
-                        ++v;
-                    }
-                }
-            grid_wait();
-            if (one)
-                for (int i = 0, v = 0, q = 0; i < ahead; ++i) {
-                    load_h(i, unit0 + v, q);
-                    if (++q == ks) {
-                        q = 0;
-                        ++v;
-                    }
-                }
-            __syncwarp();
-            it = ahead;
-            u = ahead / ks;
-            k = ahead % ks;
-            s = ahead % STAGES;
-            phase ^= ahead == STAGES ? 1u : 0u;
+    // ---- state of the roles across the meeting
+    int s = 0;
+    uint32_t phase = warp == 0 ? 1u : 0u;  // for the producer a new barrier's preceding phase counts as complete
+    bool ok = true, ready = false;
+    int acc = 0;                            // accumulators used so far
+    auto next_stage = [&] {
+        if (++s == STAGES) {
+            s = 0;
+            phase ^= 1u;
         }
-        for (; ok && u < n_units; ++u, k = 0) {
-            const int unit = unit0 + u * unit_step, chunk = chunk_of(unit), f0 = f_of(unit);
-            for (; k < ks; ++k, ++it) {
-                if (!bar_wait_warp(empty0 + 8 * s, phase, p.err, 1)) {
-                    ok = false;
-                    stop = 1;
-                    break;
-                }
-                if (one) {
-                    load_p(s, chunk, f0, k0 + k);
-                    if (!UP) load_h(s, chunk, k);
-                }
-                __syncwarp();
-                if (++s == STAGES) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
+    };
+    struct Turn {                           // a feed warp's data of a stage
+        uint32_t sp[4], sq;
+        uint4 x[MX ? 4 : 2];
+    };
+    Turn cur;
+
+    // ---- the roles' parts of a phase
+    constexpr uint32_t P_COUNT = MX ? P_BYTES / 2 : P_BYTES;  // an unpacking copy counts the packed bytes
+    auto load_up = [&](int unit, int k) {
+        const int chunk = unit / n_f, e = rt.chunk_e[chunk], f0 = unit % n_f * UP_F;
+        const uint32_t at = base + s * STAGE, bar = full0 + 8 * s;
+        bar_expect(bar, P_COUNT);
+        tma_3d(at, &p.gate, bar, k * KV, f0, e);
+        tma_3d(at + P_BYTES / 2, &p.up, bar, k * KV, f0, e);
+    };
+    auto load_down = [&](int u, int k) {
+        const uint32_t bar = full0 + 8 * s;
+        bar_expect(bar, P_COUNT + (MX ? H_TERMS : 1) * TOK * 128);
+        if (!MX) bar_arrive(bar);  // no feed warp has anything to add
+        tma_3d(base + s * STAGE, &p.down, bar, k * KV, down_tile(u) * TILE, rt.chunk_e[down_chunk(u)]);
+    };
+    auto load_h = [&](int st, int u, int k) {
+        const uint32_t at = base + st * STAGE + P_BYTES, bar = full0 + 8 * st;
+        if (MX) tma_3d(at, &p.map_h, bar, k * KV, rt.chunk_row[down_chunk(u)], 0);
+        else tma_2d(at, &p.map_h, bar, k * KV, rt.chunk_row[down_chunk(u)]);
+    };
+    auto wait_empty = [&] {
+        if (ok && !bar_wait_warp(empty0 + 8 * s, phase, p.err, 1)) {
+            ok = false;
+            stop = 1;
         }
-        if (stop)  // an aborted CTA waits for its own copies before it exits
-            for (int i = 0; i < STAGES && i < it; ++i) {
-                const int last = it - 1 - (it - 1 - i) % STAGES;
-                bar_wait(full0 + 8 * i, (uint32_t)(last / STAGES) & 1u, p.err, 5);
-            }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ products
-        constexpr uint32_t IDESC = MX ? mx_idesc(5, 0, TILE, BQ) : bf16_idesc(TILE, BQ);
-        const bool one = elect_one();
-        int s = 0;
-        uint32_t phase = 0;
-        bool ok = true, ready = false;  // ready: the next stage's barrier, asked before this stage's products
-        for (int u = 0; ok && u < n_units; ++u) {
-            const int b = u & 1;
-            if (!bar_wait_warp(acc_empty0 + 8 * b, (uint32_t)((u >> 1) + 1) & 1u, p.err, 2) || stop) {
+        return ok;
+    };
+    auto products = [&](const Line& line, uint32_t idesc) {
+        for (int u = 0; ok && u < line.units; ++u, ++acc) {
+            const int b = acc & 1;
+            if (!bar_wait_warp(acc_empty0 + 8 * b, (uint32_t)((acc >> 1) + 1) & 1u, p.err, 2) || stop) {
+                ok = false;
                 stop = 1;
                 break;
             }
             fence_after_sync();
-            const uint32_t d = tmem + (uint32_t)(b * BQ);
-            for (int k = 0; k < ks; ++k) {
+            const uint32_t d = tmem + (uint32_t)(b * C::Q_ROWS);
+            for (int k = 0; k < line.ks; ++k) {
                 if (!__all_sync(0xffffffffu, ready) && !bar_wait_warp(full0 + 8 * s, phase, p.err, 3)) {
                     ok = false;
                     stop = 1;
                     break;
                 }
                 fence_after_sync();
-                const uint32_t sp = base + s * STAGE, sq = sp + P_BYTES, sc = sq + Q_BYTES;
-                const uint32_t tp = tmem + (uint32_t)(2 * BQ + s * 8), freed = empty0 + 8 * s;
-                if (++s == STAGES) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-                ready = bar_test(full0 + 8 * s, phase);
+                const uint32_t sp = base + s * STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
+                const uint32_t tp = tmem + (uint32_t)(2 * C::Q_ROWS + s * 8), freed = empty0 + 8 * s;
+                next_stage();
+                ready = bar_test(full0 + 8 * s, phase);  // asked before this stage's products
                 if (one) {
                     if (MX) {
                         scale_copy(tp, scale_desc(sc));
@@ -589,9 +512,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // 32 bytes of each row
-                        const uint32_t acc = (k > 0 || i > 0) ? 1u : 0u;
-                        if (MX) mma_mxf8(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), idesc_at(IDESC, i), tp, tp + 4, acc);
-                        else mma_bf16(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), IDESC, acc);
+                        const uint32_t add = (k > 0 || i > 0) ? 1u : 0u;
+                        if (MX) mma_mxf8(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), idesc_at(idesc, i), tp, tp + 4, add);
+                        else mma_bf16(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), idesc, add);
                     }
                     mma_commit(freed);
                 }
@@ -600,223 +523,267 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
             if (ok && one) mma_commit(acc_full0 + 8 * b);
             __syncwarp();
         }
-        if (one) mma_commit(done);
-        __syncwarp();
-        bar_wait(done, 0, p.err, 6);
-    } else if (warp < FIRST_EPI) {
-        // ------------------------------------------------------------ scales, and the tokens' rows
-        if (FEED) {
-            // a warp's turn is every eighth stage; it requests the next turn's data before this one's work
-            constexpr int UNITS = MX ? 4 : 2;  // up: pieces of 8 values a lane
-            const int total = n_units * ks;
-            struct Turn {
-                uint32_t sp[4], sq;
-                uint4 x[UP ? UNITS : 1];
-            };
-            auto fetch = [&](Turn& to, int it, bool weights, bool rest) {
-                if (it >= total) return;
-                const int u = it / ks, k = k0 + it - u * ks, unit = unit0 + u * unit_step;
-                const int chunk = chunk_of(unit), e = rt.chunk_e[chunk], n = rt.chunk_n[chunk], row0 = rt.chunk_row[chunk];
-                if (MX && weights) {
+    };
+    // the scales of a stage of 128 weight rows, lane l with rows l, l + 32, l + 64, l + 96; and in down those of h
+    auto fetch_up = [&](Turn& to, int i) {
+        if (i >= up.stages()) return;
+        const int u = i / up.ks, k = i - u * up.ks, unit = up.unit(u), chunk = unit / n_f, f0 = unit % n_f * UP_F;
+        const int e = rt.chunk_e[chunk], n = rt.chunk_n[chunk], row0 = rt.chunk_row[chunk];
+        if (MX) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = lane + 32 * j;
-                        const uint8_t* sp = UP && j >= 2 ? p.scale_p2 : p.scale_p;
-                        const int row = UP ? f_of(unit) + (r & (UP_F - 1)) : row_p + r;
-                        const bool in = row < (UP ? p.F : p.H);
-                        to.sp[j] = in ? __ldg(reinterpret_cast<const uint32_t*>(sp + e * p.scale_stride + (int64_t)row * p.scale_pitch + 4 * k)) : 0u;
-                    }
-                }
-                if (!rest) return;
-                if (MX && !UP) {  // lane: term lane / 8 of row lane % 8
-                    to.sq = lane < C::TERMS * TOK && (lane & 7) < n
-                                ? __ldcg(reinterpret_cast<const uint32_t*>(p.h_scale + ((int64_t)(lane >> 3) * R + row0 + (lane & 7)) * p.h_scale_pitch + 4 * k))
-                                : 0u;
-                }
-                if (UP) {
-#pragma unroll
-                    for (int j = 0; j < UNITS; ++j) {
-                        // MXFP4: 16 pieces of a token's 128 values, two tokens at a time; bf16: 8 of 64, four
-                        const int tok = MX ? (lane >> 4) + 2 * j : (lane >> 3) + 4 * j, at = k * KV + 8 * (MX ? lane & 15 : lane & 7);
-                        const bool in = tok < n && at < p.H;  // H is a multiple of 8
-                        to.x[j] = in ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)rt.row_t[row0 + tok] * p.H + at))
-                                     : make_uint4(0, 0, 0, 0);
-                    }
-                }
-            };
-            const int first = warp - 2;
-            Turn cur, nxt;
-            if (UP) {
-                fetch(cur, first, true, true);
-            } else {
-                fetch(cur, first, true, false);
-                grid_wait();
-                fetch(cur, first, false, true);
-            }
-            bool ok = true;
-            for (int it = first; ok && it < total; it += FEED_WARPS) {
-                fetch(nxt, it + FEED_WARPS, true, true);
-                const int s = it % STAGES;
-                if (!bar_wait_warp(empty0 + 8 * s, (uint32_t)(it / STAGES + 1) & 1u, p.err, 7)) {
-                    ok = false;
-                    stop = 1;
-                    break;
-                }
-                const uint32_t sq = base + s * STAGE + P_BYTES, sc = sq + Q_BYTES;
-                if (MX) {
-                    // rows l, l + 32, l + 64, l + 96: side by side in the order that the tensor core reads
-                    st_shared4(sc + 16 * lane, cur.sp[0], cur.sp[1], cur.sp[2], cur.sp[3]);
-                    if (!UP)
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 512 + 16 * lane), "r"(cur.sq) : "memory");
-                }
-                if (UP) {
-                    const int n = rt.chunk_n[chunk_of(unit0 + it / ks * unit_step)];
-#pragma unroll
-                    for (int j = 0; j < UNITS; ++j) {
-                        if ((MX ? 2 : 4) * j >= n) continue;  // columns of tokens that do not exist hold anything
-                        if (MX) {
-                            uint2 o1, o2;
-                            uint32_t b1, b2;
-                            split8(cur.x[j], o1, o2, b1, b2);
-                            const int g = lane & 15, r = (lane >> 4) + 2 * j;
-                            const uint32_t at = sq + r * 128 + (uint32_t)((((g >> 1) ^ (r & 7)) << 4) + (g & 1) * 8);
-                            st_shared2(at, o1.x, o1.y);
-                            st_shared2(at + TOK * 128, o2.x, o2.y);
-                            if ((g & 3) == 0) {
-                                const uint32_t to = sc + 512 + (uint32_t)(r * 16 + (g >> 2));
-                                asm volatile("st.shared.u8 [%0], %1;" ::"r"(to), "r"(b1) : "memory");
-                                asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + TOK * 16), "r"(b2) : "memory");
-                            }
-                        } else {
-                            const int g = lane & 7, r = (lane >> 3) + 4 * j;
-                            st_shared4(sq + r * 128 + (uint32_t)((g ^ r) << 4), cur.x[j].x, cur.x[j].y, cur.x[j].z, cur.x[j].w);
-                        }
-                    }
-                }
-                fence_smem_async();
-                __syncwarp();
-                if (lane == 0) bar_arrive(full0 + 8 * s);
-                cur = nxt;
+            for (int j = 0; j < 4; ++j) {
+                const int f = f0 + ((lane + 32 * j) & (UP_F - 1));
+                to.sp[j] = f < p.F ? __ldg(reinterpret_cast<const uint32_t*>((j < 2 ? p.gate_scale : p.up_scale) + e * p.up_scale_stride +
+                                                                             (int64_t)f * p.up_scale_pitch + 4 * k))
+                                   : 0u;
             }
         }
-    }
-    // ------------------------------------------------------------ results
-    const int q = warp & 3, row = q * 32 + lane;  // the TMEM lane quarter that this warp can read
-    bool bad = false;  // a wait ran out: no later one is made, and the results are void
-    auto take = [&](int u, float (&v)[TOK]) {
-        const int b = u & 1;
-        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + b * BQ;
-        if (!bad) bad = !bar_wait_warp(acc_full0 + 8 * b, (uint32_t)(u >> 1) & 1u, p.err, 4);
+#pragma unroll
+        for (int j = 0; j < (MX ? 4 : 2); ++j) {
+            // MXFP4: 16 pieces of a token's 128 values, two tokens at a time; bf16: 8 of 64, four
+            const int tok = MX ? (lane >> 4) + 2 * j : (lane >> 3) + 4 * j, at = k * KV + 8 * (MX ? lane & 15 : lane & 7);
+            to.x[j] = tok < n && at < p.H  // H is a multiple of 8
+                          ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)rt.row_t[row0 + tok] * p.H + at))
+                          : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto fetch_down = [&](Turn& to, int i, bool weights, bool h) {
+        if (i >= down.stages()) return;
+        const int u = i / down.ks, k = i - u * down.ks, chunk = down_chunk(u), e = rt.chunk_e[chunk];
+        if (weights)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = down_tile(u) * TILE + lane + 32 * j;
+                to.sp[j] = row < p.H ? __ldg(reinterpret_cast<const uint32_t*>(p.down_scale + e * p.down_scale_stride +
+                                                                               (int64_t)row * p.down_scale_pitch + 4 * k))
+                                     : 0u;
+            }
+        if (h)  // lane: term lane / 8 of row lane % 8
+            to.sq = lane < H_TERMS * TOK && (lane & 7) < rt.chunk_n[chunk]
+                        ? __ldcg(reinterpret_cast<const uint32_t*>(p.h_scale + ((int64_t)(lane >> 3) * R + rt.chunk_row[chunk] + (lane & 7)) * p.h_scale_pitch + 4 * k))
+                        : 0u;
+    };
+    auto feed_wait = [&](int it) {
+        if (!bar_wait_warp(empty0 + 8 * (it % STAGES), (uint32_t)(it / STAGES + 1) & 1u, p.err, 7)) {
+            ok = false;
+            stop = 1;
+        }
+        return ok;
+    };
+    auto feed_done = [&](int it) {
+        fence_smem_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(full0 + 8 * (it % STAGES));
+    };
+    const int q = warp & 3, row = q * 32 + lane;  // the epilogue: the TMEM lane quarter that a warp can read
+    bool bad = false;                              // a wait ran out: no later one is made, and the results are void
+    auto take = [&](float (&v)[TOK], int terms) {
+        const int b = acc & 1;
+        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + b * C::Q_ROWS;
+        if (!bad) bad = !bar_wait_warp(acc_full0 + 8 * b, (uint32_t)(acc >> 1) & 1u, p.err, 4);
         if (bad) stop = 1;
         fence_after_sync();
-        uint32_t x[C::TERMS][8];
+        uint32_t x[H_TERMS][8];
 #pragma unroll
-        for (int i = 0; i < C::TERMS; ++i) tmem_load8(t + i * TOK, x[i]);
+        for (int i = 0; i < H_TERMS; ++i)
+            if (i < terms) tmem_load8(t + i * TOK, x[i]);
         tmem_load_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) bar_arrive(acc_empty0 + 8 * b);
+        ++acc;
 #pragma unroll
         for (int j = 0; j < TOK; ++j) {
-            v[j] = __uint_as_float(x[C::TERMS - 1][j]);  // the smallest first
+            v[j] = 0.f;
 #pragma unroll
-            for (int i = C::TERMS - 2; i >= 0; --i) v[j] += __uint_as_float(x[i][j]);
+            for (int i = H_TERMS - 1; i >= 0; --i)  // the smallest first
+                if (i < terms) v[j] += __uint_as_float(x[i][j]);
         }
     };
-    if (UP) {
-        UpSmem& sm = *reinterpret_cast<UpSmem*>(gen);
-        if (p.splits == 1) {
-            if (warp >= FIRST_EPI)
-                for (int u = 0; u < n_units; ++u) {
-                    float v[TOK];
-                    take(u, v);
-                    const int unit = unit0 + u * unit_step, chunk = chunk_of(unit);
-                    write_h<MX>(p, sm, v, q, lane, rt.chunk_row[chunk], rt.chunk_n[chunk], f_of(unit));
-                }
-        } else {  // one unit a cluster: the later CTAs leave their sums in the first one's memory
-            if (warp >= FIRST_EPI && rank > 0 && n_units > 0) {
-                float v[TOK];
-                take(0, v);
-                const uint32_t to = cluster_addr(smem_addr(&sm.red[rank - 1][0][row]), 0);
+
+    // ---- up
+    int it = 0;     // the producer's stages so far
+    int ahead = 0;  // stages of down whose weights are requested before the meeting
+    if (warp == 0) {
+        for (int u = 0; ok && u < up.units; ++u)
+            for (int k = 0; k < up.ks && wait_empty(); ++k, ++it) {
+                if (one) load_up(up.unit(u), k);
+                __syncwarp();
+                next_stage();
+            }
+        for (; ahead < min(STAGES, down.stages()) && wait_empty(); ++ahead, ++it) {
+            if (one) load_down(ahead / down.ks, ahead % down.ks);
+            __syncwarp();
+            next_stage();
+        }
+    } else if (warp == 1) {
+        products(up, MX ? mx_idesc(5, 0, TILE, 16) : bf16_idesc(TILE, 16));
+    } else if (warp < FIRST_EPI) {
+        // a turn is every eighth stage; the next turn's data are requested before this one's work
+        Turn nxt;
+        const int w = warp - 2;
+        fetch_up(cur, w);
+        for (int i = w; ok && i < up.stages(); i += FEED_WARPS) {
+            fetch_up(nxt, i + FEED_WARPS);
+            if (!feed_wait(i)) break;
+            const uint32_t sq = base + i % STAGES * STAGE + P_BYTES, sc = sq + C::Q_BYTES;
+            if (MX) st_shared4(sc + 16 * lane, cur.sp[0], cur.sp[1], cur.sp[2], cur.sp[3]);
+            const int n = rt.chunk_n[up.unit(i / up.ks) / n_f];
 #pragma unroll
-                for (int j = 0; j < TOK; ++j) st_cluster(to + j * TILE * 4, v[j]);
+            for (int j = 0; j < (MX ? 4 : 2); ++j) {
+                if ((MX ? 2 : 4) * j >= n) continue;  // columns of tokens that do not exist hold anything
+                if (MX) {
+                    uint2 o1, o2;
+                    uint32_t b1, b2;
+                    split8(cur.x[j], o1, o2, b1, b2);
+                    const int g = lane & 15, r = (lane >> 4) + 2 * j;
+                    const uint32_t at = sq + r * 128 + (uint32_t)((((g >> 1) ^ (r & 7)) << 4) + (g & 1) * 8);
+                    st_shared2(at, o1.x, o1.y);
+                    st_shared2(at + TOK * 128, o2.x, o2.y);
+                    if ((g & 3) == 0) {
+                        const uint32_t to = sc + 512 + (uint32_t)(r * 16 + (g >> 2));
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(to), "r"(b1) : "memory");
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(to + TOK * 16), "r"(b2) : "memory");
+                    }
+                } else {
+                    const int g = lane & 7, r = (lane >> 3) + 4 * j;
+                    st_shared4(sq + r * 128 + (uint32_t)((g ^ r) << 4), cur.x[j].x, cur.x[j].y, cur.x[j].z, cur.x[j].w);
+                }
+            }
+            feed_done(i);
+            cur = nxt;
+        }
+        // the weights' scales of this warp's first turn of down: the first stage it with it % 8 = w
+        if (MX) fetch_down(cur, ((w - base_it) % FEED_WARPS + FEED_WARPS) % FEED_WARPS, true, false);
+    } else {
+        for (int u = 0; u < up.units; ++u) {
+            float v[TOK];
+            take(v, MX ? X_TERMS : 1);
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) sm.turn[row][j] = v[j];
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int unit = up.unit(u), chunk = unit / n_f;
+            write_h<MX>(p, sm, (int)threadIdx.x - 32 * FIRST_EPI, rt.chunk_row[chunk], rt.chunk_n[chunk], unit % n_f * UP_F);
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        // h is read by tensor copies of other CTAs
+        asm volatile("fence.proxy.async;" ::: "memory");
+    }
+
+    // ---- the meeting: h is complete
+    __syncwarp();
+    cooperative_groups::this_grid().sync();
+
+    // ---- down
+    if (warp == 0) {
+        asm volatile("fence.proxy.async;" ::: "memory");
+        if (one)
+            for (int i = 0; i < ahead; ++i) load_h((base_it + i) % STAGES, i / down.ks, i % down.ks);
+        __syncwarp();
+        for (int i = ahead; i < down.stages() && wait_empty(); ++i, ++it) {
+            const int u = i / down.ks, k = i - u * down.ks;
+            if (one) {
+                load_down(u, k);
+                load_h(s, u, k);
             }
             __syncwarp();
-            cluster_barrier();
-            if (warp >= FIRST_EPI && rank == 0 && n_units > 0) {
-                float v[TOK];
-                take(0, v);
-#pragma unroll
-                for (int j = 0; j < TOK; ++j)
-                    for (int i = 0; i < p.splits - 1; ++i) v[j] += sm.red[i][j][row];
-                const int chunk = chunk_of(unit0);
-                write_h<MX>(p, sm, v, q, lane, rt.chunk_row[chunk], rt.chunk_n[chunk], f_of(unit0));
+            next_stage();
+        }
+        if (stop)  // an aborted CTA waits for its own copies before it exits
+            for (int i = 0; i < STAGES && i < it; ++i) {
+                const int last = it - 1 - (it - 1 - i) % STAGES;
+                bar_wait(full0 + 8 * i, (uint32_t)(last / STAGES) & 1u, p.err, 5);
+            }
+    } else if (warp == 1) {
+        products(down, MX ? mx_idesc(5, 0, TILE, 32) : bf16_idesc(TILE, 16));
+        if (one) mma_commit(done);
+        __syncwarp();
+        bar_wait(done, 0, p.err, 6);
+    } else if (warp < FIRST_EPI) {
+        if (MX) {
+            Turn nxt;
+            const int i0 = ((warp - 2 - base_it) % FEED_WARPS + FEED_WARPS) % FEED_WARPS;
+            fetch_down(cur, i0, false, true);
+            for (int i = i0; ok && i < down.stages(); i += FEED_WARPS) {
+                fetch_down(nxt, i + FEED_WARPS, true, true);
+                if (!feed_wait(base_it + i)) break;
+                const uint32_t sc = base + (base_it + i) % STAGES * STAGE + P_BYTES + C::Q_BYTES;
+                st_shared4(sc + 16 * lane, cur.sp[0], cur.sp[1], cur.sp[2], cur.sp[3]);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc + 512 + 16 * lane), "r"(cur.sq) : "memory");
+                feed_done(base_it + i);
+                cur = nxt;
             }
         }
     } else {
-        if (warp >= FIRST_EPI)
-            for (int u = 0; u < n_units; ++u) {
-                float v[TOK];
-                take(u, v);
-                const int chunk = unit0 + u, n = rt.chunk_n[chunk], row0 = rt.chunk_row[chunk];
+        for (int u = 0; u < down.units; ++u) {
+            float v[TOK];
+            take(v, MX ? H_TERMS : 1);
+            const int chunk = down_chunk(u), n = rt.chunk_n[chunk], row0 = rt.chunk_row[chunk];
 #pragma unroll
-                for (int j = 0; j < TOK; ++j)
-                    if (j < n) {
-                        float* to = sums + rt.row_t[row0 + j] * TILE + row;
-                        *to = fmaf(rt.row_w[row0 + j], v[j], *to);
-                    }
-            }
-        // the cluster's sums, in CTA order; each CTA writes a share of the outputs
-        __syncwarp();
-        if (p.splits > 1) cluster_barrier();
-        else __syncthreads();
-        for (int i = 4 * (rank * THREADS + (int)threadIdx.x); i < p.T * TILE; i += 4 * p.splits * THREADS) {
-            const int t = i / TILE, r = row_p + i % TILE;
-            if (r >= p.H) continue;  // H is a multiple of 8
-            float4 part[MAX_CLUSTER];
-#pragma unroll
-            for (int c = 0; c < MAX_CLUSTER; ++c)  // all loads before the first sum
-                if (c < p.splits)
-                    part[c] = p.splits > 1 ? ld_cluster(cluster_addr(smem_addr(sums + i), c)) : *reinterpret_cast<const float4*>(sums + i);
-            const int64_t at = (int64_t)t * p.H + r;
-            float v[4];
-            if (p.resid) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = p.resid[at + j];
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(p.x + at);
-                v[0] = __uint_as_float(x.x << 16);
-                v[1] = __uint_as_float(x.x & 0xffff0000u);
-                v[2] = __uint_as_float(x.y << 16);
-                v[3] = __uint_as_float(x.y & 0xffff0000u);
-            }
-            float4 sum = part[0];
-#pragma unroll
-            for (int c = 1; c < MAX_CLUSTER; ++c)
-                if (c < p.splits) {
-                    sum.x += part[c].x;
-                    sum.y += part[c].y;
-                    sum.z += part[c].z;
-                    sum.w += part[c].w;
+            for (int j = 0; j < TOK; ++j)
+                if (j < n) {
+                    float* to = sums + rt.row_t[row0 + j] * TILE + row;
+                    *to = fmaf(rt.row_w[row0 + j], v[j], *to);
                 }
-            v[0] += sum.x;
-            v[1] += sum.y;
-            v[2] += sum.z;
-            v[3] += sum.w;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                p.out[at + j] = __float2bfloat16_rn(v[j]);
-                if (p.out32) p.out32[at + j] = v[j];
+            if (p.shares == 1 && (u + 1) % own == 0) {  // a thread has a row of its own: no barrier
+                const int r = down_tile(u) * TILE + row;
+                for (int t = 0; t < p.T; ++t) {
+                    const int64_t at = (int64_t)t * p.H + r;
+                    if (r < p.H) {
+                        const float o = sums[t * TILE + row] + (p.resid ? p.resid[at] : __bfloat162float(p.x[at]));
+                        p.out[at] = __float2bfloat16_rn(o);
+                        if (p.out32) p.out32[at] = o;
+                    }
+                    sums[t * TILE + row] = 0.f;
+                }
             }
         }
-        __syncwarp();
-        if (p.splits > 1) cluster_barrier();  // nobody goes while its sums are read
     }
     fence_before_sync();
     __syncthreads();
     if (warp == 1) {
         fence_after_sync();
-        tmem_free(tmem, C::TMEM_COLS);
+        tmem_free(tmem, TMEM_COLS);
+    }
+    if (p.shares == 1 || share >= p.shares) return;
+
+    // ---- the sums of a tile's shares: the last CTA to leave its own adds them, in order
+    const int tile = cta % p.tiles;
+    float* part = p.partial + (int64_t)tile * p.shares * p.T * TILE;
+    for (int i = 4 * (int)threadIdx.x; i < p.T * TILE; i += 4 * THREADS)
+        *reinterpret_cast<float4*>(part + (int64_t)share * p.T * TILE + i) = *reinterpret_cast<const float4*>(sums + i);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) sm.last = atomicAdd(p.tickets + tile, 1u) == (uint32_t)p.shares - 1;
+    __syncthreads();
+    if (!sm.last) return;
+    __threadfence();
+    for (int i = 4 * (int)threadIdx.x; i < p.T * TILE; i += 4 * THREADS) {
+        const int t = i / TILE, r = tile * TILE + i % TILE;
+        if (r >= p.H) continue;  // H is a multiple of 8
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < p.shares; c0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c0 + c < p.shares) v[c] = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)(c0 + c) * p.T * TILE + i));
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c0 + c < p.shares) {
+                    sum.x += v[c].x;
+                    sum.y += v[c].y;
+                    sum.z += v[c].z;
+                    sum.w += v[c].w;
+                }
+        }
+        const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+        const int64_t at = (int64_t)t * p.H + r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = o[j] + (p.resid ? p.resid[at + j] : __bfloat162float(p.x[at + j]));
+            p.out[at + j] = __float2bfloat16_rn(v);
+            if (p.out32) p.out32[at + j] = v;
+        }
     }
 }
 
@@ -848,26 +815,21 @@ bool map_h(CUtensorMap* m, bool mx, const void* ptr, int64_t rows, int64_t cols)
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool MX, bool UP>
+template <bool MX>
 cudaError_t launch(const FewParams& p, int grid, cudaStream_t s) {
-    auto kern = moe_few_kernel<MX, UP>;
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MX, UP>(MAX_T));
+    auto kern = moe_few_kernel<MX>;
+    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MX>(MAX_T));
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes<MX, UP>(p.T);
+    cfg.dynamicSmemBytes = smem_bytes<MX>(p.T);
     cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = p.splits;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
     cfg.attrs = at;
-    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -879,9 +841,18 @@ int64_t few_h_bytes(bool mx, int64_t rows, int F) {
 
 }  // namespace
 
-int64_t moe_few_ws_bytes(bool mx, int T, int k, int F) {
+// Output tiles of H rows, and the CTAs that share one: as many as the SMs hold, no more than rows.
+static void few_shares(int T, int k, int H, int& tiles, int& shares) {
+    tiles = (H + TILE - 1) / TILE;
+    shares = std::max(1, std::min({MAX_SHARES, gemm_num_sms() / tiles, T * k}));
+}
+
+int64_t moe_few_ws_bytes(bool mx, int T, int k, int H, int F) {
     const int64_t rows = (int64_t)T * k;
-    return (int64_t)sizeof(Routing) + 256 + few_h_bytes(mx, rows, F) + (mx ? H_TERMS * rows * mx_scale_pitch(F) : 0);
+    int tiles, shares;
+    few_shares(T, k, H, tiles, shares);
+    return few_h_bytes(mx, rows, F) + (mx ? (H_TERMS * rows * mx_scale_pitch(F) + 255) / 256 * 256 : 0) +
+           (4ll * tiles + 255) / 256 * 256 + (shares > 1 ? (int64_t)tiles * shares * T * TILE * 4 : 0);
 }
 
 cudaError_t launch_moe_few(const MoeFewDesc& d, void* ws, uint32_t* err, cudaStream_t s) {
@@ -891,22 +862,26 @@ cudaError_t launch_moe_few(const MoeFewDesc& d, void* ws, uint32_t* err, cudaStr
     memset(&p, 0, sizeof(p));
     const int64_t rows = (int64_t)d.T * d.k;
     const int64_t up_pitch = d.mx ? mx_code_pitch(d.H) : 2ll * d.H, down_pitch = d.mx ? mx_code_pitch(d.F) : 2ll * d.F;
-    if (!map_experts(&p.map_p, d.mx, d.gate, up_pitch, d.F, d.E, d.gate_stride, UP_F) ||
-        !map_experts(&p.map_p2, d.mx, d.up, up_pitch, d.F, d.E, d.gate_stride, UP_F))
-        return cudaErrorInvalidValue;
-    p.scale_p = static_cast<const uint8_t*>(d.gate_scales);
-    p.scale_p2 = static_cast<const uint8_t*>(d.up_scales);
-    p.scale_stride = d.gate_scale_stride;
-    p.scale_pitch = (int)mx_scale_pitch(d.H);
+    p.gate_scale = static_cast<const uint8_t*>(d.gate_scales);
+    p.up_scale = static_cast<const uint8_t*>(d.up_scales);
+    p.down_scale = static_cast<const uint8_t*>(d.down_scales);
+    p.up_scale_stride = d.gate_scale_stride;
+    p.down_scale_stride = d.down_scale_stride;
+    p.up_scale_pitch = (int)mx_scale_pitch(d.H);
+    p.down_scale_pitch = p.h_scale_pitch = (int)mx_scale_pitch(d.F);
     p.x = static_cast<const __nv_bfloat16*>(d.x);
     p.resid = d.resid;
     p.logits = d.logits;
-    p.h = static_cast<uint8_t*>(ws);
-    p.tables = reinterpret_cast<Routing*>(p.h);
-    p.h += (sizeof(Routing) + 255) / 256 * 256;
-    p.h_scale = p.h + few_h_bytes(d.mx, rows, d.F);
     p.h_cols = few_h_cols(d.mx, d.F);
-    p.h_scale_pitch = (int)mx_scale_pitch(d.F);
+    few_shares(d.T, d.k, d.H, p.tiles, p.shares);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    p.h = w;
+    w += few_h_bytes(d.mx, rows, d.F);
+    p.h_scale = w;
+    w += d.mx ? (H_TERMS * rows * p.h_scale_pitch + 255) / 256 * 256 : 0;
+    p.tickets = reinterpret_cast<uint32_t*>(w);
+    w += (4ll * p.tiles + 255) / 256 * 256;
+    p.partial = reinterpret_cast<float*>(w);
     p.T = d.T;
     p.E = d.E;
     p.k = d.k;
@@ -915,25 +890,15 @@ cudaError_t launch_moe_few(const MoeFewDesc& d, void* ws, uint32_t* err, cudaStr
     p.out = static_cast<__nv_bfloat16*>(d.out);
     p.out32 = d.out32;
     p.err = err;
-    FewParams q = p;
-    if (!map_experts(&q.map_p, d.mx, d.down, down_pitch, d.H, d.E, d.down_stride, TILE) ||
-        !map_h(&q.map_p2, d.mx, p.h, rows, p.h_cols))
+    if (!map_experts(&p.gate, d.mx, d.gate, up_pitch, d.F, d.E, d.gate_stride, UP_F) ||
+        !map_experts(&p.up, d.mx, d.up, up_pitch, d.F, d.E, d.gate_stride, UP_F) ||
+        !map_experts(&p.down, d.mx, d.down, down_pitch, d.H, d.E, d.down_stride, TILE) ||
+        !map_h(&p.map_h, d.mx, p.h, rows, p.h_cols))
         return cudaErrorInvalidValue;
-    q.scale_p = static_cast<const uint8_t*>(d.down_scales);
-    q.scale_stride = d.down_scale_stride;
-    q.scale_pitch = (int)mx_scale_pitch(d.F);
-    const int sms = gemm_num_sms();
-    // up: at most rows x (h_cols / 64) units. Fewer than half the SMs: a cluster shares each along K
-    const int64_t units = rows * (p.h_cols / UP_F);
-    const int up_stages = (d.H + (d.mx ? 127 : 63)) / (d.mx ? 128 : 64);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_CLUSTER, sms / units, up_stages / 2}));
-    const int grid_up = (int)std::min<int64_t>(units * p.splits, sms);
-    // down: clusters of as many CTAs as the SMs hold, but no more than there are rows
-    const int tiles = (d.H + TILE - 1) / TILE;
-    q.splits = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_CLUSTER, sms / tiles, rows}));
-    cudaError_t e = d.mx ? launch<true, true>(p, grid_up, s) : launch<false, true>(p, grid_up, s);
-    if (e != cudaSuccess) return e;
-    return d.mx ? launch<true, false>(q, tiles * q.splits, s) : launch<false, false>(q, tiles * q.splits, s);
+    // no more CTAs than either phase can use: up has at most rows x (h_cols / 64) tiles
+    const int64_t most = std::max<int64_t>(rows * (p.h_cols / UP_F), (int64_t)p.tiles * p.shares);
+    const int grid = (int)std::min<int64_t>(most, gemm_num_sms());
+    return d.mx ? launch<true>(p, grid, s) : launch<false>(p, grid, s);
 }
 
 }  // namespace ls

@@ -136,7 +136,7 @@ ls_status lsk_moe_few(const void* x, const float* resid, const float* logits, co
     d.out = out;
     d.out32 = out32;
     Scratch ws((cudaStream_t)stream);
-    if (!ws.take(moe_few_ws_bytes(mx, T, k, F))) return LS_ERR_OOM;
+    if (!ws.take(moe_few_ws_bytes(mx, T, k, H, F))) return LS_ERR_OOM;
     return status_of(launch_moe_few(d, ws.p, entry_error_word(), (cudaStream_t)stream));
 }
 

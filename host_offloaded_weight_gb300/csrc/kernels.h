@@ -169,7 +169,7 @@ struct MoeFewDesc {
     void* out = nullptr;            // [T, H] bf16
     float* out32 = nullptr;         // [T, H], or NULL
 };
-int64_t moe_few_ws_bytes(bool mx, int T, int k, int F);
+int64_t moe_few_ws_bytes(bool mx, int T, int k, int H, int F);
 cudaError_t launch_moe_few(const MoeFewDesc& d, void* ws, uint32_t* err, cudaStream_t s);
 
 // ---------------------------------------------------------------- shared by the standalone entry points
