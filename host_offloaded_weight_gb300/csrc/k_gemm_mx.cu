@@ -53,21 +53,27 @@ struct Cfg {
     static constexpr int MAX_SPLIT = MODE == MX_MX ? 1 : TN == 8 ? 8 : TN <= 32 ? 4 : TN == 64 ? 2 : 1;
     static constexpr int RED_BYTES = (MAX_SPLIT - 1) * TN * TILE_P * 4;
     static constexpr int EPI_BYTES = MODE == MX_MX ? EPI_WARPS * 4096 : RED_BYTES;
-    static constexpr int FIT = (232448 - 1024 - 512 - EPI_BYTES) / STAGE;
-    static constexpr int STAGES = FIT < 10 ? FIT : 10;
+    // Up to 128 columns a stage's products are as short as an issuing warp's waits between them: two warps
+    // take the even and the odd stages, each with an accumulator of its own.
+    static constexpr int MMA_WARPS = MODE != MX_MX && BQ <= 128 ? 2 : 1;
+    static constexpr int FIT = (232448 - 1024 - 512 - EPI_BYTES) / STAGE, MOST = FIT < 10 ? FIT : 10;
+    // The scale warps work in teams that take turns of RUN stages. A wait by parity cannot tell a phase from the
+    // one two before it. Where one warp issues the products, stages are freed in order, and turns within a
+    // round of the ring are enough; where two do, each stage of the ring has a team of its own.
+    static constexpr int TEAM = MODE == ACT_IN ? 1 : 2;                     // warps of a team
+    static constexpr int TEAMS = MODE == ACT_IN ? MOST : 2;
+    static constexpr int RUN = MMA_WARPS == 2 ? 1 : 2;
+    static constexpr int STAGES = MOST / TEAMS * TEAMS;
+    static_assert(MMA_WARPS == 2 ? RUN == 1 && STAGES % TEAMS == 0 : TEAMS * RUN <= STAGES, "turns of the scale warps");
+    static constexpr int SCALE_WARPS = TEAM * TEAMS;
     static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024 + 512;
-    static constexpr int FIRST_EPI = MODE == ACT_IN ? 10 : 6;   // the first warp of the epilogue
-    static constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
-    static constexpr int ACCS = 2 * BQ + STAGES * QUADS * 4 * (1 + PARTS) <= 512 ? 2 : 1;
-    // The scale warps work in teams that take turns of RUN stages. A turn begins at most a round of the
-    // ring after the team's last one: a wait by parity cannot tell a phase from the one two before it.
-    static constexpr int SCALE_WARPS = MODE == ACT_IN ? 8 : 4;
-    static constexpr int TEAM = MODE == ACT_IN ? 1 : 2;         // warps of a team
-    static constexpr int TEAMS = SCALE_WARPS / TEAM;
-    static constexpr int RUN = MODE == ACT_IN ? 1 : 2;
-    static_assert(TEAMS * RUN <= STAGES, "a team's turns are within a round of the ring");
+    static constexpr int FIRST_EPI = 2 + SCALE_WARPS;            // the first warp of the epilogue
+    static constexpr int SECOND_MMA = FIRST_EPI + EPI_WARPS;
+    static constexpr int THREADS = 32 * (SECOND_MMA + MMA_WARPS - 1);
+    static constexpr int ACC = MMA_WARPS * BQ;  // columns of an accumulator
+    static constexpr int ACCS = 2 * ACC + STAGES * QUADS * 4 * (1 + PARTS) <= 512 ? 2 : 1;
     static constexpr int SCALE_COLS = QUADS * 4 * (1 + PARTS);  // TMEM columns of a stage's scales
-    static_assert(ACCS * BQ + STAGES * SCALE_COLS <= 512, "tensor memory");
+    static_assert(ACCS * ACC + STAGES * SCALE_COLS <= 512, "tensor memory");
     static_assert(BQ % 16 == 0 && BQ <= 256, "columns of a product");
 };
 
@@ -142,6 +148,25 @@ template <> struct Words<4> { typedef uint32_t type; };
 template <> struct Words<8> { typedef uint2 type; };
 template <> struct Words<16> { typedef uint4 type; };
 
+// A row's sums for tokens j0 to j0 + 7 of a tile of ks stages: the smaller terms first, of even and odd stages.
+template <int MODE, int BQ>
+__device__ __forceinline__ void token_sums(uint32_t t, int j0, int ks, float (&v)[8]) {
+    using C = Cfg<MODE, BQ>;
+    constexpr int N = C::MMA_WARPS;
+    uint32_t x[N][8], y[N][8];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        tmem_load8(t + i * BQ + j0, x[i]);
+        tmem_load8(t + i * BQ + C::TN + j0, y[i]);
+    }
+    tmem_load_wait();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j] = __uint_as_float(y[0][j]) + (N > 1 && ks > 1 ? __uint_as_float(y[N - 1][j]) : 0.f);
+        v[j] += __uint_as_float(x[0][j]) + (N > 1 && ks > 1 ? __uint_as_float(x[N - 1][j]) : 0.f);
+    }
+}
+
 // A warp's 32 x 32 of the result, lane l with row r0 + l: turned through shared memory (float4
 // columns, exclusive-or swizzled by the row) so that eight lanes write a row's 32 columns.
 __device__ __forceinline__ void store_chunk(const MxParams& p, float4* buf, const uint32_t (&v)[32], int r0, int col0) {
@@ -202,10 +227,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             bar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            bar_init(acc_full(b), 1);
+            bar_init(acc_full(b), C::MMA_WARPS);
             bar_init(acc_empty(b), C::EPI_WARPS);
         }
-        bar_init(done, 1);
+        bar_init(done, C::MMA_WARPS);
         bar_init_fence();
         tma_desc_prefetch(&p.map_p);
         if (MODE != ACT_IN) tma_desc_prefetch(&p.map_q);
@@ -279,13 +304,13 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                 const int last = it - 1 - (it - 1 - i) % S;
                 bar_wait(full(i), (uint32_t)(last / S) & 1u, p.err, 5);
             }
-    } else if (warp == 1) {
+    } else if (warp == 1 || (C::MMA_WARPS == 2 && warp == C::SECOND_MMA)) {
         // ------------------------------------------------------------ products
         constexpr uint32_t IDESC = MODE == MX_MX ? mx_idesc(1, 1, TILE_P, BQ) : mx_idesc(5, 0, TILE_P, BQ);
         const bool one = elect_one();
-        int s = 0, n = 0;
-        uint32_t phase = 0;
-        bool ok = true, ready = false;  // ready: the next stage's barrier, asked before this stage's products
+        const int odd = warp == 1 ? 0 : 1;
+        int n = 0, it = 0;
+        bool ok = true, ready = false;  // ready (one warp): the next stage's barrier, asked before this stage's products
         while (ok && w.next()) {
             const int b = n % C::ACCS;
             if (!bar_wait_warp(acc_empty(b), (uint32_t)(n / C::ACCS + 1) & 1u, p.err, 2) || stop) {
@@ -293,21 +318,18 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                 break;
             }
             fence_after_sync();
-            const uint32_t d = tmem + (uint32_t)(b * BQ);
-            for (int k = w.k0; k < w.k1; ++k) {
-                if (!__all_sync(0xffffffffu, ready) && !bar_wait_warp(full(s), phase, p.err, 3)) {
+            const uint32_t d = tmem + (uint32_t)(b * C::ACC + odd * BQ);
+            for (int k = w.k0 + odd; k < w.k1; k += C::MMA_WARPS) {
+                const int i = it + k - w.k0, s = i % S;
+                if (!__all_sync(0xffffffffu, ready) && !bar_wait_warp(full(s), (uint32_t)(i / S) & 1u, p.err, 3)) {
                     ok = false;
                     stop = 1;
                     break;
                 }
                 fence_after_sync();
-                const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES, freed = empty(s);
-                const uint32_t tp = tmem + (uint32_t)(C::ACCS * BQ + s * C::SCALE_COLS), tq = tp + 4 * C::QUADS;
-                if (++s == S) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-                ready = bar_test(full(s), phase);
+                const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
+                const uint32_t tp = tmem + (uint32_t)(C::ACCS * C::ACC + s * C::SCALE_COLS), tq = tp + 4 * C::QUADS;
+                if (C::MMA_WARPS == 1) ready = bar_test(full((i + 1) % S), (uint32_t)((i + 1) / S) & 1u);
                 if (one) {
 #pragma unroll
                     for (int q = 0; q < C::QUADS; ++q) {
@@ -317,22 +339,23 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                             scale_copy(tq + 4 * (q * C::PARTS + j), scale_desc(sc + 512 * (C::QUADS + q * C::PARTS + j)));
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // 32 bytes of each row
-                        const uint32_t acc = (k > w.k0 || i > 0) ? 1u : 0u;
-                        const uint64_t dp = operand_desc(sp + 32 * i), dq = operand_desc(sq + 32 * i);
+                    for (int j = 0; j < 4; ++j) {  // 32 bytes of each row
+                        const uint32_t acc = (k > w.k0 + odd || j > 0) ? 1u : 0u;
+                        const uint64_t dp = operand_desc(sp + 32 * j), dq = operand_desc(sq + 32 * j);
                         if (MODE == MX_MX)
-                            mma_mxf4(d, dp, dq, idesc_at(IDESC, 2 * (i & 1)), tp + 4 * (i >> 1),
-                                     tq + 4 * C::PARTS * (i >> 1), acc);
+                            mma_mxf4(d, dp, dq, idesc_at(IDESC, 2 * (j & 1)), tp + 4 * (j >> 1),
+                                     tq + 4 * C::PARTS * (j >> 1), acc);
                         else
-                            mma_mxf8(d, dp, dq, idesc_at(IDESC, i), tp, tq, acc);
+                            mma_mxf8(d, dp, dq, idesc_at(IDESC, j), tp, tq, acc);
                     }
-                    mma_commit(freed);
+                    mma_commit(empty(s));
                 }
                 __syncwarp();
             }
             if (ok && one) mma_commit(acc_full(b));
             __syncwarp();
             ++n;
+            it += w.k1 - w.k0;
         }
         if (one) mma_commit(done);
         __syncwarp();
@@ -340,12 +363,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
     } else if (warp < C::FIRST_EPI) {
         // ------------------------------------------------------------ scales (and ACT_IN: the rows)
         // Teams take turns, so that the latencies of several stages' waits, stores and fences
-        // overlap; a team requests its next turn's scales (ACT_IN: of two turns) before it starts one. A
+        // overlap; a team requests later turns' scales before it starts one. A
         // team's warps share the rows: of each 128, lane l has rows l + 32 j, whose words lie side by
         // side at 16 l in the order that the tensor core reads.
         constexpr int RUN = C::RUN, TEAMS = C::TEAMS, RPW = 4 / C::TEAM;   // rows of a warp, of each 128
         constexpr int NR = RPW * (MODE == ACT_IN ? 1 : 1 + C::PARTS);
-        constexpr int AHEAD = MODE == ACT_IN ? 2 : 1;
+        constexpr int AHEAD = MODE == ACT && RUN == 1 ? 3 : 1;             // turns requested ahead
         constexpr int U = MODE == ACT_IN ? C::TN / 2 : 1;                  // ACT_IN: units of 8 values a lane
         typedef typename Words<4 * C::QUADS * RUN>::type V;
         const int team = (warp - 2) / C::TEAM, first = RPW * ((warp - 2) % C::TEAM);
@@ -391,8 +414,13 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         int none = 0;
         step(tile, u, it0, team);
         step(f_tile, f_u, none, team);
-        if (MODE == ACT) {
-            fetch(v[0], x[0], f_tile, f_u, 0, RPW);
+        if (MODE == ACT) {  // the weights' scales need not wait for the split rows
+            int t = f_tile, turn = f_u;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                fetch(v[i], x[i], t, turn, 0, RPW);
+                step(t, turn, none, TEAMS);
+            }
             grid_wait();
         }
 #pragma unroll
@@ -408,7 +436,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             for (int i = 0; i < RUN; ++i) {
                 if (!ok || u * RUN + i >= stages) continue;
                 const int it = it0 + u * RUN + i, s = it % S;
-                if (!__all_sync(0xffffffffu, bar_wait(empty(s), (uint32_t)(it / S + 1) & 1u, p.err, 7))) {
+                if (!bar_wait_warp(empty(s), (uint32_t)(it / S + 1) & 1u, p.err, 7)) {
                     ok = false;
                     stop = 1;
                     continue;
@@ -457,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             }
             step(tile, u, it0, TEAMS);
         }
-    } else {
+    } else if (warp < C::SECOND_MMA) {
         // ------------------------------------------------------------ results
         const int q = warp & 3;  // the TMEM lane quarter that this warp can read
         int n = 0;
@@ -470,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                 break;
             }
             fence_after_sync();
-            const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BQ);
+            const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC);
             if (MODE == MX_MX) {
                 float4* buf = reinterpret_cast<float4*>(gbase + S * C::STAGE) + (warp - C::FIRST_EPI) * 256;
                 const int r0 = row_p + q * 32;
@@ -491,13 +519,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                 if (p.splits == 1 || slice) {
 #pragma unroll 1
                     for (int j0 = 0; j0 < tokens; j0 += 8) {
-                        uint32_t x[8], y[8];
-                        tmem_load8(t + j0, x);
-                        tmem_load8(t + C::TN + j0, y);
-                        tmem_load_wait();
+                        float sum[8];
+                        token_sums<MODE, BQ>(t, j0, w.k1 - w.k0, sum);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float v = __uint_as_float(x[j]) + __uint_as_float(y[j]);
+                            const float v = sum[j];
                             if (slice) st_cluster(red + ((j0 + j) * TILE_P + row) * 4, v);
                             else if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
                         }
@@ -513,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
     if (MODE != MX_MX && p.splits > 1) {
         __syncwarp();
         cluster_barrier();  // every CTA's sums are in the first one's memory; the sum runs in CTA order
-        if (blockIdx.x % p.splits == 0 && warp >= C::FIRST_EPI) {
+        if (blockIdx.x % p.splits == 0 && warp >= C::FIRST_EPI && warp < C::SECOND_MMA) {
             fence_after_sync();
             int row_p, row_q;
             tile_at<MODE, BQ>(p, blockIdx.x / p.splits, row_p, row_q);
@@ -523,13 +549,11 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             const uint32_t t = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
             for (int j0 = 0; j0 < tokens; j0 += 8) {
-                uint32_t x[8], y[8];
-                tmem_load8(t + j0, x);
-                tmem_load8(t + C::TN + j0, y);
-                tmem_load_wait();
+                float sum[8];
+                token_sums<MODE, BQ>(t, j0, w.k1 - w.k0, sum);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    float v = __uint_as_float(x[j]) + __uint_as_float(y[j]);
+                    float v = sum[j];
                     for (int i = 0; i < p.splits - 1; ++i) v += red[(i * C::TN + j0 + j) * TILE_P];
                     if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
                 }

@@ -21,7 +21,9 @@
 // every time, and no atomics on data.
 //
 // Warp 0 loads the weights by TMA into the ring, warps 2-9 take turns at the stages and add the
-// block scales and (up) the tokens' rows, warp 1 issues the products, warps 10-13 take the results.
+// block scales and (up) the tokens' rows, warps 1 and 14 issue the products of even and odd stages into
+// accumulators of their own (one warp alone took 385 clocks a stage of 240 clocks of products, between its
+// waits; the memory brings a stage in 370), warps 10-13 take the results.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -40,7 +42,8 @@ constexpr int TOK = 8;            // tokens of an expert that one pass over its 
 constexpr int TILE = 128;         // weight rows of a tile
 constexpr int UP_F = TILE / 2;    // columns of h of a tile of the up kernel
 constexpr int FEED_WARPS = 8, FIRST_EPI = 2 + FEED_WARPS;
-constexpr int THREADS = 32 * (FIRST_EPI + 4);
+constexpr int SECOND_MMA = FIRST_EPI + 4;  // the warp that issues the products of odd stages
+constexpr int THREADS = 32 * (SECOND_MMA + 1);
 constexpr int P_BYTES = TILE * 128;
 constexpr int X_TERMS = 2, H_TERMS = 3;  // E4M3 terms of x and of h (MXFP4 experts)
 
@@ -49,12 +52,13 @@ struct Cfg {
     static constexpr int Q_ROWS = MX ? 32 : 16;                        // columns of the widest product
     static constexpr int Q_BYTES = Q_ROWS * 128;
     static constexpr int STAGE = P_BYTES + Q_BYTES + 1024;             // and 1 KB of scales
-    static constexpr int STAGES = MX ? 8 : 9;
-    static_assert(2 * Q_ROWS + STAGES * 8 <= 128, "tensor memory: two accumulators, and each stage's scales");
-    // a wait by parity cannot tell a phase from the one two before it
-    static_assert(FEED_WARPS <= STAGES, "a feed warp's turns are within a round of the ring");
+    static constexpr int STAGES = 8;
+    static_assert(4 * Q_ROWS + STAGES * 8 <= 256, "tensor memory: two pairs of accumulators, and each stage's scales");
+    // A wait by parity cannot tell a phase from the one two before it, and stages are freed in any order (even and
+    // odd ones by different warps). A feed warp that always has the same stages of the ring has waited for each phase before.
+    static_assert(STAGES % FEED_WARPS == 0, "a stage of the ring has one feed warp");
 };
-constexpr int MAX_STAGES = 9, TMEM_COLS = 128;
+constexpr int MAX_STAGES = 8, TMEM_COLS = 256;
 constexpr int MAX_SHARES = 32;    // CTAs that share an output tile
 
 struct FewParams {
@@ -400,10 +404,10 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
             bar_init(empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
-            bar_init(acc_full0 + 8 * b, 1);
+            bar_init(acc_full0 + 8 * b, 2);  // both product warps
             bar_init(acc_empty0 + 8 * b, 4);
         }
-        bar_init(done, 1);
+        bar_init(done, 2);
         bar_init_fence();
         tma_desc_prefetch(&p.gate);
         tma_desc_prefetch(&p.up);
@@ -441,9 +445,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     const bool one = elect_one();
 
     // ---- state of the roles across the meeting
-    int s = 0;
-    uint32_t phase = warp == 0 ? 1u : 0u;  // for the producer a new barrier's preceding phase counts as complete
-    bool ok = true, ready = false;
+    int s = 0;  // the producer's next stage
+    uint32_t phase = 1;  // a new barrier's preceding phase counts as complete
+    bool ok = true;
     int acc = 0;                            // accumulators used so far
     auto next_stage = [&] {
         if (++s == STAGES) {
@@ -484,8 +488,10 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
         }
         return ok;
     };
-    auto products = [&](const Line& line, uint32_t idesc) {
-        for (int u = 0; ok && u < line.units; ++u, ++acc) {
+    // stages `first` on: those of a unit with an even or odd number are this warp's
+    auto products = [&](const Line& line, int first, uint32_t idesc) {
+        const int odd = warp == 1 ? 0 : 1;
+        for (int u = 0; ok && u < line.units; ++u, ++acc, first += line.ks) {
             const int b = acc & 1;
             if (!bar_wait_warp(acc_empty0 + 8 * b, (uint32_t)((acc >> 1) + 1) & 1u, p.err, 2) || stop) {
                 ok = false;
@@ -493,30 +499,29 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
                 break;
             }
             fence_after_sync();
-            const uint32_t d = tmem + (uint32_t)(b * C::Q_ROWS);
-            for (int k = 0; k < line.ks; ++k) {
-                if (!__all_sync(0xffffffffu, ready) && !bar_wait_warp(full0 + 8 * s, phase, p.err, 3)) {
+            const uint32_t d = tmem + (uint32_t)((2 * b + odd) * C::Q_ROWS);
+            for (int k = odd; k < line.ks; k += 2) {
+                const int i = first + k, st = i % STAGES;
+                if (!bar_wait_warp(full0 + 8 * st, (uint32_t)(i / STAGES) & 1u, p.err, 3)) {
                     ok = false;
                     stop = 1;
                     break;
                 }
                 fence_after_sync();
-                const uint32_t sp = base + s * STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
-                const uint32_t tp = tmem + (uint32_t)(2 * C::Q_ROWS + s * 8), freed = empty0 + 8 * s;
-                next_stage();
-                ready = bar_test(full0 + 8 * s, phase);  // asked before this stage's products
+                const uint32_t sp = base + st * STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
+                const uint32_t tp = tmem + (uint32_t)(4 * C::Q_ROWS + st * 8);
                 if (one) {
                     if (MX) {
                         scale_copy(tp, scale_desc(sc));
                         scale_copy(tp + 4, scale_desc(sc + 512));
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // 32 bytes of each row
-                        const uint32_t add = (k > 0 || i > 0) ? 1u : 0u;
-                        if (MX) mma_mxf8(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), idesc_at(idesc, i), tp, tp + 4, add);
-                        else mma_bf16(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), idesc, add);
+                    for (int j = 0; j < 4; ++j) {  // 32 bytes of each row
+                        const uint32_t add = (k > odd || j > 0) ? 1u : 0u;
+                        if (MX) mma_mxf8(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc_at(idesc, j), tp, tp + 4, add);
+                        else mma_bf16(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc, add);
                     }
-                    mma_commit(freed);
+                    mma_commit(empty0 + 8 * st);
                 }
                 __syncwarp();
             }
@@ -577,16 +582,19 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     };
     const int q = warp & 3, row = q * 32 + lane;  // the epilogue: the TMEM lane quarter that a warp can read
     bool bad = false;                              // a wait ran out: no later one is made, and the results are void
-    auto take = [&](float (&v)[TOK], int terms) {
+    auto take = [&](float (&v)[TOK], int terms, int ks) {
         const int b = acc & 1;
-        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + b * C::Q_ROWS;
+        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + 2 * b * C::Q_ROWS;
         if (!bad) bad = !bar_wait_warp(acc_full0 + 8 * b, (uint32_t)(acc >> 1) & 1u, p.err, 4);
         if (bad) stop = 1;
         fence_after_sync();
-        uint32_t x[H_TERMS][8];
+        uint32_t x[H_TERMS][8], y[H_TERMS][8];
 #pragma unroll
         for (int i = 0; i < H_TERMS; ++i)
-            if (i < terms) tmem_load8(t + i * TOK, x[i]);
+            if (i < terms) {
+                tmem_load8(t + i * TOK, x[i]);
+                tmem_load8(t + C::Q_ROWS + i * TOK, y[i]);
+            }
         tmem_load_wait();
         fence_before_sync();
         __syncwarp();
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
             v[j] = 0.f;
 #pragma unroll
             for (int i = H_TERMS - 1; i >= 0; --i)  // the smallest first
-                if (i < terms) v[j] += __uint_as_float(x[i][j]);
+                if (i < terms) v[j] += __uint_as_float(x[i][j]) + (ks > 1 ? __uint_as_float(y[i][j]) : 0.f);
         }
     };
 
@@ -616,8 +624,8 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
             __syncwarp();
             next_stage();
         }
-    } else if (warp == 1) {
-        products(up, MX ? mx_idesc(5, 0, TILE, 16) : bf16_idesc(TILE, 16));
+    } else if (warp == 1 || warp == SECOND_MMA) {
+        products(up, 0, MX ? mx_idesc(5, 0, TILE, 16) : bf16_idesc(TILE, 16));
     } else if (warp < FIRST_EPI) {
         // a turn is every eighth stage; the next turn's data are requested before this one's work
         Turn nxt;
@@ -658,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     } else {
         for (int u = 0; u < up.units; ++u) {
             float v[TOK];
-            take(v, MX ? X_TERMS : 1);
+            take(v, MX ? X_TERMS : 1, up.ks);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) sm.turn[row][j] = v[j];
             asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -694,8 +702,8 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
                 const int last = it - 1 - (it - 1 - i) % STAGES;
                 bar_wait(full0 + 8 * i, (uint32_t)(last / STAGES) & 1u, p.err, 5);
             }
-    } else if (warp == 1) {
-        products(down, MX ? mx_idesc(5, 0, TILE, 32) : bf16_idesc(TILE, 16));
+    } else if (warp == 1 || warp == SECOND_MMA) {
+        products(down, base_it, MX ? mx_idesc(5, 0, TILE, 32) : bf16_idesc(TILE, 16));
         if (one) mma_commit(done);
         __syncwarp();
         bar_wait(done, 0, p.err, 6);
@@ -717,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     } else {
         for (int u = 0; u < down.units; ++u) {
             float v[TOK];
-            take(v, MX ? H_TERMS : 1);
+            take(v, MX ? H_TERMS : 1, down.ks);
             const int chunk = down_chunk(u), n = rt.chunk_n[chunk], row0 = rt.chunk_row[chunk];
 #pragma unroll
             for (int j = 0; j < TOK; ++j)
