@@ -59,12 +59,13 @@ struct Cfg {
     static constexpr int FIT = (232448 - 1024 - 512 - EPI_BYTES) / STAGE, MOST = FIT < 10 ? FIT : 10;
     // The scale warps work in teams that take turns of RUN stages. A wait by parity cannot tell a phase from the
     // one two before it. Where one warp issues the products, stages are freed in order, and turns within a
-    // round of the ring are enough; where two do, each stage of the ring has a team of its own.
+    // round of the ring are enough; where two do, each place in the ring has a team and a product warp of its own.
     static constexpr int TEAM = MODE == ACT_IN ? 1 : 2;                     // warps of a team
-    static constexpr int TEAMS = MODE == ACT_IN ? MOST : 2;
+    static constexpr int TEAMS = MODE == ACT_IN ? MOST / 2 * 2 : 2;
     static constexpr int RUN = MMA_WARPS == 2 ? 1 : 2;
     static constexpr int STAGES = MOST / TEAMS * TEAMS;
-    static_assert(MMA_WARPS == 2 ? RUN == 1 && STAGES % TEAMS == 0 : TEAMS * RUN <= STAGES, "turns of the scale warps");
+    static_assert(MMA_WARPS == 2 ? RUN == 1 && STAGES % TEAMS == 0 && STAGES % 2 == 0 : TEAMS * RUN <= STAGES,
+                  "turns of the scale and the product warps");
     static constexpr int SCALE_WARPS = TEAM * TEAMS;
     static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024 + 512;
     static constexpr int FIRST_EPI = 2 + SCALE_WARPS;            // the first warp of the epilogue
@@ -148,9 +149,9 @@ template <> struct Words<4> { typedef uint32_t type; };
 template <> struct Words<8> { typedef uint2 type; };
 template <> struct Words<16> { typedef uint4 type; };
 
-// A row's sums for tokens j0 to j0 + 7 of a tile of ks stages: the smaller terms first, of even and odd stages.
+// A row's sums for tokens j0 to j0 + 7 of a tile of ks stages, `first` on: the smaller terms first, of even and odd stages.
 template <int MODE, int BQ>
-__device__ __forceinline__ void token_sums(uint32_t t, int j0, int ks, float (&v)[8]) {
+__device__ __forceinline__ void token_sums(uint32_t t, int j0, int first, int ks, float (&v)[8]) {
     using C = Cfg<MODE, BQ>;
     constexpr int N = C::MMA_WARPS;
     uint32_t x[N][8], y[N][8];
@@ -162,8 +163,10 @@ __device__ __forceinline__ void token_sums(uint32_t t, int j0, int ks, float (&v
     tmem_load_wait();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        v[j] = __uint_as_float(y[0][j]) + (N > 1 && ks > 1 ? __uint_as_float(y[N - 1][j]) : 0.f);
-        v[j] += __uint_as_float(x[0][j]) + (N > 1 && ks > 1 ? __uint_as_float(x[N - 1][j]) : 0.f);
+        const float x0 = __uint_as_float(x[0][j]), x1 = __uint_as_float(x[N - 1][j]);
+        const float y0 = __uint_as_float(y[0][j]), y1 = __uint_as_float(y[N - 1][j]);
+        if (N == 1) v[j] = y0 + x0;
+        else v[j] = ks > 1 ? (y0 + y1) + (x0 + x1) : first & 1 ? y1 + x1 : y0 + x0;
     }
 }
 
@@ -319,8 +322,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             }
             fence_after_sync();
             const uint32_t d = tmem + (uint32_t)(b * C::ACC + odd * BQ);
-            for (int k = w.k0 + odd; k < w.k1; k += C::MMA_WARPS) {
-                const int i = it + k - w.k0, s = i % S;
+            uint32_t add = 0;
+            const int end = it + w.k1 - w.k0;  // with two warps, this one's are the even or the odd stages of the ring's line
+            for (int i = C::MMA_WARPS == 2 ? it + ((it ^ odd) & 1) : it; i < end; i += C::MMA_WARPS) {
+                const int s = i % S;
                 if (!__all_sync(0xffffffffu, ready) && !bar_wait_warp(full(s), (uint32_t)(i / S) & 1u, p.err, 3)) {
                     ok = false;
                     stop = 1;
@@ -340,22 +345,22 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {  // 32 bytes of each row
-                        const uint32_t acc = (k > w.k0 + odd || j > 0) ? 1u : 0u;
                         const uint64_t dp = operand_desc(sp + 32 * j), dq = operand_desc(sq + 32 * j);
                         if (MODE == MX_MX)
                             mma_mxf4(d, dp, dq, idesc_at(IDESC, 2 * (j & 1)), tp + 4 * (j >> 1),
-                                     tq + 4 * C::PARTS * (j >> 1), acc);
+                                     tq + 4 * C::PARTS * (j >> 1), j ? 1u : add);
                         else
-                            mma_mxf8(d, dp, dq, idesc_at(IDESC, j), tp, tq, acc);
+                            mma_mxf8(d, dp, dq, idesc_at(IDESC, j), tp, tq, j ? 1u : add);
                     }
                     mma_commit(empty(s));
                 }
                 __syncwarp();
+                add = 1;
             }
             if (ok && one) mma_commit(acc_full(b));
             __syncwarp();
             ++n;
-            it += w.k1 - w.k0;
+            it = end;
         }
         if (one) mma_commit(done);
         __syncwarp();
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
 #pragma unroll 1
                     for (int j0 = 0; j0 < tokens; j0 += 8) {
                         float sum[8];
-                        token_sums<MODE, BQ>(t, j0, w.k1 - w.k0, sum);
+                        token_sums<MODE, BQ>(t, j0, n * (w.k1 - w.k0), w.k1 - w.k0, sum);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float v = sum[j];
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
 #pragma unroll 1
             for (int j0 = 0; j0 < tokens; j0 += 8) {
                 float sum[8];
-                token_sums<MODE, BQ>(t, j0, w.k1 - w.k0, sum);
+                token_sums<MODE, BQ>(t, j0, 0, w.k1 - w.k0, sum);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float v = sum[j];

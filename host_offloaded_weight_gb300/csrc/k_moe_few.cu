@@ -17,7 +17,7 @@
 // up, meets the others once, and takes a tile of 128 output rows for its share of the experts. Across the
 // meeting the ring of stages goes on: the first weights of down are requested before it. (As two
 // launches the second one's start, routing and first loads cost 8 us of 18 at one token.) The CTAs of a tile add
-// their sums through memory, the last one to finish in the order of the CTAs: the same bits
+// their sums through memory, each a part of the outputs, in the order of the CTAs: the same bits
 // every time, and no atomics on data.
 //
 // Warp 0 loads the weights by TMA into the ring, warps 2-9 take turns at the stages and add the
@@ -56,7 +56,7 @@ struct Cfg {
     static_assert(4 * Q_ROWS + STAGES * 8 <= 256, "tensor memory: two pairs of accumulators, and each stage's scales");
     // A wait by parity cannot tell a phase from the one two before it, and stages are freed in any order (even and
     // odd ones by different warps). A feed warp that always has the same stages of the ring has waited for each phase before.
-    static_assert(STAGES % FEED_WARPS == 0, "a stage of the ring has one feed warp");
+    static_assert(STAGES % FEED_WARPS == 0 && STAGES % 2 == 0, "a stage of the ring has one feed warp and one product warp");
 };
 constexpr int MAX_STAGES = 8, TMEM_COLS = 256;
 constexpr int MAX_SHARES = 32;    // CTAs that share an output tile
@@ -323,7 +323,7 @@ __device__ __forceinline__ void route(Routing& r, const FewParams& p, int warp, 
 // ------------------------------------------------------------------ the kernel
 struct alignas(16) Smem {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], done;
-    uint32_t tmem, last;
+    uint32_t tmem, met;
     float turn[TILE][TOK + 1];  // a tile's sums, on their way to the threads that make h
     Routing r;
 };
@@ -395,7 +395,10 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     const uint32_t full0 = smem_addr(sm.full), empty0 = smem_addr(sm.empty), acc_full0 = smem_addr(sm.acc_full),
                    acc_empty0 = smem_addr(sm.acc_empty), done = smem_addr(&sm.done);
     __shared__ volatile int stop;
-    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    // Thread 0 waits for the other CTAs at the meeting and can come back from it apart from its warp. A copy issued
+    // under elect_one() by a warp in two parts is issued twice, so the first four warps are the epilogue's.
+    const int hw_warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int warp = hw_warp < 4 ? FIRST_EPI + hw_warp : hw_warp < SECOND_MMA ? hw_warp - 4 : SECOND_MMA;
 
     if (threadIdx.x == 0) {
         stop = 0;
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
         for (int i = threadIdx.x; i < p.tiles; i += THREADS) p.tickets[i] = 0;
     fence_before_sync();
     grid_wait();
-    route(rt, p, warp, lane);  // begins and ends with a barrier of the CTA
+    route(rt, p, hw_warp, lane);  // begins and ends with a barrier of the CTA
     fence_after_sync();
     const uint32_t tmem = sm.tmem;
 
@@ -463,23 +466,34 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
 
     // ---- the roles' parts of a phase
     constexpr uint32_t P_COUNT = MX ? P_BYTES / 2 : P_BYTES;  // an unpacking copy counts the packed bytes
-    auto load_up = [&](int unit, int k) {
-        const int chunk = unit / n_f, e = rt.chunk_e[chunk], f0 = unit % n_f * UP_F;
+    auto load_up = [&](int e, int f0, int k) {
         const uint32_t at = base + s * STAGE, bar = full0 + 8 * s;
         bar_expect(bar, P_COUNT);
         tma_3d(at, &p.gate, bar, k * KV, f0, e);
         tma_3d(at + P_BYTES / 2, &p.up, bar, k * KV, f0, e);
     };
-    auto load_down = [&](int u, int k) {
+    // the producer's place in down; what a unit needs is looked up once (an integer division of
+    // this hardware is as long as a copy's issue)
+    struct Place {
+        int u, k, e, row, h_row;
+    };
+    auto place = [&](int u) {
+        const int chunk = down_chunk(u);
+        return Place{u, 0, rt.chunk_e[chunk], down_tile(u) * TILE, rt.chunk_row[chunk]};
+    };
+    auto advance = [&](Place& at) {
+        if (++at.k == down.ks && at.u + 1 < down.units) at = place(at.u + 1);
+    };
+    auto load_down = [&](const Place& from) {
         const uint32_t bar = full0 + 8 * s;
         bar_expect(bar, P_COUNT + (MX ? H_TERMS : 1) * TOK * 128);
         if (!MX) bar_arrive(bar);  // no feed warp has anything to add
-        tma_3d(base + s * STAGE, &p.down, bar, k * KV, down_tile(u) * TILE, rt.chunk_e[down_chunk(u)]);
+        tma_3d(base + s * STAGE, &p.down, bar, from.k * KV, from.row, from.e);
     };
-    auto load_h = [&](int st, int u, int k) {
+    auto load_h = [&](int st, const Place& from) {
         const uint32_t at = base + st * STAGE + P_BYTES, bar = full0 + 8 * st;
-        if (MX) tma_3d(at, &p.map_h, bar, k * KV, rt.chunk_row[down_chunk(u)], 0);
-        else tma_2d(at, &p.map_h, bar, k * KV, rt.chunk_row[down_chunk(u)]);
+        if (MX) tma_3d(at, &p.map_h, bar, from.k * KV, from.h_row, 0);
+        else tma_2d(at, &p.map_h, bar, from.k * KV, from.h_row);
     };
     auto wait_empty = [&] {
         if (ok && !bar_wait_warp(empty0 + 8 * s, phase, p.err, 1)) {
@@ -488,7 +502,8 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
         }
         return ok;
     };
-    // stages `first` on: those of a unit with an even or odd number are this warp's
+    // Stages `first` on of the ring's line: this warp's are the even or the odd ones, so that a place in the ring is
+    // always the same warp's (its wait by parity for a round follows its wait for the round before).
     auto products = [&](const Line& line, int first, uint32_t idesc) {
         const int odd = warp == 1 ? 0 : 1;
         for (int u = 0; ok && u < line.units; ++u, ++acc, first += line.ks) {
@@ -500,8 +515,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
             }
             fence_after_sync();
             const uint32_t d = tmem + (uint32_t)((2 * b + odd) * C::Q_ROWS);
-            for (int k = odd; k < line.ks; k += 2) {
-                const int i = first + k, st = i % STAGES;
+            uint32_t add = 0;
+            for (int i = first + ((first ^ odd) & 1); i < first + line.ks; i += 2) {
+                const int st = i % STAGES;
                 if (!bar_wait_warp(full0 + 8 * st, (uint32_t)(i / STAGES) & 1u, p.err, 3)) {
                     ok = false;
                     stop = 1;
@@ -517,13 +533,13 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {  // 32 bytes of each row
-                        const uint32_t add = (k > odd || j > 0) ? 1u : 0u;
-                        if (MX) mma_mxf8(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc_at(idesc, j), tp, tp + 4, add);
-                        else mma_bf16(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc, add);
+                        if (MX) mma_mxf8(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc_at(idesc, j), tp, tp + 4, j ? 1u : add);
+                        else mma_bf16(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc, j ? 1u : add);
                     }
                     mma_commit(empty0 + 8 * st);
                 }
                 __syncwarp();
+                add = 1;
             }
             if (ok && one) mma_commit(acc_full0 + 8 * b);
             __syncwarp();
@@ -580,9 +596,10 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) bar_arrive(full0 + 8 * (it % STAGES));
     };
-    const int q = warp & 3, row = q * 32 + lane;  // the epilogue: the TMEM lane quarter that a warp can read
+    const int q = hw_warp, row = q * 32 + lane;  // the epilogue: the TMEM lane quarter that a warp can read
     bool bad = false;                              // a wait ran out: no later one is made, and the results are void
-    auto take = [&](float (&v)[TOK], int terms, int ks) {
+    // the sums of a unit of ks stages, `first` on
+    auto take = [&](float (&v)[TOK], int terms, int first, int ks) {
         const int b = acc & 1;
         const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + 2 * b * C::Q_ROWS;
         if (!bad) bad = !bar_wait_warp(acc_full0 + 8 * b, (uint32_t)(acc >> 1) & 1u, p.err, 4);
@@ -605,23 +622,31 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
             v[j] = 0.f;
 #pragma unroll
             for (int i = H_TERMS - 1; i >= 0; --i)  // the smallest first
-                if (i < terms) v[j] += __uint_as_float(x[i][j]) + (ks > 1 ? __uint_as_float(y[i][j]) : 0.f);
+                if (i < terms) {
+                    const float even = __uint_as_float(x[i][j]), odd = __uint_as_float(y[i][j]);
+                    v[j] += ks > 1 ? even + odd : first & 1 ? odd : even;
+                }
         }
     };
 
     // ---- up
     int it = 0;     // the producer's stages so far
     int ahead = 0;  // stages of down whose weights are requested before the meeting
+    Place w_at{}, h_at{};
     if (warp == 0) {
-        for (int u = 0; ok && u < up.units; ++u)
+        for (int u = 0; ok && u < up.units; ++u) {
+            const int unit = up.unit(u), e = rt.chunk_e[unit / n_f], f0 = unit % n_f * UP_F;
             for (int k = 0; k < up.ks && wait_empty(); ++k, ++it) {
-                if (one) load_up(up.unit(u), k);
+                if (one) load_up(e, f0, k);
                 __syncwarp();
                 next_stage();
             }
+        }
+        if (down.units) w_at = h_at = place(0);
         for (; ahead < min(STAGES, down.stages()) && wait_empty(); ++ahead, ++it) {
-            if (one) load_down(ahead / down.ks, ahead % down.ks);
+            if (one) load_down(w_at);
             __syncwarp();
+            advance(w_at);
             next_stage();
         }
     } else if (warp == 1 || warp == SECOND_MMA) {
@@ -666,12 +691,12 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     } else {
         for (int u = 0; u < up.units; ++u) {
             float v[TOK];
-            take(v, MX ? X_TERMS : 1, up.ks);
+            take(v, MX ? X_TERMS : 1, u * up.ks, up.ks);
 #pragma unroll
             for (int j = 0; j < TOK; ++j) sm.turn[row][j] = v[j];
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const int unit = up.unit(u), chunk = unit / n_f;
-            write_h<MX>(p, sm, (int)threadIdx.x - 32 * FIRST_EPI, rt.chunk_row[chunk], rt.chunk_n[chunk], unit % n_f * UP_F);
+            write_h<MX>(p, sm, (int)threadIdx.x, rt.chunk_row[chunk], rt.chunk_n[chunk], unit % n_f * UP_F);
             asm volatile("bar.sync 1, 128;" ::: "memory");
         }
         // h is read by tensor copies of other CTAs
@@ -685,16 +710,18 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     // ---- down
     if (warp == 0) {
         asm volatile("fence.proxy.async;" ::: "memory");
-        if (one)
-            for (int i = 0; i < ahead; ++i) load_h((base_it + i) % STAGES, i / down.ks, i % down.ks);
-        __syncwarp();
+        for (int i = 0; i < ahead; ++i) {
+            if (one) load_h((base_it + i) % STAGES, h_at);
+            __syncwarp();
+            advance(h_at);
+        }
         for (int i = ahead; i < down.stages() && wait_empty(); ++i, ++it) {
-            const int u = i / down.ks, k = i - u * down.ks;
             if (one) {
-                load_down(u, k);
-                load_h(s, u, k);
+                load_down(w_at);
+                load_h(s, w_at);
             }
             __syncwarp();
+            advance(w_at);
             next_stage();
         }
         if (stop)  // an aborted CTA waits for its own copies before it exits
@@ -725,7 +752,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     } else {
         for (int u = 0; u < down.units; ++u) {
             float v[TOK];
-            take(v, MX ? H_TERMS : 1, down.ks);
+            take(v, MX ? H_TERMS : 1, base_it + u * down.ks, down.ks);
             const int chunk = down_chunk(u), n = rt.chunk_n[chunk], row0 = rt.chunk_row[chunk];
 #pragma unroll
             for (int j = 0; j < TOK; ++j)
@@ -755,18 +782,25 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     }
     if (p.shares == 1 || share >= p.shares) return;
 
-    // ---- the sums of a tile's shares: the last CTA to leave its own adds them, in order
+    // ---- the sums of a tile's shares: its CTAs meet, and each adds a part of the outputs, in their order
     const int tile = cta % p.tiles;
     float* part = p.partial + (int64_t)tile * p.shares * p.T * TILE;
     for (int i = 4 * (int)threadIdx.x; i < p.T * TILE; i += 4 * THREADS)
         *reinterpret_cast<float4*>(part + (int64_t)share * p.T * TILE + i) = *reinterpret_cast<const float4*>(sums + i);
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) sm.last = atomicAdd(p.tickets + tile, 1u) == (uint32_t)p.shares - 1;
+    if (threadIdx.x == 0) {
+        atomicAdd(p.tickets + tile, 1u);
+        const uint64_t t0 = globaltimer_ns();
+        uint32_t met = 0;
+        while (!(met = ld_acquire_gpu(p.tickets + tile) == (uint32_t)p.shares) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {}
+        if (!met) raise_error(p.err, DERR_GEMM_TIMEOUT | (10u << 8));
+        sm.met = met;
+    }
     __syncthreads();
-    if (!sm.last) return;
+    if (!sm.met) return;
     __threadfence();
-    for (int i = 4 * (int)threadIdx.x; i < p.T * TILE; i += 4 * THREADS) {
+    for (int i = 4 * (share * THREADS + (int)threadIdx.x); i < p.T * TILE; i += 4 * p.shares * THREADS) {
         const int t = i / TILE, r = tile * TILE + i % TILE;
         if (r >= p.H) continue;  // H is a multiple of 8
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);

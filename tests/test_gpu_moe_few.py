@@ -93,6 +93,20 @@ def test_layer_vs_oracle(T, E, k, H, F, mx4):
     _check(out, *layer.reference(x, lg, k))
 
 
+@pytest.mark.parametrize("T,E,k,H,F", [(7, 60, 4, 1048, 520), (40, 64, 8, 776, 328), (64, 64, 2, 1160, 584)])
+@pytest.mark.parametrize("mx4", [False, True])
+def test_many_units_of_an_odd_number_of_stages(T, E, k, H, F, mx4):
+    """A stage of the ring changes between even and odd places of a unit: its waits must not take an older round for theirs."""
+    layer = Layer(E, H, F, mx4, 91)
+    xb, x = rand_bf16((T, H), 92)
+    lg = np.random.default_rng(93).standard_normal((T, E)).astype(np.float32)
+    x_dev, lg_dev = bf16_dev(xb), torch.from_numpy(lg).cuda()
+    out = layer.run(x_dev, lg_dev, k)
+    _check(out, *layer.reference(x, lg, k))
+    for _ in range(20):
+        assert torch.equal(layer.run(x_dev, lg_dev, k), out)
+
+
 @pytest.mark.parametrize("mx4", [False, True])
 def test_blobs_residual_stream_and_fp32_output(mx4):
     T, E, k, H, F = 5, 6, 2, 264, 96

@@ -173,6 +173,22 @@ def test_gemm_bf16_mxfp4_vs_oracle(M, N, K, f32):
     assert bool((out[M] == 77.0).all()), "wrote past the last row"
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 128 * 500, 384), (16, 128 * 470 + 60, 128), (40, 128 * 333 + 4, 640), (64, 128 * 310, 896)])
+def test_gemm_bf16_mxfp4_many_tiles_of_an_odd_number_of_stages(M, N, K):
+    ab, a = rand_bf16((M, K), 21)
+    bc, bs, b = _rand_mx(N, K, 22, K ** -0.5)
+    a_dev = bf16_dev(ab)
+    outs = [torch.empty((M, N), dtype=torch.float32, device="cuda") for _ in range(5)]
+    for o in outs:
+        L.lsk_gemm_bf16_mxfp4(a_dev, bc, bs, o, M, N, K)
+    torch.cuda.synchronize()
+    assert L.lsk_device_error() == 0
+    ref, tol = _few_ref(a, b, K)
+    assert np.all(np.abs(to_f64(outs[0]) - ref) <= tol)
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
 @pytest.mark.parametrize("pad", [1, 8])
 def test_gemm_bf16_mxfp4_strided_rows_of_many_magnitudes(pad):
     M, N, K = 7, 300, 700
