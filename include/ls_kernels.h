@@ -198,7 +198,7 @@ int64_t lsk_mxfp4_code_pitch(int32_t K);   /* 0 for K < 1 */
 int64_t lsk_mxfp4_scale_pitch(int32_t K);
 
 /* src_dev [rows, K] bf16 (fp32 when src_f32 != 0), ld >= K elements between rows -> codes_dev,
- * scales_dev. Any row alignment (16-byte aligned rows are read 16 bytes at a time). */
+ * scales_dev. Any row alignment (rows aligned to 32 or 16 bytes are read in accesses of that size). */
 ls_status lsk_mxfp4_quantize(const void* src_dev, int32_t src_f32, int64_t rows, int32_t K, int64_t ld,
                              void* codes_dev, void* scales_dev, void* stream);
 
@@ -216,8 +216,8 @@ ls_status lsk_gemm_mxfp4(const void* a_codes_dev, const void* a_scales_dev, cons
  * sums, C dense bf16 (fp32 when c_f32 != 0). Any M; made for few tokens (M = 1 upwards), where it streams the
  * weights once at 17/32 byte a value. A keeps its eight bits: values down to 2^-13 of the
  * largest of their block of 32 enter exactly, smaller ones within 2^-22 of that largest. A NaN or an
- * infinity in a row of A makes that row of C NaN. Takes scratch on `stream` from the library's
- * pool, as lsk_gemm_bf16 does (LS_ERR_OOM if refused). */
+ * infinity in a row of A makes that row of C NaN. More than 16 rows take scratch on `stream`
+ * from the library's pool, as lsk_gemm_bf16 does (LS_ERR_OOM if refused). */
 ls_status lsk_gemm_bf16_mxfp4(const void* A_dev, int64_t lda, const void* b_codes_dev, const void* b_scales_dev,
                               void* C_dev, int32_t c_f32, int32_t M, int32_t N, int32_t K, void* stream);
 
@@ -241,15 +241,15 @@ typedef struct lsk_moe_experts {
     int64_t down_scale_stride;
 } lsk_moe_experts;
 
-/* A whole MoE layer for a few tokens, in two launches:
+/* A whole MoE layer for a few tokens, in one cooperative launch (one CTA per SM):
  *   out[t] = r[t] + sum_{j<k} w[t,j] D_e (SiLU(G_e x[t]) * (U_e x[t])),  e = sel[t,j]
  * with sel and w as lsk_moe_route gives them from logits_dev [T, E] fp32 (the k largest, ties to the
  * lower expert, softmax over the chosen), r = resid_dev [T, H] fp32, or x_dev when that is NULL.
  * x_dev [T, H] bf16 (16-byte aligned), out_dev [T, H] bf16; out32_dev (may be NULL) gets the fp32
  * result. A NaN logit counts as the lowest one and makes its token NaN if it is chosen; a token
- * whose logits are all -infinity gets no expert (out = r). Sums are fp32 in a fixed order; the
- * hidden activation is rounded once (to bf16, or with MXFP4 experts to f16 times a power of two
- * for each 32, as x is for each row). T <= 64, E <= 256, k <= 8 (LS_ERR_UNSUPPORTED above:
+ * whose logits are all -infinity gets no expert (out = r). Sums are fp32 in a fixed order. With bf16
+ * experts the hidden activation is rounded once, to bf16. With MXFP4 experts it keeps twelve bits
+ * and x all eight (as in lsk_gemm_bf16_mxfp4), relative to the largest of 32 neighbours. T <= 64, E <= 256, k <= 8 (LS_ERR_UNSUPPORTED above:
  * lsk_moe_route to lsk_moe_combine serve more tokens), H and F multiples of 8. Takes scratch on
  * `stream` from the library's pool (LS_ERR_OOM if refused). */
 ls_status lsk_moe_few(const void* x_dev, const float* resid_dev, const float* logits_dev,
