@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblstream.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["ls_sched.cpp", "runtime.cu", "k_copy.cu", "k_gemm.cu", "k_simt.cu", "k_moe.cu", "k_debug.cu", "k_mxfp4.cu",
-           "k_gemm_mx.cu", "k_moe_few.cu", "kapi.cu", "kapi_static.cu", "kapi_ops.cu"]
+           "k_gemm_mx.cu", "k_gemm_mx4.cu", "k_moe_few.cu", "kapi.cu", "kapi_static.cu", "kapi_ops.cu"]
 
 
 def _nvcc() -> str:

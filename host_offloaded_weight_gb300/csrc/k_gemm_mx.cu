@@ -1,26 +1,21 @@
-// Products with MXFP4 matrices on the sm_103a tensor cores (tcgen05, block-scaled).
+// C[M,N] = sum_k A[m,k] B[n,k] with A bf16 and B MXFP4 on the sm_103a tensor cores (kind::mxf8f6f4, block-scaled),
+// for few rows of A (tokens). The weights are the left operand (128 rows a tile) and the tokens the right one, so a
+// single token costs 16 columns instead of 128 padded rows. The tensor core has no bf16 x E2M1 form; a bf16 value
+// has 8 significant bits and an E4M3 value 4, so A is written as two E4M3 terms with a power-of-two scale for each
+// block of 32:
+//   a = t1 2^s1 + t2 2^s2,  s1 = floor(log2 max|a|) - 7,  s2 = s1 - 5.
+// t1 is a 2^-s1 to the nearest, t2 the rest: exact for every value down to 2^-13 of its block's largest, below that
+// within 2^-22 of the largest. Both terms are columns of the same product and are added in fp32 in the epilogue.
 //
-//   4-bit x 4-bit   C[M,N] = sum_k A[m,k] B[n,k], both MXFP4: kind::mxf4, 64 values of K an
-//                   instruction, codes packed in shared memory as they lie in global memory.
-//   bf16 x 4-bit    C[M,N] = sum_k A[m,k] B[n,k], A bf16, B MXFP4: kind::mxf8f6f4. The weights
-//                   are the left operand (128 rows a tile) and the tokens the right one, so a
-//                   single token costs 16 columns instead of 128 padded rows. The tensor core has no bf16 x E2M1 form;
-//                   a bf16 value has 8 significant bits and an E4M3 value 4, so A is written as two
-//                   E4M3 terms with a power-of-two scale for each block of 32:
-//                     a = t1 2^s1 + t2 2^s2,  s1 = floor(log2 max|a|) - 7,  s2 = s1 - 5.
-//                   t1 is a 2^-s1 to the nearest, t2 the rest: exact for every value down to 2^-13 of its
-//                   block's largest, below that within 2^-22 of the largest. Both terms are columns
-//                   of the same product and are added in fp32 in the epilogue.
+// Structure (one persistent CTA per SM): warp 0 loads the weights by TMA, which unpacks them to a byte a value
+// (128-byte rows, 128-byte swizzle), into a ring of stages; the warps after warp 1 bring the scales into the stage
+// in the order that the tensor core reads them (32 rows of 16 bytes, the four 32-row groups side by side), and, up to
+// 16 tokens, the tokens' terms themselves (more come from memory by TMA, split by a kernel before). One or two warps
+// copy the scales to TMEM and issue the products; four write the results. The scales' TMEM columns belong to the
+// stage, so the barrier that frees a stage orders their reuse too.
 //
-// Structure (one persistent CTA per SM): warp 0 loads operand tiles by TMA (128-byte rows,
-// 128-byte swizzle) into a ring of stages; warps 2-5 bring the scales, 16 bytes a row at a
-// time, into the stage in the order that the tensor core reads them (32 rows of 16 bytes, the
-// four 32-row groups side by side); warp 1 copies the scales to TMEM and issues the
-// products; the others write the results. The scales' TMEM columns belong to the stage, so
-// the barrier that frees a stage orders their reuse too.
-//
-// Few tiles (bf16 x 4-bit) are shared along K by a cluster of CTAs, whose sums meet in the first one's shared
-// memory. Sums are fp32 and each output is written by one thread from a fixed order of sums.
+// Few tiles are shared along K by a cluster of CTAs, whose sums meet in the first one's shared memory. Sums are fp32
+// and each output is written by one thread from a fixed order of sums.
 #include <algorithm>
 #include <mutex>
 
@@ -32,31 +27,28 @@ namespace {
 
 using namespace tc;
 
-// MX_MX: both operands MXFP4. ACT: the right operand is the split rows in memory.
+// ACT: the right operand is the split rows in memory.
 // ACT_IN: up to 16 bf16 rows, split by the scale warps on their way into each stage.
-enum { MX_MX = 0, ACT = 1, ACT_IN = 2 };
+enum { ACT = 1, ACT_IN = 2 };
 
 constexpr int TILE_P = 128;               // rows of the left operand in a tile
 constexpr int P_BYTES = TILE_P * 128;     // a stage of it
 
 template <int MODE, int BQ>
 struct Cfg {
-    static constexpr int TN = BQ / 2;                          // ACT: tokens of a tile (two terms each)
-    static constexpr int QUADS = MODE == MX_MX ? 2 : 1;        // words of four blocks (128 values of K) in a stage
-    static constexpr int PER = 4 / QUADS;                      // stages of one 16-byte load of scales
+    static constexpr int TN = BQ / 2;                          // tokens of a tile (two terms each)
     static constexpr int PARTS = (BQ + 127) / 128;             // 128-row parts of the right operand's scales
     static constexpr int Q_BYTES = BQ * 128;
-    static constexpr int SCALE_BYTES = QUADS * (1 + PARTS) * 512;
+    static constexpr int SCALE_BYTES = (1 + PARTS) * 512;
     static constexpr int STAGE = (P_BYTES + Q_BYTES + SCALE_BYTES + 1023) / 1024 * 1024;
-    static constexpr int EPI_WARPS = MODE == MX_MX ? 8 : 4;
+    static constexpr int EPI_WARPS = 4;
     // CTAs that may share a tile along K, and the room for the others' sums in the first one's memory
-    static constexpr int MAX_SPLIT = MODE == MX_MX ? 1 : TN == 8 ? 8 : TN <= 32 ? 4 : TN == 64 ? 2 : 1;
+    static constexpr int MAX_SPLIT = TN == 8 ? 8 : TN <= 32 ? 4 : TN == 64 ? 2 : 1;
     static constexpr int RED_BYTES = (MAX_SPLIT - 1) * TN * TILE_P * 4;
-    static constexpr int EPI_BYTES = MODE == MX_MX ? EPI_WARPS * 4096 : RED_BYTES;
     // Up to 128 columns a stage's products are as short as an issuing warp's waits between them: two warps
     // take the even and the odd stages, each with an accumulator of its own.
-    static constexpr int MMA_WARPS = MODE != MX_MX && BQ <= 128 ? 2 : 1;
-    static constexpr int FIT = (232448 - 1024 - 512 - EPI_BYTES) / STAGE, MOST = FIT < 10 ? FIT : 10;
+    static constexpr int MMA_WARPS = BQ <= 128 ? 2 : 1;
+    static constexpr int FIT = (232448 - 1024 - 512 - RED_BYTES) / STAGE, MOST = FIT < 10 ? FIT : 10;
     // The scale warps work in teams that take turns of RUN stages. A wait by parity cannot tell a phase from the
     // one two before it. Where one warp issues the products, stages are freed in order, and turns within a
     // round of the ring are enough; where two do, each place in the ring has a team and a product warp of its own.
@@ -67,13 +59,13 @@ struct Cfg {
     static_assert(MMA_WARPS == 2 ? RUN == 1 && STAGES % TEAMS == 0 && STAGES % 2 == 0 : TEAMS * RUN <= STAGES,
                   "turns of the scale and the product warps");
     static constexpr int SCALE_WARPS = TEAM * TEAMS;
-    static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024 + 512;
+    static constexpr int SMEM = STAGES * STAGE + RED_BYTES + 1024 + 512;
     static constexpr int FIRST_EPI = 2 + SCALE_WARPS;            // the first warp of the epilogue
     static constexpr int SECOND_MMA = FIRST_EPI + EPI_WARPS;
     static constexpr int THREADS = 32 * (SECOND_MMA + MMA_WARPS - 1);
     static constexpr int ACC = MMA_WARPS * BQ;  // columns of an accumulator
-    static constexpr int ACCS = 2 * ACC + STAGES * QUADS * 4 * (1 + PARTS) <= 512 ? 2 : 1;
-    static constexpr int SCALE_COLS = QUADS * 4 * (1 + PARTS);  // TMEM columns of a stage's scales
+    static constexpr int ACCS = 2 * ACC + STAGES * 4 * (1 + PARTS) <= 512 ? 2 : 1;
+    static constexpr int SCALE_COLS = 4 * (1 + PARTS);  // TMEM columns of a stage's scales
     static_assert(ACCS * ACC + STAGES * SCALE_COLS <= 512, "tensor memory");
     static_assert(BQ % 16 == 0 && BQ <= 256, "columns of a product");
 };
@@ -83,9 +75,9 @@ struct MxParams {
     const uint8_t* scale_p;
     const uint8_t* scale_q;
     int scale_pitch;
-    int rows_p, rows_q;   // rows of the operands (ACT: rows_q = tokens)
+    int rows_p, rows_q;   // rows of the weights; tokens
     int q_term_rows;      // ACT: rows between the two terms
-    int k_stages;         // stages along K
+    int k_stages;         // stages along K (128 values)
     int tiles_p, tiles_q, tiles;
     int splits;           // CTAs (a cluster) that share a tile along K
     const __nv_bfloat16* a;  // ACT_IN: the rows themselves
@@ -93,22 +85,21 @@ struct MxParams {
     int K, vec;
     void* C;
     int64_t ldc;
-    int c_f32, c_vec;     // c_vec: groups of four columns are whole and aligned
+    int c_f32;
     uint32_t* err;
 };
 
 // The tiles of a CTA, in order, and its stages of each: with splits > 1 a cluster has one tile,
 // and its CTAs a run of whole scale groups each.
-template <int PER>
 struct Work {
     int tile, step, tiles, k0, k1;
     __device__ __forceinline__ Work(const MxParams& p) {
-        const int slice = (int)blockIdx.x % p.splits, groups = (p.k_stages + PER - 1) / PER;
+        const int slice = (int)blockIdx.x % p.splits, groups = (p.k_stages + 3) / 4;  // 16 bytes of scales
         step = (int)gridDim.x / p.splits;
         tile = (int)blockIdx.x / p.splits - step;
         tiles = p.tiles;
-        k0 = (int)((int64_t)slice * groups / p.splits) * PER;
-        k1 = min(p.k_stages, (int)((int64_t)(slice + 1) * groups / p.splits) * PER);
+        k0 = (int)((int64_t)slice * groups / p.splits) * 4;
+        k1 = min(p.k_stages, (int)((int64_t)(slice + 1) * groups / p.splits) * 4);
     }
     __device__ __forceinline__ bool next() {
         tile += step;
@@ -116,15 +107,11 @@ struct Work {
     }
 };
 
-template <int MODE, int BQ>
+// The token tiles of one weight tile follow one another.
+template <int BQ>
 __device__ __forceinline__ void tile_at(const MxParams& p, int tile, int& row_p, int& row_q) {
-    if (MODE == MX_MX) {
-        row_p = tile % p.tiles_p * TILE_P;
-        row_q = tile / p.tiles_p * BQ;
-    } else {  // the token tiles of one weight tile follow one another
-        row_p = tile / p.tiles_q * TILE_P;
-        row_q = tile % p.tiles_q * (BQ / 2);
-    }
+    row_p = tile / p.tiles_q * TILE_P;
+    row_q = tile % p.tiles_q * (BQ / 2);
 }
 
 __device__ __forceinline__ void store_c(const MxParams& p, int64_t at, float v) {
@@ -132,11 +119,7 @@ __device__ __forceinline__ void store_c(const MxParams& p, int64_t at, float v) 
     else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
-__device__ __forceinline__ void load_words(const uint8_t* p, bool in, uint4& v) {
-    v = in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-}
 __device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
 __device__ __forceinline__ void load_words(const uint8_t* p, bool in, uint2& v) {
     v = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
@@ -147,7 +130,6 @@ __device__ __forceinline__ void load_words(const uint8_t* p, bool in, uint32_t& 
 template <int BYTES> struct Words;
 template <> struct Words<4> { typedef uint32_t type; };
 template <> struct Words<8> { typedef uint2 type; };
-template <> struct Words<16> { typedef uint4 type; };
 
 // A row's sums for tokens j0 to j0 + 7 of a tile of ks stages, `first` on: the smaller terms first, of even and odd stages.
 template <int MODE, int BQ>
@@ -170,50 +152,15 @@ __device__ __forceinline__ void token_sums(uint32_t t, int j0, int first, int ks
     }
 }
 
-// A warp's 32 x 32 of the result, lane l with row r0 + l: turned through shared memory (float4
-// columns, exclusive-or swizzled by the row) so that eight lanes write a row's 32 columns.
-__device__ __forceinline__ void store_chunk(const MxParams& p, float4* buf, const uint32_t (&v)[32], int r0, int col0) {
-    const int lane = threadIdx.x & 31;
-    if (col0 >= p.rows_q || r0 >= p.rows_p) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        buf[lane * 8 + (j ^ (lane & 7))] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                                       __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-    __syncwarp();
-    const int c4 = lane & 7, col = col0 + 4 * c4;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3), row = r0 + r;
-        const float4 o = buf[r * 8 + (c4 ^ (r & 7))];
-        if (row >= p.rows_p || col >= p.rows_q) continue;
-        const int64_t at = (int64_t)row * p.ldc + col;
-        if (p.c_vec) {  // rows of whole, aligned groups of four
-            if (p.c_f32) {
-                *reinterpret_cast<float4*>(static_cast<float*>(p.C) + at) = o;
-            } else {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.C) + at) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            }
-        } else {
-            store_c(p, at, o.x);
-            if (col + 1 < p.rows_q) store_c(p, at + 1, o.y);
-            if (col + 2 < p.rows_q) store_c(p, at + 2, o.z);
-            if (col + 3 < p.rows_q) store_c(p, at + 3, o.w);
-        }
-    }
-    __syncwarp();
-}
-
 template <int MODE, int BQ>
 __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(const __grid_constant__ MxParams p) {
     using C = Cfg<MODE, BQ>;
-    constexpr int S = C::STAGES, PER = C::PER;
+    constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
-    const uint32_t bars = base + S * C::STAGE + C::EPI_BYTES;
+    const uint32_t bars = base + S * C::STAGE + C::RED_BYTES;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (S + s); };
     auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
@@ -241,14 +188,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
     if (warp == 1) tmem_get(smem_addr(tmem_slot), 512);
     fence_before_sync();
     __syncwarp();
-    if (MODE != MX_MX && p.splits > 1) cluster_barrier();
+    if (p.splits > 1) cluster_barrier();
     else __syncthreads();
     fence_after_sync();
     // ACT: the kernel before this one, which splits the rows, began after everything earlier was
     // complete, so only the split rows have to be waited for; the weights start at once
     if (MODE != ACT) grid_wait();
     const uint32_t tmem = *tmem_slot;
-    Work<PER> w(p);
+    Work w(p);
 
     if (warp == 0) {
         // ------------------------------------------------------------ operand tiles
@@ -257,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         uint32_t phase = 1;  // a new barrier's preceding phase counts as complete
         bool ok = true;
         // an unpacking copy counts the packed bytes (it leaves every second 8 bytes alone)
-        constexpr uint32_t BYTES = MODE == MX_MX ? P_BYTES + C::Q_BYTES : MODE == ACT ? P_BYTES / 2 + C::Q_BYTES : P_BYTES / 2;
+        constexpr uint32_t BYTES = MODE == ACT ? P_BYTES / 2 + C::Q_BYTES : P_BYTES / 2;
         auto load_q = [&](int st, int k, int row_q) {
             const uint32_t at = base + st * C::STAGE + P_BYTES;
             if (MODE != ACT_IN) tma_2d(at, &p.map_q, full(st), k * 128, row_q);
@@ -265,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         };
         while (ok && w.next()) {
             int row_p, row_q, k = w.k0;
-            tile_at<MODE, BQ>(p, w.tile, row_p, row_q);
+            tile_at<BQ>(p, w.tile, row_p, row_q);
             if (MODE == ACT && it == 0) {
                 const int ahead = min(S, w.k1 - w.k0);
                 if (one)
@@ -309,7 +256,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             }
     } else if (warp == 1 || (C::MMA_WARPS == 2 && warp == C::SECOND_MMA)) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t IDESC = MODE == MX_MX ? mx_idesc(1, 1, TILE_P, BQ) : mx_idesc(5, 0, TILE_P, BQ);
+        constexpr uint32_t IDESC = mx_idesc(5, 0, TILE_P, BQ);
         const bool one = elect_one();
         const int odd = warp == 1 ? 0 : 1;
         int n = 0, it = 0;
@@ -333,25 +280,15 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                 }
                 fence_after_sync();
                 const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
-                const uint32_t tp = tmem + (uint32_t)(C::ACCS * C::ACC + s * C::SCALE_COLS), tq = tp + 4 * C::QUADS;
+                const uint32_t tp = tmem + (uint32_t)(C::ACCS * C::ACC + s * C::SCALE_COLS), tq = tp + 4;
                 if (C::MMA_WARPS == 1) ready = bar_test(full((i + 1) % S), (uint32_t)((i + 1) / S) & 1u);
                 if (one) {
+scale_copy(tp, scale_desc(sc));
 #pragma unroll
-                    for (int q = 0; q < C::QUADS; ++q) {
-                        scale_copy(tp + 4 * q, scale_desc(sc + 512 * q));
+                    for (int j = 0; j < C::PARTS; ++j) scale_copy(tq + 4 * j, scale_desc(sc + 512 * (1 + j)));
 #pragma unroll
-                        for (int j = 0; j < C::PARTS; ++j)
-                            scale_copy(tq + 4 * (q * C::PARTS + j), scale_desc(sc + 512 * (C::QUADS + q * C::PARTS + j)));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // 32 bytes of each row
-                        const uint64_t dp = operand_desc(sp + 32 * j), dq = operand_desc(sq + 32 * j);
-                        if (MODE == MX_MX)
-                            mma_mxf4(d, dp, dq, idesc_at(IDESC, 2 * (j & 1)), tp + 4 * (j >> 1),
-                                     tq + 4 * C::PARTS * (j >> 1), j ? 1u : add);
-                        else
-                            mma_mxf8(d, dp, dq, idesc_at(IDESC, j), tp, tq, j ? 1u : add);
-                    }
+                    for (int j = 0; j < 4; ++j)  // 32 bytes of each row
+                        mma_mxf8(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc_at(IDESC, j), tp, tq, j ? 1u : add);
                     mma_commit(empty(s));
                 }
                 __syncwarp();
@@ -375,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         constexpr int NR = RPW * (MODE == ACT_IN ? 1 : 1 + C::PARTS);
         constexpr int AHEAD = MODE == ACT && RUN == 1 ? 3 : 1;             // turns requested ahead
         constexpr int U = MODE == ACT_IN ? C::TN / 2 : 1;                  // ACT_IN: units of 8 values a lane
-        typedef typename Words<4 * C::QUADS * RUN>::type V;
+        typedef typename Words<4 * RUN>::type V;
         const int team = (warp - 2) / C::TEAM, first = RPW * ((warp - 2) % C::TEAM);
         w.next();
         const int stages = w.k1 - w.k0, turns = (stages + RUN - 1) / RUN;
@@ -391,8 +328,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             const bool on = t < p.tiles;
             const int k = w.k0 + turn * RUN;
             int row_p = 0, row_q = 0;
-            if (on) tile_at<MODE, BQ>(p, t, row_p, row_q);
-            const int64_t at = (int64_t)k * (4 * C::QUADS);
+            if (on) tile_at<BQ>(p, t, row_p, row_q);
+            const int64_t at = 4ll * k;
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
                 if (j < j0 || j >= j1) continue;
@@ -401,9 +338,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                     load_words(p.scale_p + (int64_t)row * p.scale_pitch + at, on && row < p.rows_p, to[j]);
                 } else {
                     const int rq = lane + 128 * (j / RPW - 1) + 32 * (first + j % RPW);
-                    const int64_t row = MODE == MX_MX ? row_q + rq
-                                        : rq < BQ / 2 ? row_q + rq : (int64_t)row_q + rq - BQ / 2 + p.q_term_rows;
-                    load_words(p.scale_q + row * p.scale_pitch + at, on && rq < BQ && (MODE != MX_MX || row < p.rows_q), to[j]);
+                    const int64_t row = rq < BQ / 2 ? row_q + rq : (int64_t)row_q + rq - BQ / 2 + p.q_term_rows;
+                    load_words(p.scale_q + row * p.scale_pitch + at, on && rq < BQ, to[j]);
                 }
             }
             if (MODE == ACT_IN && j0 == 0) {
@@ -448,17 +384,13 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                 }
                 const uint32_t sq = base + s * C::STAGE + P_BYTES, sc = sq + C::Q_BYTES, at = sc + lane * 16 + 4 * first;
 #pragma unroll
-                for (int q = 0; q < C::QUADS; ++q)
-#pragma unroll
-                    for (int j = 0; j < NR / RPW; ++j) {  // the left operand's chunk, then the right one's parts
-                        const uint32_t to = at + 512 * (j == 0 ? q : C::QUADS + q * C::PARTS + j - 1);
-                        const int wi = i * C::QUADS + q;
-                        if (RPW == 4)
-                            st_shared4(to, word_of(v[0][RPW * j], wi), word_of(v[0][RPW * j + 1], wi),
-                                       word_of(v[0][RPW * j + 2 % RPW], wi), word_of(v[0][RPW * j + 3 % RPW], wi));
-                        else
-                            st_shared2(to, word_of(v[0][RPW * j], wi), word_of(v[0][RPW * j + 1], wi));
-                    }
+                for (int j = 0; j < NR / RPW; ++j) {  // the left operand's chunk, then the right one's parts
+                    if (RPW == 4)
+                        st_shared4(at + 512 * j, word_of(v[0][RPW * j], i), word_of(v[0][RPW * j + 1], i),
+                                   word_of(v[0][RPW * j + 2 % RPW], i), word_of(v[0][RPW * j + 3 % RPW], i));
+                    else
+                        st_shared2(at + 512 * j, word_of(v[0][RPW * j], i), word_of(v[0][RPW * j + 1], i));
+                }
                 if (MODE == ACT_IN) {
 #pragma unroll
                     for (int j = 0; j < U; ++j) {
@@ -496,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         int n = 0;
         while (w.next()) {
             int row_p, row_q;
-            tile_at<MODE, BQ>(p, w.tile, row_p, row_q);
+            tile_at<BQ>(p, w.tile, row_p, row_q);
             const int b = n % C::ACCS;
             if (!__all_sync(0xffffffffu, bar_wait(acc_full(b), (uint32_t)(n / C::ACCS) & 1u, p.err, 4) && !stop)) {
                 stop = 1;
@@ -504,34 +436,21 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             }
             fence_after_sync();
             const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC);
-            if (MODE == MX_MX) {
-                float4* buf = reinterpret_cast<float4*>(gbase + S * C::STAGE) + (warp - C::FIRST_EPI) * 256;
-                const int r0 = row_p + q * 32;
-                const int half = (warp - C::FIRST_EPI) >> 2;
+            const int row = q * 32 + lane, col = row_p + row;  // the weight row is the output column
+            const int tokens = min(C::TN, p.rows_q - row_q);
+            const uint32_t slice = blockIdx.x % p.splits;
+            // a cluster's later CTAs leave their sums in the first one's memory
+            const uint32_t red = slice ? cluster_addr(base + S * C::STAGE + (slice - 1) * C::TN * TILE_P * 4, 0) : 0u;
+            if (p.splits == 1 || slice) {
 #pragma unroll 1
-                for (int c = half; c < BQ / 32; c += 2) {
-                    uint32_t v[32];
-                    tmem_load32(t + 32 * c, v);
-                    tmem_load_wait();
-                    store_chunk(p, buf, v, r0, row_q + 32 * c);
-                }
-            } else {
-                const int row = q * 32 + lane, col = row_p + row;  // the weight row is the output column
-                const int tokens = min(C::TN, p.rows_q - row_q);
-                const uint32_t slice = blockIdx.x % p.splits;
-                // a cluster's later CTAs leave their sums in the first one's memory
-                const uint32_t red = slice ? cluster_addr(base + S * C::STAGE + (slice - 1) * C::TN * TILE_P * 4, 0) : 0u;
-                if (p.splits == 1 || slice) {
-#pragma unroll 1
-                    for (int j0 = 0; j0 < tokens; j0 += 8) {
-                        float sum[8];
-                        token_sums<MODE, BQ>(t, j0, n * (w.k1 - w.k0), w.k1 - w.k0, sum);
+                for (int j0 = 0; j0 < tokens; j0 += 8) {
+                    float sum[8];
+                    token_sums<MODE, BQ>(t, j0, n * (w.k1 - w.k0), w.k1 - w.k0, sum);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float v = sum[j];
-                            if (slice) st_cluster(red + ((j0 + j) * TILE_P + row) * 4, v);
-                            else if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        const float v = sum[j];
+                        if (slice) st_cluster(red + ((j0 + j) * TILE_P + row) * 4, v);
+                        else if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
                     }
                 }
             }
@@ -541,13 +460,13 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
             ++n;
         }
     }
-    if (MODE != MX_MX && p.splits > 1) {
+    if (p.splits > 1) {
         __syncwarp();
         cluster_barrier();  // every CTA's sums are in the first one's memory; the sum runs in CTA order
         if (blockIdx.x % p.splits == 0 && warp >= C::FIRST_EPI && warp < C::SECOND_MMA) {
             fence_after_sync();
             int row_p, row_q;
-            tile_at<MODE, BQ>(p, blockIdx.x / p.splits, row_p, row_q);
+            tile_at<BQ>(p, blockIdx.x / p.splits, row_p, row_q);
             const int q = warp & 3, row = q * 32 + lane, col = row_p + row;
             const int tokens = min(C::TN, p.rows_q - row_q);
             const float* red = reinterpret_cast<const float*>(gbase + S * C::STAGE) + row;
@@ -601,20 +520,6 @@ split_rows_kernel(const __nv_bfloat16* __restrict__ a, int64_t lda, int M, int K
 }
 
 // ------------------------------------------------------------------ host side
-// View of `rows` rows of `pitch` bytes in boxes of 128 x box_rows, 128-byte swizzle. unpack:
-// packed 4-bit values to a byte each (128 values a row of the box).
-bool map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows, bool unpack) {
-    const MxEncodeFn fn = mx_encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)(unpack ? 2 * pitch : pitch), (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-    cuuint32_t one[2] = {1, 1};
-    return fn(m, unpack ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr),
-              dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MODE, int BQ>
 cudaError_t launch(const MxParams& p, cudaStream_t s) {
     auto kern = gemm_mx_kernel<MODE, BQ>;
@@ -680,32 +585,18 @@ MxEncodeFn mx_encode_fn() {
     return fn;
 }
 
-cudaError_t launch_gemm_mx(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales, void* C,
-                           bool c_f32, int M, int N, int K, uint32_t* err, cudaStream_t s) {
-    if (M <= 0) return cudaSuccess;
-    constexpr int BQ = 192;
-    MxParams p;
-    memset(&p, 0, sizeof(p));
-    const int64_t pitch = mx_code_pitch(K);
-    if (!map_rows(&p.map_p, a_codes, M, pitch, TILE_P, false) || !map_rows(&p.map_q, b_codes, N, pitch, BQ, false))
-        return cudaErrorInvalidValue;
-    p.scale_p = static_cast<const uint8_t*>(a_scales);
-    p.scale_q = static_cast<const uint8_t*>(b_scales);
-    p.scale_pitch = (int)mx_scale_pitch(K);
-    p.rows_p = M;
-    p.rows_q = N;
-    p.k_stages = (K + 255) / 256;
-    p.tiles_p = (int)(up(M, TILE_P) / TILE_P);
-    p.tiles_q = (int)(up(N, BQ) / BQ);
-    if ((int64_t)p.tiles_p * p.tiles_q > 0x3fffffffll) return cudaErrorInvalidValue;
-    p.tiles = p.tiles_p * p.tiles_q;
-    p.splits = 1;
-    p.C = C;
-    p.ldc = N;
-    p.c_f32 = c_f32;
-    p.c_vec = N % 4 == 0 && (reinterpret_cast<uintptr_t>(C) & (c_f32 ? 15 : 7)) == 0;
-    p.err = err;
-    return launch<MX_MX, BQ>(p, s);
+// View of `rows` rows of `pitch` bytes in boxes of 128 x box_rows, 128-byte swizzle. unpack:
+// packed 4-bit values to a byte each (128 values a row of the box).
+bool mx_map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows, bool unpack) {
+    const MxEncodeFn fn = mx_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)(unpack ? 2 * pitch : pitch), (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t one[2] = {1, 1};
+    return fn(m, unpack ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr),
+              dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t act_mx_ws_bytes(int M, int K) {
@@ -725,7 +616,7 @@ cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, 
     p.tiles_q = (int)(rows / tn);
     if ((int64_t)p.tiles_p * p.tiles_q > 0x3fffffffll || 2 * rows > 0x7fffffffll) return cudaErrorInvalidValue;
     p.tiles = p.tiles_p * p.tiles_q;
-    if (!map_rows(&p.map_p, b_codes, N, mx_code_pitch(K), TILE_P, true)) return cudaErrorInvalidValue;
+    if (!mx_map_rows(&p.map_p, b_codes, N, mx_code_pitch(K), TILE_P, true)) return cudaErrorInvalidValue;
     p.scale_p = static_cast<const uint8_t*>(b_scales);
     p.rows_p = N;
     p.rows_q = M;
@@ -742,7 +633,7 @@ cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, 
     if (tn == 16) return launch_act<ACT_IN, 32>(p, s);
     uint8_t* terms = static_cast<uint8_t*>(ws);
     uint8_t* scales = terms + 2 * rows * kp;
-    if (!map_rows(&p.map_q, terms, 2 * rows, kp, tn, false)) return cudaErrorInvalidValue;
+    if (!mx_map_rows(&p.map_q, terms, 2 * rows, kp, tn, false)) return cudaErrorInvalidValue;
     p.scale_q = scales;
     p.q_term_rows = (int)rows;
     const uint32_t per_row = (uint32_t)(kp / 8);

@@ -144,6 +144,9 @@ typedef CUresult (*MxEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, vo
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 MxEncodeFn mx_encode_fn();  // the driver's tensor map encoder; NULL without a driver
+// View of `rows` rows of `pitch` bytes in boxes of 128 x box_rows, 128-byte swizzle. unpack:
+// packed 4-bit values to a byte each (128 values a row of the box).
+bool mx_map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows, bool unpack);
 cudaError_t launch_gemm_mx(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales, void* C,
                            bool c_f32, int M, int N, int K, uint32_t* err, cudaStream_t s);
 // bf16 x MXFP4: ws holds the split rows of more than 16 tokens (act_mx_ws_bytes, 0 for fewer; 256-byte aligned).

@@ -114,6 +114,27 @@ def test_gemm_mxfp4_vs_oracle(M, N, K, f32):
     assert bool((out[M] == 77.0).all()), "wrote past the last row"
 
 
+@pytest.mark.parametrize("M,N,K", [(2050, 5000, 700), (520, 10000, 260), (300, 3001, 96), (256, 17936, 1300), (1537, 1111, 2100)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_gemm_mxfp4_many_tiles(M, N, K, f32):
+    """Several tiles a CTA pair (rings and accumulators taken more than once), ragged last tiles, rows with and without alignment."""
+    ac, as_, a = _rand_mx(M, K, 31)
+    bc, bs, b = _rand_mx(N, K, 32, K ** -0.5)
+    out = torch.full((M + 1, N), 77.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    L.lsk_gemm_mxfp4(ac, as_, bc, bs, out, M, N, K)
+    torch.cuda.synchronize()
+    assert L.lsk_device_error() == 0
+    ref = a @ b.T
+    tol = _sum_tol(np.abs(a) @ np.abs(b).T, K) + (0 if f32 else 2.0 ** -8 * np.abs(ref))
+    assert np.all(np.abs(to_f64(out[:M]) - ref) <= tol)
+    assert bool((out[M] == 77.0).all()), "wrote past the last row"
+    again = torch.empty_like(out[:M])
+    for _ in range(5):
+        L.lsk_gemm_mxfp4(ac, as_, bc, bs, again, M, N, K)
+        assert torch.equal(again, out[:M])
+
+
+
 def test_gemm_mxfp4_applies_every_block_scale():
     """Each block of each row has a scale of its own, over the whole of the usual range."""
     M, N, K = 200, 260, 768
