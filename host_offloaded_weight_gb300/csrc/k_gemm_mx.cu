@@ -14,8 +14,14 @@
 // copy the scales to TMEM and issue the products; four write the results. The scales' TMEM columns belong to the
 // stage, so the barrier that frees a stage orders their reuse too.
 //
-// Few tiles are shared along K by a cluster of CTAs, whose sums meet in the first one's shared memory. Sums are fp32
-// and each output is written by one thread from a fixed order of sums.
+// Few tiles are shared along K by a cluster of CTAs, each of which adds the sums of every so many tokens, out of its
+// shared memory. Sums are fp32 and each output is written by one thread from a fixed order of sums.
+//
+// What bounds it: the tensor core's reads of shared memory. Unpacked weights are 4 KB a product of K = 32 however few
+// the columns: a stage takes 263 clocks with 16 columns and 362 with 64, about 68 bytes a clock, where its bytes from
+// memory would take 175 of a busy SM's share; and tiles of 128 rows leave SMs without one (13824 rows: 108 of 152).
+// 1 token through 13824 x 5120 takes 9.8 us (3.9 TB/s), 32 tokens through 5120 x 13824 14.4 us, of which the split
+// kernel, the launch and the first load are 6.
 #include <algorithm>
 #include <mutex>
 
@@ -41,8 +47,8 @@ struct Cfg {
     static constexpr int Q_BYTES = BQ * 128;
     static constexpr int SCALE_BYTES = (1 + PARTS) * 512;
     static constexpr int STAGE = (P_BYTES + Q_BYTES + SCALE_BYTES + 1023) / 1024 * 1024;
-    static constexpr int EPI_WARPS = 4;
-    // CTAs that may share a tile along K, and the room for the others' sums in the first one's memory
+    static constexpr int EPI_WARPS = MODE == ACT ? 8 : 4;  // ACT: 64 tokens through 13824 x 5120 from four warps 22.0 us, eight 20.0
+    // CTAs that may share a tile along K, and the room for the others' sums of this one's tokens
     static constexpr int MAX_SPLIT = TN == 8 ? 8 : TN <= 32 ? 4 : TN == 64 ? 2 : 1;
     static constexpr int RED_BYTES = (MAX_SPLIT - 1) * TN * TILE_P * 4;
     // Up to 128 columns a stage's products are as short as an issuing warp's waits between them: two warps
@@ -114,9 +120,21 @@ __device__ __forceinline__ void tile_at(const MxParams& p, int tile, int& row_p,
     row_q = tile % p.tiles_q * (BQ / 2);
 }
 
-__device__ __forceinline__ void store_c(const MxParams& p, int64_t at, float v) {
-    if (p.c_f32) static_cast<float*>(p.C)[at] = v;
-    else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
+// Eight tokens' sums of a weight row (an output column), tokens from `token` on.
+__device__ __forceinline__ void store_tokens(const MxParams& p, int col, int token, const float (&v)[8]) {
+    if (col >= p.rows_p) return;
+    const int64_t at = (int64_t)token * p.ldc + col;
+    if (p.c_f32) {
+        float* c = static_cast<float*>(p.C) + at;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (token + j < p.rows_q) c[j * p.ldc] = v[j];
+    } else {
+        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (token + j < p.rows_q) c[j * p.ldc] = __float2bfloat16_rn(v[j]);
+    }
 }
 
 __device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
@@ -196,6 +214,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
     if (MODE != ACT) grid_wait();
     const uint32_t tmem = *tmem_slot;
     Work w(p);
+    // the epilogue's warps: the TMEM lane quarter that a warp can read, and which of a quarter's warps it is
+    constexpr int HALVES = C::EPI_WARPS / 4;
+    const int q = warp & 3, half = (warp - C::FIRST_EPI) >> 2, slice = (int)blockIdx.x % p.splits;
 
     if (warp == 0) {
         // ------------------------------------------------------------ operand tiles
@@ -207,8 +228,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
         constexpr uint32_t BYTES = MODE == ACT ? P_BYTES / 2 + C::Q_BYTES : P_BYTES / 2;
         auto load_q = [&](int st, int k, int row_q) {
             const uint32_t at = base + st * C::STAGE + P_BYTES;
-            if (MODE != ACT_IN) tma_2d(at, &p.map_q, full(st), k * 128, row_q);
-            if (MODE == ACT) tma_2d(at + C::Q_BYTES / 2, &p.map_q, full(st), k * 128, row_q + p.q_term_rows);
+            if (MODE == ACT) tma_3d(at, &p.map_q, full(st), k * 128, row_q, 0);  // both terms
         };
         while (ok && w.next()) {
             int row_p, row_q, k = w.k0;
@@ -424,7 +444,6 @@ scale_copy(tp, scale_desc(sc));
         }
     } else if (warp < C::SECOND_MMA) {
         // ------------------------------------------------------------ results
-        const int q = warp & 3;  // the TMEM lane quarter that this warp can read
         int n = 0;
         while (w.next()) {
             int row_p, row_q;
@@ -436,22 +455,20 @@ scale_copy(tp, scale_desc(sc));
             }
             fence_after_sync();
             const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC);
-            const int row = q * 32 + lane, col = row_p + row;  // the weight row is the output column
-            const int tokens = min(C::TN, p.rows_q - row_q);
-            const uint32_t slice = blockIdx.x % p.splits;
-            // a cluster's later CTAs leave their sums in the first one's memory
-            const uint32_t red = slice ? cluster_addr(base + S * C::STAGE + (slice - 1) * C::TN * TILE_P * 4, 0) : 0u;
-            if (p.splits == 1 || slice) {
+            const int row = q * 32 + lane, groups = (min(C::TN, p.rows_q - row_q) + 7) / 8;
 #pragma unroll 1
-                for (int j0 = 0; j0 < tokens; j0 += 8) {
-                    float sum[8];
-                    token_sums<MODE, BQ>(t, j0, n * (w.k1 - w.k0), w.k1 - w.k0, sum);
+            for (int g = half; g < groups; g += HALVES) {  // eight tokens
+                // a cluster's CTAs take the groups in turn; the others leave their sums in the owner's memory
+                const int owner = g % p.splits;
+                if (p.splits > 1 && owner == slice) continue;
+                float sum[8];
+                token_sums<MODE, BQ>(t, 8 * g, n * (w.k1 - w.k0), w.k1 - w.k0, sum);
+                if (p.splits == 1) {
+                    store_tokens(p, row_p + row, row_q + 8 * g, sum);
+                } else {
+                    const uint32_t to = cluster_addr(base + S * C::STAGE + ((slice - (slice > owner)) * C::TN + 8 * g) * TILE_P * 4, owner);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float v = sum[j];
-                        if (slice) st_cluster(red + ((j0 + j) * TILE_P + row) * 4, v);
-                        else if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
-                    }
+                    for (int j = 0; j < 8; ++j) st_cluster(to + (j * TILE_P + row) * 4, sum[j]);
                 }
             }
             fence_before_sync();
@@ -462,25 +479,23 @@ scale_copy(tp, scale_desc(sc));
     }
     if (p.splits > 1) {
         __syncwarp();
-        cluster_barrier();  // every CTA's sums are in the first one's memory; the sum runs in CTA order
-        if (blockIdx.x % p.splits == 0 && warp >= C::FIRST_EPI && warp < C::SECOND_MMA) {
+        cluster_barrier();  // the sums are in their owners' memory; they are added in CTA order
+        if (warp >= C::FIRST_EPI && warp < C::SECOND_MMA) {
             fence_after_sync();
             int row_p, row_q;
             tile_at<BQ>(p, blockIdx.x / p.splits, row_p, row_q);
-            const int q = warp & 3, row = q * 32 + lane, col = row_p + row;
-            const int tokens = min(C::TN, p.rows_q - row_q);
+            const int row = q * 32 + lane, groups = (min(C::TN, p.rows_q - row_q) + 7) / 8;
             const float* red = reinterpret_cast<const float*>(gbase + S * C::STAGE) + row;
             const uint32_t t = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
-            for (int j0 = 0; j0 < tokens; j0 += 8) {
+            for (int g = slice + half * p.splits; g < groups; g += HALVES * p.splits) {
                 float sum[8];
-                token_sums<MODE, BQ>(t, j0, 0, w.k1 - w.k0, sum);
+                token_sums<MODE, BQ>(t, 8 * g, 0, w.k1 - w.k0, sum);
+#pragma unroll 1
+                for (int i = 0; i < p.splits - 1; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v = sum[j];
-                    for (int i = 0; i < p.splits - 1; ++i) v += red[(i * C::TN + j0 + j) * TILE_P];
-                    if (j0 + j < tokens && col < p.rows_p) store_c(p, (int64_t)(row_q + j0 + j) * p.ldc + col, v);
-                }
+                    for (int j = 0; j < 8; ++j) sum[j] += red[(i * C::TN + 8 * g + j) * TILE_P];
+                store_tokens(p, row_p + row, row_q + 8 * g, sum);
             }
         }
     }
@@ -541,6 +556,19 @@ cudaError_t launch(const MxParams& p, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = p.splits > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// View [2][rows][pitch bytes] of the split rows, in boxes of 128 bytes x both terms of `tokens`, 128-byte swizzle.
+bool map_terms(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int tokens) {
+    const MxEncodeFn fn = mx_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)rows, 2};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(rows * pitch)};
+    cuuint32_t box[3] = {128, (cuuint32_t)tokens, 2};
+    cuuint32_t one[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
@@ -633,7 +661,7 @@ cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, 
     if (tn == 16) return launch_act<ACT_IN, 32>(p, s);
     uint8_t* terms = static_cast<uint8_t*>(ws);
     uint8_t* scales = terms + 2 * rows * kp;
-    if (!mx_map_rows(&p.map_q, terms, 2 * rows, kp, tn, false)) return cudaErrorInvalidValue;
+    if (!map_terms(&p.map_q, terms, rows, kp, tn)) return cudaErrorInvalidValue;
     p.scale_q = scales;
     p.q_term_rows = (int)rows;
     const uint32_t per_row = (uint32_t)(kp / 8);
