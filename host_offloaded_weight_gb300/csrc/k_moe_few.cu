@@ -20,10 +20,14 @@
 // their sums through memory, each a part of the outputs, in the order of the CTAs: the same bits
 // every time, and no atomics on data.
 //
-// Warp 0 loads the weights by TMA into the ring, warps 2-9 take turns at the stages and add the
-// block scales and (up) the tokens' rows, warps 1 and 14 issue the products of even and odd stages into
-// accumulators of their own (one warp alone took 385 clocks a stage of 240 clocks of products, between its
-// waits; the memory brings a stage in 370), warps 10-13 take the results.
+// Roles (numbers of the code, see the kernel for the hardware's warps): 0 loads the weights by TMA into the ring,
+// 2 to 9 take turns at the stages and add the block scales and (up) the tokens' rows, 1 and 14 issue the products of
+// even and odd stages into accumulators of their own (one warp alone took 385 clocks a stage of 240 clocks of
+// products, between its waits; the memory brings a stage in 370), 10 to 13 take the results.
+//
+// 128 experts of 2048 x 768, k = 8: 16 tokens bf16 124 us (6.25 TB/s of the routed experts' bytes), 32 tokens MXFP4
+// 64 us (4.4 TB/s): routing 4.5, first load 3, up 31, the meeting and h on its way back 4, down 14, the tile's sums 4.
+// 1 token MXFP4 15 us, nearly all of it those latencies.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -43,7 +47,7 @@ constexpr int TILE = 128;         // weight rows of a tile
 constexpr int UP_F = TILE / 2;    // columns of h of a tile of the up kernel
 constexpr int FEED_WARPS = 8, FIRST_EPI = 2 + FEED_WARPS;
 constexpr int SECOND_MMA = FIRST_EPI + 4;  // the warp that issues the products of odd stages
-constexpr int THREADS = 32 * (SECOND_MMA + 1);
+constexpr int THREADS = 32 * (SECOND_MMA + 2);  // the last warp takes part in the routing alone: 16 tokens in one pass
 constexpr int P_BYTES = TILE * 128;
 constexpr int X_TERMS = 2, H_TERMS = 3;  // E4M3 terms of x and of h (MXFP4 experts)
 
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     // Thread 0 waits for the other CTAs at the meeting and can come back from it apart from its warp. A copy issued
     // under elect_one() by a warp in two parts is issued twice, so the first four warps are the epilogue's.
     const int hw_warp = uniform_warp(), lane = threadIdx.x & 31;
-    const int warp = hw_warp < 4 ? FIRST_EPI + hw_warp : hw_warp < SECOND_MMA ? hw_warp - 4 : SECOND_MMA;
+    const int warp = hw_warp < 4 ? FIRST_EPI + hw_warp : hw_warp < SECOND_MMA ? hw_warp - 4 : hw_warp;
 
     if (threadIdx.x == 0) {
         stop = 0;
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
         }
         // the weights' scales of this warp's first turn of down: the first stage it with it % 8 = w
         if (MX) fetch_down(cur, ((w - base_it) % FEED_WARPS + FEED_WARPS) % FEED_WARPS, true, false);
-    } else {
+    } else if (warp < SECOND_MMA) {
         for (int u = 0; u < up.units; ++u) {
             float v[TOK];
             take(v, MX ? X_TERMS : 1, u * up.ks, up.ks);
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
                 cur = nxt;
             }
         }
-    } else {
+    } else if (warp < SECOND_MMA) {
         for (int u = 0; u < down.units; ++u) {
             float v[TOK];
             take(v, MX ? H_TERMS : 1, base_it + u * down.ks, down.ks);
@@ -787,10 +791,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     float* part = p.partial + (int64_t)tile * p.shares * p.T * TILE;
     for (int i = 4 * (int)threadIdx.x; i < p.T * TILE; i += 4 * THREADS)
         *reinterpret_cast<float4*>(part + (int64_t)share * p.T * TILE + i) = *reinterpret_cast<const float4*>(sums + i);
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) {
-        atomicAdd(p.tickets + tile, 1u);
+    if (threadIdx.x == 0) {  // a release and an acquire by one thread, between barriers of the CTA, order every thread's parts
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.tickets + tile) : "memory");
         const uint64_t t0 = globaltimer_ns();
         uint32_t met = 0;
         while (!(met = ld_acquire_gpu(p.tickets + tile) == (uint32_t)p.shares) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {}
@@ -799,7 +802,6 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     }
     __syncthreads();
     if (!sm.met) return;
-    __threadfence();
     for (int i = 4 * (share * THREADS + (int)threadIdx.x); i < p.T * TILE; i += 4 * p.shares * THREADS) {
         const int t = i / TILE, r = tile * TILE + i % TILE;
         if (r >= p.H) continue;  // H is a multiple of 8
