@@ -31,9 +31,9 @@ using namespace tc;
 constexpr int TILE_P = 128;              // rows of A of a CTA
 constexpr int P_BYTES = TILE_P * 128;    // a stage of it
 constexpr int QUADS = 2;                 // words of four blocks (128 values of K) in a stage
-constexpr int EPI_WARPS = 8, SCALE_WARPS = 4;
-constexpr int RUN = 4;                   // stages of a scale warp's loads (32 bytes of each row)
-constexpr int FIRST_EPI = 2 + SCALE_WARPS, THREADS = 32 * (FIRST_EPI + EPI_WARPS);
+constexpr int EPI_WARPS = 8, TEAM = 4, TEAMS = 2;  // scale warps: teams of four take turns
+constexpr int RUN = 4;                   // stages of a turn: 32 bytes of a row's scales
+constexpr int FIRST_EPI = 2 + TEAM * TEAMS, THREADS = 32 * (FIRST_EPI + EPI_WARPS);
 
 template <int BQ>
 struct Cfg {
@@ -47,6 +47,9 @@ struct Cfg {
     static constexpr int SCALE_COLS = QUADS * 4 * (1 + PARTS);  // TMEM columns of a stage's scales
     static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024 + 512;
     static_assert(2 * BQ + 2 * SCALE_COLS <= 512, "tensor memory");
+    // A wait by parity cannot tell a phase from the one two before it. Stages are freed in order, so a team's wait for
+    // one stage covers every older one: its next may be a round of the ring later, not more.
+    static_assert(RUN * (TEAMS - 1) + 1 <= STAGES, "turns of the scale warps");
     static_assert(BQ % 32 == 0 && BQ <= 224, "columns of a product");
 };
 
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_mx4_pair_kernel(const __grid_
     if (threadIdx.x == 0) {
         stop = 0;
         for (int s = 0; s < S; ++s) {
-            bar_init(full(s), 1 + 2 * SCALE_WARPS);  // the first CTA's TMA thread and both CTAs' scale warps
+            bar_init(full(s), 1 + 2 * TEAM);  // the first CTA's TMA thread and a team of scale warps of each CTA
             bar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_mx4_pair_kernel(const __grid_
         // order that the tensor core reads. A row's words for RUN stages are loaded together, while the RUN stages
         // before are at hand: whole 32-byte sectors, where 16 bytes a load would fetch each sector twice.
         constexpr int NR = 1 + C::PARTS;
-        const int w = warp - 2, runs = (stages + RUN - 1) / RUN, quarters = p.scale_pitch / 16;
+        const int team = (warp - 2) / TEAM, w = (warp - 2) % TEAM, runs = (stages + RUN - 1) / RUN, quarters = p.scale_pitch / 16;
         const uint32_t full_at = cluster_addr(full(0), 0);
         uint4 v[2][NR][2];
         auto fetch = [&](uint4 (&to)[NR][2], int tile, int run) {
@@ -271,40 +274,39 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_mx4_pair_kernel(const __grid_
                 }
             }
         };
-        int tile = pair, run = 0, s = 0;
-        uint32_t phase = 1;
+        struct Turn {
+            int tile, run, first;  // first: the tile's first stage in the ring's line
+        };
+        auto after = [&](Turn t, int by) {
+            for (t.run += by; t.run >= runs; t.run -= runs, t.tile += pairs, t.first += stages) {}
+            return t;
+        };
+        Turn at = after(Turn{pair, 0, 0}, team);
         bool ok = true;
-        fetch(v[0], tile, run);
-        while (ok && tile < p.tiles) {
-            int n_tile = tile, n_run = run + 1;
-            if (n_run == runs) {
-                n_run = 0;
-                n_tile += pairs;
-            }
-            fetch(v[1], n_tile, n_run);
+        fetch(v[0], at.tile, at.run);
+        while (ok && at.tile < p.tiles) {
+            const Turn next = after(at, TEAMS);
+            fetch(v[1], next.tile, next.run);
 #pragma unroll
             for (int i = 0; i < RUN; ++i) {
-                if (!ok || run * RUN + i >= stages) continue;
-                if (!bar_wait_warp(empty(s), phase, p.err, 7)) {
+                if (!ok || at.run * RUN + i >= stages) continue;
+                const int it = at.first + at.run * RUN + i, s = it % S;
+                if (!bar_wait_warp(empty(s), (uint32_t)(it / S + 1) & 1u, p.err, 7)) {
                     ok = false;
                     stop = 1;
                     continue;
                 }
-                const uint32_t at = base + s * C::STAGE + P_BYTES + C::Q_BYTES + lane * 16 + 4 * w;
+                const uint32_t to = base + s * C::STAGE + P_BYTES + C::Q_BYTES + lane * 16 + 4 * w;
 #pragma unroll
                 for (int q = 0; q < QUADS; ++q)
 #pragma unroll
                     for (int j = 0; j < NR; ++j)  // A's chunk, then B's parts
-                        st_shared1(at + 512 * (j == 0 ? q : QUADS + q * C::PARTS + j - 1), word_of(v[0][j][i >> 1], 2 * (i & 1) + q));
+                        st_shared1(to + 512 * (j == 0 ? q : QUADS + q * C::PARTS + j - 1), word_of(v[0][j][i >> 1], 2 * (i & 1) + q));
                 fence_smem_async();
                 __syncwarp();
                 if (lane == 0) {
                     if (rank == 0) bar_arrive(full(s));
                     else bar_arrive_cluster(full_at + 8 * s);
-                }
-                if (++s == S) {
-                    s = 0;
-                    phase ^= 1u;
                 }
             }
 #pragma unroll
@@ -312,8 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_mx4_pair_kernel(const __grid_
                 v[0][j][0] = v[1][j][0];
                 v[0][j][1] = v[1][j][1];
             }
-            tile = n_tile;
-            run = n_run;
+            at = next;
         }
     } else {
         // ------------------------------------------------------------ results
