@@ -189,12 +189,14 @@ def _check(status: int, ctx=None) -> int:
 
 def _ptr(t) -> int:
     """Address of a torch tensor, numpy array or raw int pointer (None -> 0)."""
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        pass
     if t is None:
         return 0
     if isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
-        return t.data_ptr()
     if hasattr(t, "ctypes"):
         return t.ctypes.data
     raise TypeError(f"cannot take the address of {type(t)}")
@@ -569,9 +571,17 @@ def lsk_moe_combine(x, y, T, k, H, out, out32=None, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ MXFP4
+_f32_of = {None: 0}  # a tensor's dtype -> whether it is float32, as far as they have been met
+
+
 def _is_f32(t) -> int:
     """1 for float32, 0 for bf16 and for raw addresses; other types are a TypeError."""
-    return int(hasattr(t, "dtype") and _dtype_code(t) == LS_DTYPE_F32)
+    d = getattr(t, "dtype", None)
+    try:
+        return _f32_of[d]
+    except KeyError:
+        _f32_of[d] = int(_dtype_code(t) == LS_DTYPE_F32)
+        return _f32_of[d]
 
 
 def lsk_mxfp4_code_pitch(K: int) -> int:
