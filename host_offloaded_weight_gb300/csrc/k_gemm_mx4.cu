@@ -1,11 +1,11 @@
 // C[M,N] = sum_k A[m,k] B[n,k] with both operands MXFP4, on the sm_103a tensor cores: kind::mxf4, 64 values of K
 // an instruction, codes packed in shared memory as they lie in global memory, fp32 sums.
 //
-// What bounds it: at 4 bits the tensor core takes 64 bytes of each operand row in less time than a stage's rows
-// take to arrive from L2 (without three quarters of the products a large call takes 52 us, with them 55), so a
-// tile's cost is the rows that an SM must load. A pair of CTAs therefore shares a tile of 256 x BQ
-// (cta_group::2): each SM loads 128 rows of A and BQ / 2 of B for 128 x BQ outputs. One CTA with 128 x 192 tiles
-// loaded 320 rows for 24576 outputs, a pair with 256 x 224 loads 240 for 28672.
+// What bounds it: shared memory, at 128 bytes a clock. A stage's rows are written once and read by the products once
+// for every tile, so a tile's shape decides: a pair of CTAs shares a tile of 256 x BQ (cta_group::2), each SM loads 128
+// rows of A and BQ / 2 of B for 128 x BQ outputs. With 256 x 224 a stage writes 31 KB and its products read 45: about
+// 600 of the 690 clocks that it takes (its products alone would take 320). One CTA with 128 x 192 tiles wrote 41 KB
+// for 24576 outputs in place of 28672. A wider tile leaves no TMEM for a second accumulator.
 //
 // Structure (persistent pairs, one CTA an SM): warp 0 loads the CTA's operand rows by TMA (128-byte rows = 256
 // values of K, 128-byte swizzle) into a ring of stages; warps 2 to 5 bring the scales, 32 bytes of a row at a time,
@@ -15,9 +15,10 @@
 // count at the first CTA's `full` barriers; what frees a stage, and what completes a tile, is signalled in both.
 // The scales have two sets of TMEM columns, taken in turn: the products of two stages before have to be complete.
 //
-// 2048 x 13824 x 5120: 55 us, 5.3 PFLOP/s (single CTAs: 63 us); 4096 x 4096 x 1024: 12.7 us (17.7); 333 x 1111 x
-// 1000: 4.7 us (10.5); 8192 x 8192 x 8192: 6.0 PFLOP/s. Scales cost 6 us of the first: every row's 8 bytes a stage
-// come as sectors of their own. Results written by lanes in place of bulk stores: 55.9 and 14.1 us.
+// 2048 x 13824 x 5120: 50 us, 5.75 PFLOP/s (single CTAs: 63 us); 4096 x 4096 x 1024: 12.4 us (17.7); 333 x 1111 x
+// 1000: 4.8 us (10.5); 8192 x 8192 x 8192: 6.6 PFLOP/s. One team of scale warps in place of two: 54.5 us for the
+// first; results written by lanes in place of bulk stores: 14.1 us for the second. A ring of the scales' own and a warp
+// that copies them to TMEM, with 192 columns: 49.9 and 12.6 us, not worth their barriers.
 #include <algorithm>
 
 #include "kernels.h"
