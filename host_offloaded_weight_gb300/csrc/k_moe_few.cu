@@ -423,10 +423,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     }
     if (warp == 1) tmem_get(smem_addr(&sm.tmem), TMEM_COLS);
     for (int i = threadIdx.x; i < p.T * TILE; i += THREADS) sums[i] = 0.f;
+    fence_before_sync();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < p.tiles; i += THREADS) p.tickets[i] = 0;
-    fence_before_sync();
-    grid_wait();
     route(rt, p, hw_warp, lane);  // begins and ends with a barrier of the CTA
     fence_after_sync();
     const uint32_t tmem = sm.tmem;
@@ -869,7 +868,7 @@ cudaError_t launch(const FewParams& p, int grid, cudaStream_t s) {
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem_bytes<MX>(p.T);
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[1];  // programmatic stream serialization changes nothing for a cooperative launch (measured)
     at[0].id = cudaLaunchAttributeCooperative;
     at[0].val.cooperative = 1;
     cfg.attrs = at;
