@@ -10,7 +10,7 @@
 // Structure (one persistent CTA per SM): warp 0 loads the weights by TMA, which unpacks them to a byte a value
 // (128-byte rows, 128-byte swizzle), into a ring of stages; the warps after warp 1 bring the scales into the stage
 // in the order that the tensor core reads them (32 rows of 16 bytes, the four 32-row groups side by side), and, up to
-// 16 tokens, the tokens' terms themselves (more come from memory by TMA, split by a kernel before). One or two warps
+// 8 tokens, the tokens' terms themselves (more come from memory by TMA, split by a kernel before). One or two warps
 // copy the scales to TMEM and issue the products; four write the results. The scales' TMEM columns belong to the
 // stage, so the barrier that frees a stage orders their reuse too.
 //
@@ -34,7 +34,8 @@ namespace {
 using namespace tc;
 
 // ACT: the right operand is the split rows in memory.
-// ACT_IN: up to 16 bf16 rows, split by the scale warps on their way into each stage.
+// ACT_IN: up to 8 bf16 rows, split by the scale warps on their way into each stage (16 rows so took 16.9 us through
+// 13824 x 5120, with a split kernel before 13.4; 8 rows 11.8).
 enum { ACT = 1, ACT_IN = 2 };
 
 constexpr int TILE_P = 128;               // rows of the left operand in a tile
@@ -629,7 +630,7 @@ bool mx_map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, i
 
 int64_t act_mx_ws_bytes(int M, int K) {
     const int tn = act_tile(M);
-    return tn <= 16 ? 0 : 2 * up(M, tn) * (up(K, 128) + mx_scale_pitch(K));
+    return tn <= 8 ? 0 : 2 * up(M, tn) * (up(K, 128) + mx_scale_pitch(K));
 }
 
 cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, const void* b_scales, void* C, bool c_f32,
@@ -658,7 +659,6 @@ cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, 
     p.c_f32 = c_f32;
     p.err = err;
     if (tn == 8) return launch_act<ACT_IN, 16>(p, s);
-    if (tn == 16) return launch_act<ACT_IN, 32>(p, s);
     uint8_t* terms = static_cast<uint8_t*>(ws);
     uint8_t* scales = terms + 2 * rows * kp;
     if (!map_terms(&p.map_q, terms, rows, kp, tn)) return cudaErrorInvalidValue;
@@ -680,6 +680,7 @@ cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, 
                                              p.scale_pitch);
     if (e != cudaSuccess) return e;
     switch (tn) {
+        case 16: return launch_act<ACT, 32>(p, s);
         case 32: return launch_act<ACT, 64>(p, s);
         case 64: return launch_act<ACT, 128>(p, s);
         default: return launch_act<ACT, 256>(p, s);

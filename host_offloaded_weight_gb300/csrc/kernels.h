@@ -149,7 +149,7 @@ MxEncodeFn mx_encode_fn();  // the driver's tensor map encoder; NULL without a d
 bool mx_map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows, bool unpack);
 cudaError_t launch_gemm_mx(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales, void* C,
                            bool c_f32, int M, int N, int K, uint32_t* err, cudaStream_t s);
-// bf16 x MXFP4: ws holds the split rows of more than 16 tokens (act_mx_ws_bytes, 0 for fewer; 256-byte aligned).
+// bf16 x MXFP4: ws holds the split rows of more than 8 tokens (act_mx_ws_bytes, 0 for fewer; 256-byte aligned).
 int64_t act_mx_ws_bytes(int M, int K);
 cudaError_t launch_gemm_act_mx(const void* a, int64_t lda, const void* b_codes, const void* b_scales, void* C, bool c_f32,
                                int M, int N, int K, void* ws, uint32_t* err, cudaStream_t s);

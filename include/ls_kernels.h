@@ -216,7 +216,7 @@ ls_status lsk_gemm_mxfp4(const void* a_codes_dev, const void* a_scales_dev, cons
  * sums, C dense bf16 (fp32 when c_f32 != 0). Any M; made for few tokens (M = 1 upwards), where it streams the
  * weights once at 17/32 byte a value. A keeps its eight bits: values down to 2^-13 of the
  * largest of their block of 32 enter exactly, smaller ones within 2^-22 of that largest. A NaN or an
- * infinity in a row of A makes that row of C NaN. More than 16 rows take scratch on `stream`
+ * infinity in a row of A makes that row of C NaN. More than 8 rows take scratch on `stream`
  * from the library's pool, as lsk_gemm_bf16 does (LS_ERR_OOM if refused). */
 ls_status lsk_gemm_bf16_mxfp4(const void* A_dev, int64_t lda, const void* b_codes_dev, const void* b_scales_dev,
                               void* C_dev, int32_t c_f32, int32_t M, int32_t N, int32_t K, void* stream);
