@@ -189,12 +189,12 @@ def _check(status: int, ctx=None) -> int:
 
 def _ptr(t) -> int:
     """Address of a torch tensor, numpy array or raw int pointer (None -> 0)."""
+    if t is None:
+        return 0
     try:
         return t.data_ptr()
     except AttributeError:
         pass
-    if t is None:
-        return 0
     if isinstance(t, int):
         return t
     if hasattr(t, "ctypes"):
@@ -619,21 +619,23 @@ def lsk_gemm_bf16_mxfp4(A, B_codes, B_scales, C_out, M: int, N: int, K: int, lda
                                            _ptr(C_out), _is_f32(C_out), M, N, K, _stream(stream)))
 
 
-def _stride_bytes(t) -> int:
-    """Bytes between the experts of a stacked tensor."""
-    return t.stride(0) * t.itemsize
-
-
 def lsk_moe_few(x, logits, gate, up, down, T: int, E: int, k: int, H: int, F: int, out, gate_scales=None,
                 up_scales=None, down_scales=None, resid=None, out32=None, stream=None) -> int:
     """One MoE layer for T <= 64 tokens. gate, up [E, F, H] and down [E, H, F] bf16, or MXFP4 codes
     [E, rows, code pitch] with their scales [E, rows, scale pitch]; an expert's rows are dense."""
-    mx = gate_scales is not None
-    gs, ss = _stride_bytes(gate), _stride_bytes(gate_scales) if mx else 0
-    if _stride_bytes(up) != gs or (mx and _stride_bytes(up_scales) != ss):
+    # bytes between the experts of a stacked tensor
+    gs = gate.stride(0) * gate.itemsize
+    if up.stride(0) * up.itemsize != gs:
         raise ValueError("gate and up need the same distance between experts")
-    w = lsk_moe_experts(mx, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), gs, _stride_bytes(down),
-                        _ptr(gate_scales), _ptr(up_scales), _ptr(down_scales), ss,
-                        _stride_bytes(down_scales) if mx else 0)
+    if gate_scales is None:
+        w = lsk_moe_experts(0, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), gs, down.stride(0) * down.itemsize)
+    else:
+        if up_scales is None or down_scales is None:
+            raise ValueError("MXFP4 experts need the scales of all three matrices")
+        ss = gate_scales.stride(0)
+        if up_scales.stride(0) != ss:
+            raise ValueError("gate and up need the same distance between experts")
+        w = lsk_moe_experts(1, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), gs, down.stride(0) * down.itemsize,
+                            gate_scales.data_ptr(), up_scales.data_ptr(), down_scales.data_ptr(), ss, down_scales.stride(0))
     return _check(_lib.lsk_moe_few(_ptr(x), _ptr(resid), _ptr(logits), C.byref(w), T, E, k, H, F, _ptr(out),
                                    _ptr(out32), _stream(stream)))
