@@ -13,7 +13,7 @@
 // values: 32 bytes of bf16 in one access, 8 bytes of codes; two neighbouring lanes join their
 // maxima by one shuffle, and the index arithmetic (no division: a block of threads is columns x
 // rows) and the scale are paid once for 16 values.
-// 13824 x 5120 bf16: 28.0 us there and 30.3 us back (6.4 and 5.9 TB/s; 8 values a thread and an index division
+// 13824 x 5120 bf16: 27.9 us there and 29.0 us back (6.4 and 6.2 TB/s; 8 values a thread and an index division
 // took 89 for both); fp32 47 and 48 us (6.8 and 6.6 TB/s). fp32 back in 16-byte accesses: 69 us.
 #include "kernels.h"
 #include "tc.cuh"
@@ -206,16 +206,17 @@ int vec_of(const void* p, int64_t ld, bool f32) {
 }
 
 // A block of threads is bx half blocks of a row x by rows, launched behind the kernel before it
-// (programmatic stream serialization). Two rows a thread where that still fills the device (13824 x 5120 bf16: 28.0 us, from
-// one row a thread 30.0).
+// (programmatic stream serialization). `per` rows a thread where that still fills the device. 13824 x 5120 bf16, rows a
+// thread and us: there 1 30.0, 2 27.9, 4 28.8; back in 32-byte accesses 1 31.6, 2 30.3, 4 29.0, in 16-byte ones 2 33.3, 4
+// 36.1; fp32 the same with 2 and 4 back, 47.1 and 49.4 there.
 template <class Kernel, class... Args>
-cudaError_t launch_halves(Kernel one, Kernel two, int64_t rows, int64_t per_row, cudaStream_t s, Args... args) {
+cudaError_t launch_halves(Kernel one, Kernel several, int per, int64_t rows, int64_t per_row, cudaStream_t s, Args... args) {
     int64_t segments = (per_row + 255) / 256, bx = per_row, by = 1;
     if (per_row >= 128) bx = ((per_row + segments - 1) / segments + 31) / 32 * 32;  // whole warps
     else by = 256 / per_row >= 4 ? 256 / per_row / 4 * 4 : 4;  // per_row is a multiple of 8
     if (segments > 65535) segments = 65535;
     const bool many = rows * per_row >= 2ll * 2048 * 4 * gemm_num_sms();
-    const int64_t blocks = (rows + by * (many ? 2 : 1) - 1) / (by * (many ? 2 : 1));
+    const int64_t blocks = (rows + by * (many ? per : 1) - 1) / (by * (many ? per : 1));
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)segments);
@@ -226,7 +227,7 @@ cudaError_t launch_halves(Kernel one, Kernel two, int64_t rows, int64_t per_row,
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, many ? two : one, args...);
+    return cudaLaunchKernelEx(&cfg, many ? several : one, args...);
 }
 
 }  // namespace
@@ -238,9 +239,9 @@ cudaError_t launch_mx_quantize(const void* src, bool f32, int64_t rows, int K, i
     const int vec = vec_of(src, ld, f32);
     uint2* c = static_cast<uint2*>(codes);
     uint8_t* sc = static_cast<uint8_t*>(scales);
-    return f32 ? launch_halves(mx_quantize_kernel<true, 1>, mx_quantize_kernel<true, 2>, rows, per_row, s, src, rows,
+    return f32 ? launch_halves(mx_quantize_kernel<true, 1>, mx_quantize_kernel<true, 2>, 2, rows, per_row, s, src, rows,
                                (int64_t)K, ld, vec, per_row, c, sc, sp)
-               : launch_halves(mx_quantize_kernel<false, 1>, mx_quantize_kernel<false, 2>, rows, per_row, s, src, rows,
+               : launch_halves(mx_quantize_kernel<false, 1>, mx_quantize_kernel<false, 2>, 2, rows, per_row, s, src, rows,
                                (int64_t)K, ld, vec, per_row, c, sc, sp);
 }
 
@@ -251,10 +252,11 @@ cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t 
     const int vec = vec_of(dst, ld, f32);
     const uint2* c = static_cast<const uint2*>(codes);
     const uint8_t* sc = static_cast<const uint8_t*>(scales);
-    return f32 ? launch_halves(mx_dequantize_kernel<true, 1>, mx_dequantize_kernel<true, 2>, rows, per_row, s, c, sc, sp,
+    const bool four = !f32 && vec == 2;
+    return f32 ? launch_halves(mx_dequantize_kernel<true, 1>, mx_dequantize_kernel<true, 2>, 2, rows, per_row, s, c, sc, sp,
                                rows, (int64_t)K, per_row, dst, ld, vec)
-               : launch_halves(mx_dequantize_kernel<false, 1>, mx_dequantize_kernel<false, 2>, rows, per_row, s, c, sc,
-                               sp, rows, (int64_t)K, per_row, dst, ld, vec);
+               : launch_halves(mx_dequantize_kernel<false, 1>, four ? mx_dequantize_kernel<false, 4> : mx_dequantize_kernel<false, 2>,
+                               four ? 4 : 2, rows, per_row, s, c, sc, sp, rows, (int64_t)K, per_row, dst, ld, vec);
 }
 
 }  // namespace ls

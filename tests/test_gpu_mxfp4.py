@@ -89,6 +89,30 @@ def test_quantize_extreme_magnitudes_and_non_finite_blocks():
     assert np.array_equal(got.astype(np.float64), mx.decode(want_c, want_s, K), equal_nan=True)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("pad", [0, 8, 24])
+def test_a_large_matrix_has_the_bits_of_its_parts(f32, pad):
+    """Large calls give a thread several rows: the last block's are not all there."""
+    rows, K = 17003, 2600
+    dt = torch.float32 if f32 else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(41)
+    src = torch.randn((rows, K + pad), generator=g, device="cuda").to(dt)
+    codes, scales = _empty(rows + 1, K)
+    codes[rows:], scales[rows:] = 7, 7
+    L.lsk_mxfp4_quantize(src, rows, K, codes, scales, ld=K + pad)
+    back = torch.full((rows, K + pad), 7.0, dtype=dt, device="cuda")
+    L.lsk_mxfp4_dequantize(codes, scales, rows, K, back, ld=K + pad)
+    assert bool((codes[rows:] == 7).all()) and bool((scales[rows:] == 7).all()) and bool((back[:, K:] == 7).all())
+    for r0 in range(0, rows, 1000):
+        n = min(1000, rows - r0)
+        c, s = _empty(n, K)
+        L.lsk_mxfp4_quantize(src[r0:r0 + n], n, K, c, s, ld=K + pad)
+        b = torch.empty((n, K), dtype=dt, device="cuda")
+        L.lsk_mxfp4_dequantize(c, s, n, K, b)
+        assert torch.equal(c, codes[r0:r0 + n]) and torch.equal(s, scales[r0:r0 + n])
+        assert torch.equal(b, back[r0:r0 + n, :K])
+
+
 # ------------------------------------------------------------------ 4-bit x 4-bit
 def _sum_tol(absum, K):
     """fp32 sums: K/32 additions, each within 2^-22 of the sum of magnitudes."""
