@@ -1,11 +1,12 @@
 // C[M,N] = sum_k A[m,k] B[n,k] with both operands MXFP4, on the sm_103a tensor cores: kind::mxf4, 64 values of K
 // an instruction, codes packed in shared memory as they lie in global memory, fp32 sums.
 //
-// What bounds it: shared memory, at 128 bytes a clock. A stage's rows are written once and read by the products once
-// for every tile, so a tile's shape decides: a pair of CTAs shares a tile of 256 x BQ (cta_group::2), each SM loads 128
-// rows of A and BQ / 2 of B for 128 x BQ outputs. With 256 x 224 a stage writes 31 KB and its products read 45: about
-// 600 of the 690 clocks that it takes (its products alone would take 320). One CTA with 128 x 192 tiles wrote 41 KB
-// for 24576 outputs in place of 28672. A wider tile leaves no TMEM for a second accumulator.
+// What bounds it: an SM takes in about 60 bytes a clock (a stage of 28.7 KB took 476 clocks with the products and the
+// scales left out), and at 4 bits the products of a stage are shorter than its loads. A tile's shape decides: a pair of
+// CTAs shares a tile of 256 x BQ (cta_group::2), each SM loads 128 rows of A and BQ / 2 of B for 128 x BQ outputs. With
+// 256 x 224 a stage is 31 KB of rows and 3 KB of scales, about 560 of the 690 clocks that it takes (products: 450; the
+// tensor pipe is active 66 %). One CTA with 128 x 192 tiles loaded 41 KB for 24576 outputs in place of 28672. A wider
+// tile leaves no TMEM for a second accumulator.
 //
 // Structure (persistent pairs, one CTA an SM): warp 0 loads the CTA's operand rows by TMA (128-byte rows = 256
 // values of K, 128-byte swizzle) into a ring of stages; warps 2 to 5 bring the scales, 32 bytes of a row at a time,
