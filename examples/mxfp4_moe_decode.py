@@ -103,18 +103,21 @@ class Stack:
                       stream=self.compute)
 
     def logits(self, x):
-        """The head's product for the rows of x, fp32, on the compute stream."""
+        """The head's product for the rows of x, fp32; ordered with the caller's stream on both sides."""
         M, H = x.shape
+        self.compute.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(self.compute):
             out = torch.empty((M, self.vocab), dtype=torch.float32, device="cuda")
             if M <= FEW:
                 L.lsk_gemm_bf16_mxfp4(x, *self.head, out, M, self.vocab, H)
             else:
                 L.lsk_gemm_mxfp4(*quantise(x), *self.head, out, M, self.vocab, H)
+        torch.cuda.current_stream().wait_stream(self.compute)
         return out
 
     def step(self, x):
         """x [T, H] bf16, T <= 64 -> the head's logits [T, vocab], layers streamed."""
+        self.compute.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(self.compute):
             bufs = [x, torch.empty_like(x), torch.empty_like(x)]
             logits = torch.empty((x.shape[0], self.lay.E), dtype=torch.float32, device="cuda")
