@@ -94,13 +94,17 @@ struct alignas(16) Routing {
     float sel_w[MAX_ROWS];
     float row_w[MAX_ROWS];        // weight and token of a row
     int16_t chunk_row[MAX_ROWS];  // first row, expert and rows of each chunk of up to TOK rows
-    uint8_t sel[MAX_ROWS];
+    uint16_t sel[MAX_ROWS];       // NONE: chosen for want of a better one, takes no part
     uint8_t row_t[MAX_ROWS];
     uint8_t chunk_e[MAX_ROWS];
     uint8_t chunk_n[MAX_ROWS];
     int n_chunks;
     int pad[3];                   // 16-byte multiples: what follows is read as float4
 };
+
+// A chosen logit of -infinity has weight 0: its pair gets no row, so that its expert is not read and what the expert or
+// the token holds (0 times infinity, NaN) cannot reach the sums.
+constexpr uint16_t NONE = 0xffffu;
 
 // Order of floats as unsigned numbers; -0 as 0, NaN as -infinity. Never 0.
 constexpr uint32_t KEY_LOWEST = 0x007fffffu;  // of -infinity
@@ -160,7 +164,7 @@ __device__ __forceinline__ void route_tokens(Routing& r, const FewParams& p, int
         float sum = 0.f;
         for (int j = 0; j < p.k; ++j) sum += __shfl_sync(0xffffffffu, ex, j, W);
         if (l < p.k && t < p.T) {
-            r.sel[t * p.k + l] = (uint8_t)mine;
+            r.sel[t * p.k + l] = v == -INFINITY ? NONE : (uint16_t)mine;
             r.sel_w[t * p.k + l] = sum == 0.f ? 0.f : ex / sum;
         }
     }
@@ -196,7 +200,7 @@ __device__ __forceinline__ void route_ranks(Routing& r, const FewParams& p) {
         const int c = e & 3;
         const int before = n0 + n1 + n2 + n3 + (c > 0 && o.x == key) + (c > 1 && o.y == key) + (c > 2 && o.z == key);
         if (before < p.k) {
-            r.sel[t * p.k + before] = (uint8_t)e;
+            r.sel[t * p.k + before] = v == -INFINITY ? NONE : (uint16_t)e;
             chosen[t * p.k + before] = v;
         }
     }
@@ -225,12 +229,13 @@ __device__ __forceinline__ void small_tables(Routing& r, const FewParams& p) {
     uint32_t* used = &r.mask[MAX_E - 4][0];  // a bit for each expert
     if (i < 8) used[i] = 0;
     __syncthreads();
-    if (i < n) atomicOr(&used[r.sel[i] >> 5], 1u << (r.sel[i] & 31));
+    const int e = i < n ? r.sel[i] : NONE;
+    if (e != NONE) atomicOr(&used[e >> 5], 1u << (e & 31));
     __syncthreads();
-    if (i < n) {
-        const int e = r.sel[i], t = i / p.k;
+    if (e != NONE) {
+        const int t = i / p.k;
         int row = 0, same = 0, first = 0;
-        for (int j = 0; j < n; ++j) {  // pairs are in order of their tokens
+        for (int j = 0; j < n; ++j) {  // pairs are in order of their tokens; NONE is above every expert
             const int o = r.sel[j];
             row += o < e || (o == e && j < i);
             first += o < e;
@@ -261,7 +266,8 @@ __device__ __forceinline__ void small_tables(Routing& r, const FewParams& p) {
 __device__ __forceinline__ void large_tables(Routing& r, const FewParams& p, int warp, int lane) {
     for (int e = threadIdx.x; e < MAX_E; e += THREADS) r.mask[e][0] = r.mask[e][1] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < p.T * p.k; i += THREADS) atomicOr(&r.mask[r.sel[i]][i / p.k >> 5], 1u << (i / p.k & 31));
+    for (int i = threadIdx.x; i < p.T * p.k; i += THREADS)
+        if (r.sel[i] != NONE) atomicOr(&r.mask[r.sel[i]][i / p.k >> 5], 1u << (i / p.k & 31));
     __syncthreads();
     uint32_t n = 0, chunks = 0, sum = 0;
     const int e = 32 * warp + lane;
@@ -297,6 +303,7 @@ __device__ __forceinline__ void large_tables(Routing& r, const FewParams& p, int
     __syncthreads();
     for (int i = threadIdx.x; i < p.T * p.k; i += THREADS) {
         const int t = i / p.k, x = r.sel[i];
+        if (x == NONE) continue;
         const uint32_t below = (1u << (t & 31)) - 1u;
         const int rank = t < 32 ? __popc(r.mask[x][0] & below) : __popc(r.mask[x][0]) + __popc(r.mask[x][1] & below);
         r.row_t[r.first[x] + rank] = (uint8_t)t;
@@ -753,6 +760,18 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
             }
         }
     } else if (warp < SECOND_MMA) {
+        auto write_tile = [&](int tile) {  // a thread has a row of its own: no barrier
+            const int r = tile * TILE + row;
+            for (int t = 0; t < p.T; ++t) {
+                const int64_t at = (int64_t)t * p.H + r;
+                if (r < p.H) {
+                    const float o = sums[t * TILE + row] + (p.resid ? p.resid[at] : __bfloat162float(p.x[at]));
+                    p.out[at] = __float2bfloat16_rn(o);
+                    if (p.out32) p.out32[at] = o;
+                }
+                sums[t * TILE + row] = 0.f;
+            }
+        };
         for (int u = 0; u < down.units; ++u) {
             float v[TOK];
             take(v, MX ? H_TERMS : 1, base_it + u * down.ks, down.ks);
@@ -763,19 +782,10 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
                     float* to = sums + rt.row_t[row0 + j] * TILE + row;
                     *to = fmaf(rt.row_w[row0 + j], v[j], *to);
                 }
-            if (p.shares == 1 && (u + 1) % own == 0) {  // a thread has a row of its own: no barrier
-                const int r = down_tile(u) * TILE + row;
-                for (int t = 0; t < p.T; ++t) {
-                    const int64_t at = (int64_t)t * p.H + r;
-                    if (r < p.H) {
-                        const float o = sums[t * TILE + row] + (p.resid ? p.resid[at] : __bfloat162float(p.x[at]));
-                        p.out[at] = __float2bfloat16_rn(o);
-                        if (p.out32) p.out32[at] = o;
-                    }
-                    sums[t * TILE + row] = 0.f;
-                }
-            }
+            if (p.shares == 1 && (u + 1) % own == 0) write_tile(down_tile(u));
         }
+        if (p.shares == 1 && own == 0)  // no token has an expert
+            for (int i = 0; i < out_tiles; ++i) write_tile(cta + i * grid);
     }
     fence_before_sync();
     __syncthreads();

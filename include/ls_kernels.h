@@ -246,8 +246,9 @@ typedef struct lsk_moe_experts {
  * with sel and w as lsk_moe_route gives them from logits_dev [T, E] fp32 (the k largest, ties to the
  * lower expert, softmax over the chosen), r = resid_dev [T, H] fp32, or x_dev when that is NULL.
  * x_dev [T, H] bf16 (16-byte aligned), out_dev [T, H] bf16; out32_dev (may be NULL) gets the fp32
- * result. A NaN logit counts as the lowest one and makes its token NaN if it is chosen; a token
- * whose logits are all -infinity gets no expert (out = r). Sums are fp32 in a fixed order. With bf16
+ * result. A NaN logit counts as the lowest one and makes its token NaN if it is chosen. An expert chosen with a
+ * logit of -infinity takes no part: it is not read, and a token that has no other gets out = r, whatever x holds
+ * (lsk_moe_route gives such an expert weight 0, and NaN weights to a token that has no other). Sums are fp32 in a fixed order. With bf16
  * experts the hidden activation is rounded once, to bf16. With MXFP4 experts it keeps twelve bits
  * and x all eight (as in lsk_gemm_bf16_mxfp4), relative to the largest of 32 neighbours. T <= 64, E <= 256, k <= 8 (LS_ERR_UNSUPPORTED above:
  * lsk_moe_route to lsk_moe_combine serve more tokens), H and F multiples of 8. Takes scratch on
