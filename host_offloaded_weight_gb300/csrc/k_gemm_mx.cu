@@ -5,7 +5,8 @@
 // block of 32:
 //   a = t1 2^s1 + t2 2^s2,  s1 = floor(log2 max|a|) - 7,  s2 = s1 - 5.
 // t1 is a 2^-s1 to the nearest, t2 the rest: exact for every value down to 2^-13 of its block's largest, below that
-// within 2^-22 of the largest. Both terms are columns of the same product and are added in fp32 in the epilogue.
+// within 2^-22 of the largest. (A block that reaches 2^127: t1 is cut, so that t1 2^s1 stays finite, s2 = s1 - 4, and the
+// smallest values are within 2^-21.) Both terms are columns of the same product and are added in fp32 in the epilogue.
 //
 // Structure (one persistent CTA per SM): warp 0 loads the weights by TMA, which unpacks them to a byte a value
 // (128-byte rows, 128-byte swizzle), into a ring of stages; the warps after warp 1 bring the scales into the stage

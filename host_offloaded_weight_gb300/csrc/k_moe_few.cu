@@ -366,15 +366,15 @@ __device__ __forceinline__ void write_h(const FewParams& p, const Smem& sm, int 
         const float g = sm.turn[c][j], h = g / (1.f + __expf(-g)) * sm.turn[UP_F + c][j];
         if (MX) {  // a warp has one block of 32: each term takes four bits of what the ones before leave
             const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu) >> 23;
-            float rest = h;
+            float rest = h * __uint_as_float((254 - min(term_byte(e, 0), 253u)) << 23);  // in units of the next term's scale
 #pragma unroll
             for (int i = 0; i < H_TERMS; ++i) {
-                const uint32_t low = 7 + 5 * i, b = e == 255 ? 255 : e < low ? 0 : e - low;
+                const uint32_t b = term_byte(e, i);
                 uint16_t t;
                 uint32_t back;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t) : "f"(0.f), "f"(rest * __uint_as_float((254 - min(b, 253u)) << 23)));
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t) : "f"(0.f), "f"(i ? rest : first_term(rest, e)));
                 asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(t));
-                rest -= __half2float(__ushort_as_half((unsigned short)(back & 0xffffu))) * e8m0_to_float(min(b, 254u));
+                rest = (rest - __half2float(__ushort_as_half((unsigned short)(back & 0xffffu)))) * pow2(b - term_byte(e, i + 1));
                 p.h[(i * R + row0 + j) * p.h_cols + f] = e == 255 ? 0 : (uint8_t)t;
                 if ((c & 31) == 0) p.h_scale[(i * R + row0 + j) * p.h_scale_pitch + f / 32] = (uint8_t)b;
             }

@@ -298,8 +298,22 @@ __device__ __forceinline__ uint4 row8(const __nv_bfloat16* row, int k, int K, in
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The two E4M3 terms of eight values and the scale bytes of their block (a 2^-s1 to the nearest, then
-// the rest 2^-s2). Four
+// The first term of a block whose largest magnitude has exponent field 254 is cut to its four bits: rounded up, it could
+// be 2^128, whose products with weights of 1 and more are infinite. It leaves up to twice as much, so the next terms'
+// scales are a bit larger.
+constexpr uint32_t TOP_FIELD = 254;
+__device__ __forceinline__ float first_term(float v, uint32_t field) {
+    return __uint_as_float(__float_as_uint(v) & (field == TOP_FIELD ? 0xfff00000u : 0xffffffffu));
+}
+// The scale byte of term i: the field - 127 - 7 - 5 i as a byte, not below 0; a block with a NaN or an infinity reads as NaN.
+__device__ __forceinline__ uint32_t term_byte(uint32_t field, int i) {
+    const uint32_t low = 7 + 5 * i - (i > 0 && field == TOP_FIELD ? 1 : 0);
+    return field == 255 ? 255 : field < low ? 0 : field - low;
+}
+__device__ __forceinline__ float pow2(uint32_t e) { return __uint_as_float((127 + e) << 23); }
+
+// The two E4M3 terms of eight values and the scale bytes of their block (a 2^-s1 to the nearest, then the rest 2^-s2,
+// exact in units of 2^s1: an unscaled first term could overflow). Four
 // neighbouring lanes hold a block; every lane of the warp takes part.
 __device__ __forceinline__ void split8(uint4 raw, uint2& o1, uint2& o2, uint32_t& b1, uint32_t& b2) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -309,22 +323,19 @@ __device__ __forceinline__ void split8(uint4 raw, uint2& o1, uint2& o2, uint32_t
     m = max(m & 0xffffu, m >> 16);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // s1 = e - 127 - 7 and s2 = s1 - 5 as bytes, not below 0; a block with a NaN or an infinity reads as NaN
     const uint32_t e = m >> 7;
-    b1 = e == 255 ? 255 : e < 7 ? 0 : e - 7;
-    b2 = e == 255 ? 255 : e < 12 ? 0 : e - 12;
-    const float f1 = __uint_as_float((254 - min(b1, 253u)) << 23), u1 = e8m0_to_float(min(b1, 254u));
-    const float f2 = __uint_as_float((254 - min(b2, 253u)) << 23);
+    b1 = term_byte(e, 0);
+    b2 = term_byte(e, 1);
+    const float f1 = __uint_as_float((254 - min(b1, 253u)) << 23), f2 = pow2(b1 - b2);
     uint16_t t1[4], t2[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float x = __uint_as_float(w[j] << 16), y = __uint_as_float(w[j] & 0xffff0000u);
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t1[j]) : "f"(y * f1), "f"(x * f1));
+        const float x = __uint_as_float(w[j] << 16) * f1, y = __uint_as_float(w[j] & 0xffff0000u) * f1;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t1[j]) : "f"(first_term(y, e)), "f"(first_term(x, e)));
         uint32_t h;
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(t1[j]));
         const float2 d = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        const float rx = x - d.x * u1, ry = y - d.y * u1;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t2[j]) : "f"(ry * f2), "f"(rx * f2));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(t2[j]) : "f"((y - d.y) * f2), "f"((x - d.x) * f2));
     }
     o1 = make_uint2(t1[0] | (uint32_t)t1[1] << 16, t1[2] | (uint32_t)t1[3] << 16);
     o2 = make_uint2(t2[0] | (uint32_t)t2[1] << 16, t2[2] | (uint32_t)t2[3] << 16);

@@ -215,7 +215,7 @@ ls_status lsk_gemm_mxfp4(const void* a_codes_dev, const void* a_scales_dev, cons
 /* C[M,N] = A[M,K] B[N,K]^T with A bf16 (lda >= K elements between rows) and B in MXFP4, fp32
  * sums, C dense bf16 (fp32 when c_f32 != 0). Any M; made for few tokens (M = 1 upwards), where it streams the
  * weights once at 17/32 byte a value. A keeps its eight bits: values down to 2^-13 of the
- * largest of their block of 32 enter exactly, smaller ones within 2^-22 of that largest. A NaN or an
+ * largest of their block of 32 enter exactly, smaller ones within 2^-22 of that largest (2^-21 where it is 2^127 or more). A NaN or an
  * infinity in a row of A makes that row of C NaN. More than 8 rows take scratch on `stream`
  * from the library's pool, as lsk_gemm_bf16 does (LS_ERR_OOM if refused). */
 ls_status lsk_gemm_bf16_mxfp4(const void* A_dev, int64_t lda, const void* b_codes_dev, const void* b_scales_dev,
