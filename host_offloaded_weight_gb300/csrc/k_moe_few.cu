@@ -406,8 +406,9 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     const uint32_t full0 = smem_addr(sm.full), empty0 = smem_addr(sm.empty), acc_full0 = smem_addr(sm.acc_full),
                    acc_empty0 = smem_addr(sm.acc_empty), done = smem_addr(&sm.done);
     __shared__ volatile int stop;
-    // Thread 0 waits for the other CTAs at the meeting and can come back from it apart from its warp. A copy issued
-    // under elect_one() by a warp in two parts is issued twice, so the first four warps are the epilogue's.
+    // A thread that waits for the other CTAs at the meeting (thread 0) can come back from it apart from its warp, and a
+    // copy issued under elect_one() by a warp in two parts is issued twice. Every warp joins again after the meeting;
+    // the first four warps are the epilogue's, which issue none.
     const int hw_warp = uniform_warp(), lane = threadIdx.x & 31;
     const int warp = hw_warp < 4 ? FIRST_EPI + hw_warp : hw_warp < SECOND_MMA ? hw_warp - 4 : hw_warp;
 
@@ -716,6 +717,7 @@ __global__ void __launch_bounds__(THREADS, 1) moe_few_kernel(const __grid_consta
     // ---- the meeting: h is complete
     __syncwarp();
     cooperative_groups::this_grid().sync();
+    __syncwarp();  // whichever thread the barrier lets poll: what follows is issued by whole warps
 
     // ---- down
     if (warp == 0) {
