@@ -1273,12 +1273,9 @@ bool cached_tmap(CUtensorMap* out, const void* ptr, int64_t rows, int64_t cols, 
 template <int EPI, bool DUAL, bool GROUPED>
 cudaError_t launch_t(const GemmParams& p, int grid, cudaStream_t s) {
     auto kern = gemm_bf16_tc<EPI, DUAL, GROUPED>;
-    static bool attr_set = false;
-    if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-        if (e != cudaSuccess) return e;
-        attr_set = true;
-    }
+    static SmemAllowance allowed;
+    const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), SMEM_BYTES);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(NUM_THREADS);
@@ -1295,13 +1292,9 @@ cudaError_t launch_t(const GemmParams& p, int grid, cudaStream_t s) {
 template <int EPI, bool DUAL, int BN, bool ONE = false>
 cudaError_t launch_t2(const GemmParams& p, int clusters, cudaStream_t s) {
     auto kern = gemm_bf16_tc2<EPI, DUAL, BN, ONE>;
-    static bool attr_set = false;
-    if (!attr_set) {
-        cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s2_smem_bytes(EPI, BN, ONE));
-        if (e != cudaSuccess) return e;
-        attr_set = true;
-    }
+    static SmemAllowance allowed;
+    const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), s2_smem_bytes(EPI, BN, ONE));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters);
     cfg.blockDim = dim3(s2_threads(EPI));
@@ -1388,13 +1381,13 @@ int gemm_pair_tile_n(int64_t M, int64_t N) {
 }
 
 int gemm_num_sms() {
-    static int n = 0;
-    if (!n) {
-        int dev = 0;
-        cudaGetDevice(&dev);
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (n <= 0) n = 1;
-    }
+    static std::atomic<int> count[SmemAllowance::DEVICES];
+    int dev = 0, n = 0;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < SmemAllowance::DEVICES;
+    if (known) n = count[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 1;
+    if (known) count[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

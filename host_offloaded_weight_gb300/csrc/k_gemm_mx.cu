@@ -541,8 +541,9 @@ template <int MODE, int BQ>
 cudaError_t launch(const MxParams& p, cudaStream_t s) {
     auto kern = gemm_mx_kernel<MODE, BQ>;
     using C = Cfg<MODE, BQ>;
-    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (attr != cudaSuccess) return attr;
+    static SmemAllowance allowed;
+    const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), C::SMEM);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.splits > 1 ? p.tiles * p.splits : std::min(p.tiles, gemm_num_sms()));
     cfg.blockDim = dim3(C::THREADS);

@@ -396,8 +396,9 @@ template <int BQ>
 cudaError_t launch(PairParams& p, const void* b_codes, int64_t pitch, cudaStream_t s) {
     auto kern = gemm_mx4_pair_kernel<BQ>;
     using C = Cfg<BQ>;
-    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (attr != cudaSuccess) return attr;
+    static SmemAllowance allowed;
+    const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), C::SMEM);
+    if (e != cudaSuccess) return e;
     if (!mx_map_rows(&p.map_b, b_codes, p.N, pitch, BQ / 2, false)) return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)p.tiles_m * ((p.N + BQ - 1) / BQ);
     if (tiles > 0x3fffffffll) return cudaErrorInvalidValue;

@@ -873,8 +873,9 @@ bool map_h(CUtensorMap* m, bool mx, const void* ptr, int64_t rows, int64_t cols)
 template <bool MX>
 cudaError_t launch(const FewParams& p, int grid, cudaStream_t s) {
     auto kern = moe_few_kernel<MX>;
-    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<MX>(MAX_T));
-    if (attr != cudaSuccess) return attr;
+    static SmemAllowance allowed;
+    const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), smem_bytes<MX>(MAX_T));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(THREADS);

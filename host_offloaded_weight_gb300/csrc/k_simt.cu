@@ -70,12 +70,10 @@ cudaError_t launch_linear_gelu_f32(const float* x, const float* w, const float* 
     if (T <= 0) return cudaSuccess;
     size_t smem = (size_t)SIMT_MAX_T * H * sizeof(float);
     if (smem > 200 * 1024) return cudaErrorInvalidValue;
-    static size_t attr = 0;
-    if (smem > 48 * 1024 && smem > attr) {
-        cudaError_t e = cudaFuncSetAttribute(linear_gelu_f32_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemAllowance allowed;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(linear_gelu_f32_kernel), (int)smem);
         if (e != cudaSuccess) return e;
-        attr = smem;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((F + SIMT_WARPS - 1) / SIMT_WARPS);

@@ -4,6 +4,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
+
 namespace ls {
 
 // ---------------------------------------------------------------- copy path
@@ -91,7 +94,27 @@ struct GemmDesc {
 
 // max_ctas <= 0: one CTA per SM.
 cudaError_t launch_gemm_bf16(const GemmDesc& d, int max_ctas, cudaStream_t s);
-int gemm_num_sms();
+int gemm_num_sms();  // of the current device
+
+// Dynamic shared memory above the default is allowed to a kernel for each device apart: what a kernel was allowed so
+// far, by device. A refusal is not kept.
+struct SmemAllowance {
+    static constexpr int DEVICES = 64;
+    std::atomic<int> bytes[DEVICES] = {};
+    std::mutex mu;
+    cudaError_t ensure(const void* kernel, int need) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool known = dev >= 0 && dev < DEVICES;
+        if (known && bytes[dev].load(std::memory_order_acquire) >= need) return cudaSuccess;
+        std::lock_guard<std::mutex> g(mu);  // a smaller need must not replace a larger one
+        if (known && bytes[dev].load(std::memory_order_relaxed) >= need) return cudaSuccess;
+        const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, need);
+        if (set == cudaSuccess && known) bytes[dev].store(need, std::memory_order_release);
+        return set;
+    }
+};
 // Tile width (output columns) of the dense pair-CTA GEMM for an M x N output.
 int gemm_pair_tile_n(int64_t M, int64_t N);
 // K slices of a dense single-CTA GEMM (M <= 128, not the gate/up pair): 1 when it is not split.
