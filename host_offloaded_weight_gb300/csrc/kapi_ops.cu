@@ -95,16 +95,17 @@ ls_status lsk_moe_few(const void* x, const float* resid, const float* logits, co
     if (T > 64 || E > 256 || k > 8) return LS_ERR_UNSUPPORTED;
     if (T == 0) return LS_OK;
     const bool mx = w->mxfp4 != 0;
-    const uintptr_t al = mx ? 32 : 16;
+    const int al = mx ? 32 : 16;
     if (!x || !logits || !out || !w->gate || !w->up || !w->down || !aligned(x, 16) || !aligned(resid, 4) ||
         !aligned(logits, 4) || !aligned(out, 2) || !aligned(out32, 4) || !aligned(w->gate, al) || !aligned(w->up, al) ||
         !aligned(w->down, al))
         return LS_ERR_INVALID_ARG;
     const int64_t up_bytes = (int64_t)F * (mx ? mx_code_pitch(H) : 2ll * H);
     const int64_t down_bytes = (int64_t)H * (mx ? mx_code_pitch(F) : 2ll * F);
-    // a stride may be anything with one expert; the tensor copies want multiples of 16 bytes below 2^40
+    // a stride may be anything with one expert; the tensor copies want multiples of 16 bytes (of 32 where they unpack
+    // 4-bit codes) below 2^40
     const int64_t gs = E == 1 ? up_bytes : w->gate_stride, ds = E == 1 ? down_bytes : w->down_stride;
-    if (gs < up_bytes || ds < down_bytes || (gs % 16) || (ds % 16) || gs >= (1ll << 40) || ds >= (1ll << 40))
+    if (gs < up_bytes || ds < down_bytes || (gs % al) || (ds % al) || gs >= (1ll << 40) || ds >= (1ll << 40))
         return LS_ERR_INVALID_ARG;
     MoeFewDesc d;
     if (mx) {

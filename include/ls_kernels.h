@@ -224,8 +224,9 @@ ls_status lsk_gemm_bf16_mxfp4(const void* A_dev, int64_t lda, const void* b_code
 /* The experts of one MoE layer: gate and up [F, H] and down [H, F] of each, row-major, an
  * expert's matrix a fixed number of bytes after the one before (the gate and up matrices
  * alike), so that stacked tensors [E, F, H] and expert-major blobs both fit. bf16, or MXFP4
- * (mxfp4 != 0: the pointers are codes, with the scales beside them). Strides are multiples of 16
- * bytes; matrices 16-byte aligned (32 for MXFP4 codes). */
+ * (mxfp4 != 0: the pointers are codes, with the scales beside them). Strides of bf16
+ * matrices and of scales are multiples of 16 bytes, those of MXFP4 codes of 32; matrices and scales are 16-byte
+ * aligned, codes 32-byte aligned. With one expert the strides are not read. */
 typedef struct lsk_moe_experts {
     int32_t mxfp4;
     int32_t reserved;

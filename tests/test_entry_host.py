@@ -118,3 +118,18 @@ def test_grids_are_sized_for_the_current_device(lib):
         lib.fake_set_device(device)
         assert lib.lsk_num_sms() == sms
         assert CALLS["4-bit product, wide tiles"](lib) == L.LS_OK and lib.fake_last_grid() <= sms
+
+
+@pytest.mark.parametrize("mx,gaps,status", [
+    (True, {"gap": 32}, L.LS_OK), (True, {"down_gap": 96}, L.LS_OK), (True, {"scale_gap": 16}, L.LS_OK),
+    (True, {"gap": 16}, L.LS_ERR_INVALID_ARG), (True, {"down_gap": 48}, L.LS_ERR_INVALID_ARG),
+    (True, {"scale_gap": 8}, L.LS_ERR_INVALID_ARG), (True, {"gap": -32}, L.LS_ERR_INVALID_ARG),
+    (False, {"gap": 16}, L.LS_OK), (False, {"down_gap": 48}, L.LS_OK), (False, {"gap": 8}, L.LS_ERR_INVALID_ARG),
+    (False, {"down_gap": -16}, L.LS_ERR_INVALID_ARG)])
+def test_strides_between_experts(lib, mx, gaps, status):
+    """Packed codes are unpacked by tensor copies whose strides are multiples of 32 bytes: refused as arguments, before
+    scratch is taken or a tensor map is made."""
+    assert moe(lib, mx, **gaps) == status
+    if status != L.LS_OK:
+        assert lib.fake_encodes() == lib.fake_pool_allocations() == lib.fake_launches() == 0
+    assert moe(lib, mx, E=1, k=1, **gaps) == L.LS_OK, "one expert's strides are not read"
