@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
+import sys
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblstream.so")
@@ -156,7 +158,7 @@ _sig = {
     "lsk_mxfp4_dequantize": (_I32, [_P, _P, _I64, _I32, _P, _I32, _I64, _P]),
     "lsk_gemm_mxfp4": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "lsk_gemm_bf16_mxfp4": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
-    "lsk_moe_few": (_I32, [_P, _P, _P, C.POINTER(lsk_moe_experts), _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "lsk_moe_few": (_I32, [_P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "ls_helper_share": (C.c_double, [_I64]),
     "ls_host_alloc": (_I32, [_U64, C.POINTER(_P)]),
     "ls_host_free": (_I32, [_P]),
@@ -594,48 +596,173 @@ def lsk_mxfp4_scale_pitch(K: int) -> int:
     return _lib.lsk_mxfp4_scale_pitch(K)
 
 
+def _dense(t, what: str):
+    f = getattr(t, "is_contiguous", None)
+    if not (f() if f is not None else t.flags.c_contiguous):
+        raise ValueError(f"{what} is not dense")
+
+
+def _values(t, f32: int, what: str) -> int:
+    """Address of a dense bf16 (f32 = 0) or float32 (1) tensor; raw addresses and None pass."""
+    if getattr(t, "dtype", None) is not None:
+        if _is_f32(t) != f32:
+            raise TypeError(f"{what} has to be {'float32' if f32 else 'bf16'}, not {t.dtype}")
+        _dense(t, what)
+    return _ptr(t)
+
+
+def _rows(t, ld, what: str):
+    """A matrix's rows: dense, or ld elements apart and dense in themselves."""
+    if getattr(t, "dtype", None) is None:
+        return
+    if ld is None:
+        _dense(t, what)
+    elif hasattr(t, "stride") and t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the rows of {what} are not dense")
+
+
+def _bytes(t, what: str) -> int:
+    """Address of a dense tensor of codes or scales (a byte each)."""
+    if getattr(t, "dtype", None) is not None:
+        if t.itemsize != 1:
+            raise TypeError(f"{what} has to be bytes, not {t.dtype}")
+        _dense(t, what)
+    return _ptr(t)
+
+
+def _expert_rows(t, what: str):
+    """Experts may lie apart; the rows of each are dense."""
+    if not t.is_contiguous():
+        shape, stride = t.shape, t.stride()
+        if len(shape) < 2 or (stride[-1] != 1 and shape[-1] > 1) or (stride[-2] != shape[-1] and shape[-2] > 1):
+            raise ValueError(f"an expert's rows of {what} are not dense")
+
+
+# The usual arguments (torch tensors of the right types, dense) are recognised in few steps, since a check of each by the
+# functions above would cost a one-token layer 2 us of its call; all others take those functions.
+_BF16 = _F32 = _U8 = None
+
+
+def _bind_types():
+    global _BF16, _F32, _U8
+    torch = sys.modules.get("torch")
+    if torch is not None:
+        _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+
+
+def _conversion(values, ld, codes, scales, what: str):
+    """Addresses of a conversion's matrix, codes and scales."""
+    try:
+        usual = (codes.dtype is _U8 and scales.dtype is _U8 and codes.is_contiguous() and scales.is_contiguous()
+                 and (values.is_contiguous() if ld is None else values.stride(-1) == 1))
+    except (AttributeError, IndexError, TypeError):
+        usual = False
+    if usual:
+        return values.data_ptr(), codes.data_ptr(), scales.data_ptr()
+    _bind_types()
+    _rows(values, ld, what)
+    return _ptr(values), _bytes(codes, "codes"), _bytes(scales, "scales")
+
+
 def lsk_mxfp4_quantize(src, rows: int, K: int, codes, scales, ld: int | None = None, stream=None) -> int:
-    """src [rows, K] bf16 or float32, ld elements between rows (None = K)."""
-    return _check(_lib.lsk_mxfp4_quantize(_ptr(src), _is_f32(src), rows, K, K if ld is None else ld, _ptr(codes),
-                                          _ptr(scales), _stream(stream)))
+    """src [rows, K] bf16 or float32, ld elements between rows (None = K, dense)."""
+    v, c, s = _conversion(src, ld, codes, scales, "src")
+    return _check(_lib.lsk_mxfp4_quantize(v, _is_f32(src), rows, K, K if ld is None else ld, c, s, _stream(stream)))
 
 
 def lsk_mxfp4_dequantize(codes, scales, rows: int, K: int, dst, ld: int | None = None, stream=None) -> int:
-    """dst [rows, K] bf16 or float32, ld elements between rows (None = K)."""
-    return _check(_lib.lsk_mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, K, _ptr(dst), _is_f32(dst),
-                                            K if ld is None else ld, _stream(stream)))
+    """dst [rows, K] bf16 or float32, ld elements between rows (None = K, dense)."""
+    v, c, s = _conversion(dst, ld, codes, scales, "dst")
+    return _check(_lib.lsk_mxfp4_dequantize(c, s, rows, K, v, _is_f32(dst), K if ld is None else ld, _stream(stream)))
 
 
 def lsk_gemm_mxfp4(A_codes, A_scales, B_codes, B_scales, C_out, M: int, N: int, K: int, stream=None) -> int:
-    """C_out [M, N] bf16 or float32."""
-    return _check(_lib.lsk_gemm_mxfp4(_ptr(A_codes), _ptr(A_scales), _ptr(B_codes), _ptr(B_scales), _ptr(C_out),
-                                      _is_f32(C_out), M, N, K, _stream(stream)))
+    """C_out [M, N] bf16 or float32, dense."""
+    try:
+        f32 = 1 if C_out.dtype is _F32 else 0
+        usual = ((f32 or C_out.dtype is _BF16) and A_codes.dtype is _U8 and A_scales.dtype is _U8
+                 and B_codes.dtype is _U8 and B_scales.dtype is _U8 and A_codes.is_contiguous() and A_scales.is_contiguous()
+                 and B_codes.is_contiguous() and B_scales.is_contiguous() and C_out.is_contiguous())
+    except AttributeError:
+        usual = False
+    if usual:
+        ac, as_, bc, bs, c = A_codes.data_ptr(), A_scales.data_ptr(), B_codes.data_ptr(), B_scales.data_ptr(), C_out.data_ptr()
+    else:
+        _bind_types()
+        f32 = _is_f32(C_out)
+        ac, as_ = _bytes(A_codes, "A_codes"), _bytes(A_scales, "A_scales")
+        bc, bs, c = _bytes(B_codes, "B_codes"), _bytes(B_scales, "B_scales"), _values(C_out, f32, "C_out")
+    return _check(_lib.lsk_gemm_mxfp4(ac, as_, bc, bs, c, f32, M, N, K, _stream(stream)))
 
 
 def lsk_gemm_bf16_mxfp4(A, B_codes, B_scales, C_out, M: int, N: int, K: int, lda: int | None = None,
                         stream=None) -> int:
-    """A [M, K] bf16, lda elements between rows (None = K); C_out [M, N] bf16 or float32."""
-    return _check(_lib.lsk_gemm_bf16_mxfp4(_ptr(A), K if lda is None else lda, _ptr(B_codes), _ptr(B_scales),
-                                           _ptr(C_out), _is_f32(C_out), M, N, K, _stream(stream)))
+    """A [M, K] bf16, lda elements between rows (None = K, dense); C_out [M, N] bf16 or float32, dense."""
+    try:
+        f32 = 1 if C_out.dtype is _F32 else 0
+        usual = ((f32 or C_out.dtype is _BF16) and A.dtype is _BF16 and lda is None and A.is_contiguous()
+                 and B_codes.dtype is _U8 and B_scales.dtype is _U8 and B_codes.is_contiguous()
+                 and B_scales.is_contiguous() and C_out.is_contiguous())
+    except AttributeError:
+        usual = False
+    if usual:
+        lda, a, b, bs, c = K, A.data_ptr(), B_codes.data_ptr(), B_scales.data_ptr(), C_out.data_ptr()
+    else:
+        _bind_types()
+        if _is_f32(A):
+            raise TypeError("A has to be bf16, not float32")
+        _rows(A, lda, "A")
+        lda, f32 = K if lda is None else lda, _is_f32(C_out)
+        a, b, bs, c = _ptr(A), _bytes(B_codes, "B_codes"), _bytes(B_scales, "B_scales"), _values(C_out, f32, "C_out")
+    return _check(_lib.lsk_gemm_bf16_mxfp4(a, lda, b, bs, c, f32, M, N, K, _stream(stream)))
+
+
+_experts = struct.Struct("@2i10q").pack   # lsk_moe_experts, as bytes: a third of the time that the ctypes structure takes
 
 
 def lsk_moe_few(x, logits, gate, up, down, T: int, E: int, k: int, H: int, F: int, out, gate_scales=None,
                 up_scales=None, down_scales=None, resid=None, out32=None, stream=None) -> int:
-    """One MoE layer for T <= 64 tokens. gate, up [E, F, H] and down [E, H, F] bf16, or MXFP4 codes
-    [E, rows, code pitch] with their scales [E, rows, scale pitch]; an expert's rows are dense."""
+    """One MoE layer for T <= 64 tokens. x and out [T, H] bf16, logits [T, E], resid and out32 [T, H] float32, all dense.
+    gate, up [E, F, H] and down [E, H, F] bf16, or MXFP4 codes [E, rows, code pitch] with their scales
+    [E, rows, scale pitch]; an expert's rows are dense."""
+    mx = gate_scales is not None
+    if mx and (up_scales is None or down_scales is None):
+        raise ValueError("MXFP4 experts need the scales of all three matrices")
+    weight, size = (_U8, 1) if mx else (_BF16, 2)
+    if not (gate.dtype is weight and up.dtype is weight and down.dtype is weight
+            and gate.is_contiguous() and up.is_contiguous() and down.is_contiguous()):
+        _bind_types()
+        for t, what in ((gate, "gate"), (up, "up"), (down, "down")):
+            if (t.itemsize != 1) if mx else _is_f32(t):
+                raise TypeError(f"{what} has to be {'bytes (it has scales)' if mx else 'bf16'}, not {t.dtype}")
+            _expert_rows(t, what)
     # bytes between the experts of a stacked tensor
-    gs = gate.stride(0) * gate.itemsize
-    if up.stride(0) * up.itemsize != gs:
+    gs = gate.stride(0)
+    if up.stride(0) != gs:
         raise ValueError("gate and up need the same distance between experts")
-    if gate_scales is None:
-        w = lsk_moe_experts(0, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), gs, down.stride(0) * down.itemsize)
-    else:
-        if up_scales is None or down_scales is None:
-            raise ValueError("MXFP4 experts need the scales of all three matrices")
+    if mx:
+        if not (gate_scales.dtype is _U8 and up_scales.dtype is _U8 and down_scales.dtype is _U8
+                and gate_scales.is_contiguous() and up_scales.is_contiguous() and down_scales.is_contiguous()):
+            for t, what in ((gate_scales, "gate_scales"), (up_scales, "up_scales"), (down_scales, "down_scales")):
+                if t.itemsize != 1:
+                    raise TypeError(f"{what} has to be bytes, not {t.dtype}")
+                _expert_rows(t, what)
         ss = gate_scales.stride(0)
         if up_scales.stride(0) != ss:
             raise ValueError("gate and up need the same distance between experts")
-        w = lsk_moe_experts(1, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), gs, down.stride(0) * down.itemsize,
-                            gate_scales.data_ptr(), up_scales.data_ptr(), down_scales.data_ptr(), ss, down_scales.stride(0))
-    return _check(_lib.lsk_moe_few(_ptr(x), _ptr(resid), _ptr(logits), C.byref(w), T, E, k, H, F, _ptr(out),
-                                   _ptr(out32), _stream(stream)))
+        w = _experts(1, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), gs, down.stride(0), gate_scales.data_ptr(),
+                     up_scales.data_ptr(), down_scales.data_ptr(), ss, down_scales.stride(0))
+    else:
+        w = _experts(0, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), size * gs, size * down.stride(0), 0, 0, 0, 0, 0)
+    try:
+        usual = (x.dtype is _BF16 and out.dtype is _BF16 and logits.dtype is _F32 and x.is_contiguous()
+                 and out.is_contiguous() and logits.is_contiguous())
+    except AttributeError:
+        usual = False
+    if usual:
+        px, pl, po = x.data_ptr(), logits.data_ptr(), out.data_ptr()
+    else:
+        px, pl, po = _values(x, 0, "x"), _values(logits, 1, "logits"), _values(out, 0, "out")
+    pr = 0 if resid is None else _values(resid, 1, "resid")
+    p32 = 0 if out32 is None else _values(out32, 1, "out32")
+    return _check(_lib.lsk_moe_few(px, pr, pl, w, T, E, k, H, F, po, p32, _stream(stream)))
