@@ -736,9 +736,9 @@ def lsk_moe_few(x, logits, gate, up, down, T: int, E: int, k: int, H: int, F: in
             if (t.itemsize != 1) if mx else _is_f32(t):
                 raise TypeError(f"{what} has to be {'bytes (it has scales)' if mx else 'bf16'}, not {t.dtype}")
             _expert_rows(t, what)
-    # bytes between the experts of a stacked tensor
+    # bytes between the experts of a stacked tensor (one expert's are not read)
     gs = gate.stride(0)
-    if up.stride(0) != gs:
+    if up.stride(0) != gs and E > 1:
         raise ValueError("gate and up need the same distance between experts")
     if mx:
         if not (gate_scales.dtype is _U8 and up_scales.dtype is _U8 and down_scales.dtype is _U8
@@ -748,7 +748,7 @@ def lsk_moe_few(x, logits, gate, up, down, T: int, E: int, k: int, H: int, F: in
                     raise TypeError(f"{what} has to be bytes, not {t.dtype}")
                 _expert_rows(t, what)
         ss = gate_scales.stride(0)
-        if up_scales.stride(0) != ss:
+        if up_scales.stride(0) != ss and E > 1:
             raise ValueError("gate and up need the same distance between experts")
         w = _experts(1, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr(), gs, down.stride(0), gate_scales.data_ptr(),
                      up_scales.data_ptr(), down_scales.data_ptr(), ss, down_scales.stride(0))

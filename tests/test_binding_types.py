@@ -123,3 +123,16 @@ def test_packed_experts_are_the_headers_struct(tmp_path):
     subprocess.run(["gcc", "-I", include, str(src), "-o", exe], check=True)
     got = list(map(int, subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()))
     assert got == [ctypes.sizeof(L.lsk_moe_experts)] + [getattr(L.lsk_moe_experts, f).offset for f in fields]
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_one_experts_strides_are_free(mx):
+    """A layer of one expert, its matrices cut out of stacks of different kinds."""
+    def cut(rows, cols, gap, dt):
+        return torch.zeros((2, rows + gap, cols), dtype=dt)[:1, :rows]
+
+    dt, pitch = (U8, L.lsk_mxfp4_code_pitch) if mx else (BF16, lambda K: K)
+    x, out, lg = torch.zeros((2, H), dtype=BF16), torch.zeros((2, H), dtype=BF16), torch.zeros((2, 1))
+    scales = {n + "_scales": cut(rows, 16, i, U8) for i, (n, rows) in enumerate((("gate", F), ("up", F), ("down", H)))} if mx else {}
+    assert L.lsk_moe_few(x, lg, cut(F, pitch(H), 3, dt), cut(F, pitch(H), 0, dt), cut(H, pitch(F), 1, dt), 0, 1, 1, H, F, out,
+                         stream=0, **scales) == L.LS_OK
