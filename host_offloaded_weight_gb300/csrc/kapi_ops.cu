@@ -36,6 +36,8 @@ struct Scratch {
 };
 
 constexpr int32_t MX_MAX_K = 1 << 24;
+// Rows are counted in 32 bits, whole tiles of them (256 rows of A and 224 of B; 128 rows of A twice).
+constexpr int32_t MX_MAX_M = 0x7fffffff - 255, MX_MAX_N = 0x7fffffff - 223, ACT_MAX_M = (1 << 30) - 128;
 
 }  // namespace
 
@@ -66,6 +68,7 @@ ls_status lsk_mxfp4_dequantize(const void* codes, const void* scales, int64_t ro
 ls_status lsk_gemm_mxfp4(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales, void* C,
                          int32_t c_f32, int32_t M, int32_t N, int32_t K, void* stream) {
     if (M < 0 || N < 1 || K < 1 || K > MX_MAX_K) return LS_ERR_INVALID_ARG;
+    if (M > MX_MAX_M || N > MX_MAX_N) return LS_ERR_UNSUPPORTED;
     if (M == 0) return LS_OK;
     if (!a_codes || !a_scales || !b_codes || !b_scales || !C || !aligned(a_codes, 32) || !aligned(b_codes, 32) ||
         !aligned(a_scales, 16) || !aligned(b_scales, 16) || !aligned(C, c_f32 ? 4 : 2))
@@ -77,6 +80,7 @@ ls_status lsk_gemm_mxfp4(const void* a_codes, const void* a_scales, const void* 
 ls_status lsk_gemm_bf16_mxfp4(const void* A, int64_t lda, const void* b_codes, const void* b_scales, void* C,
                               int32_t c_f32, int32_t M, int32_t N, int32_t K, void* stream) {
     if (M < 0 || N < 1 || K < 1 || K > MX_MAX_K || lda < K) return LS_ERR_INVALID_ARG;
+    if (M > ACT_MAX_M) return LS_ERR_UNSUPPORTED;
     if (M == 0) return LS_OK;
     if (!A || !b_codes || !b_scales || !C || !aligned(A, 2) || !aligned(b_codes, 32) || !aligned(b_scales, 16) ||
         !aligned(C, c_f32 ? 4 : 2))

@@ -207,16 +207,18 @@ ls_status lsk_mxfp4_dequantize(const void* codes_dev, const void* scales_dev, in
                                void* dst_dev, int32_t dst_f32, int64_t ld, void* stream);
 
 /* C[M,N] = A[M,K] B[N,K]^T with both operands in MXFP4, fp32 sums, C dense bf16 (fp32 when
- * c_f32 != 0), any M, N and K. The activations' side is written by lsk_mxfp4_quantize. */
+ * c_f32 != 0). M up to 2^31 - 256 and N up to 2^31 - 224 (LS_ERR_UNSUPPORTED above). The activations'
+ * side is written by lsk_mxfp4_quantize. */
 ls_status lsk_gemm_mxfp4(const void* a_codes_dev, const void* a_scales_dev, const void* b_codes_dev,
                          const void* b_scales_dev, void* C_dev, int32_t c_f32, int32_t M, int32_t N, int32_t K,
                          void* stream);
 
 /* C[M,N] = A[M,K] B[N,K]^T with A bf16 (lda >= K elements between rows) and B in MXFP4, fp32
- * sums, C dense bf16 (fp32 when c_f32 != 0). Any M; made for few tokens (M = 1 upwards), where it streams the
- * weights once at 17/32 byte a value. A keeps its eight bits: values down to 2^-13 of the
- * largest of their block of 32 enter exactly, smaller ones within 2^-22 of that largest (2^-21 where it is 2^127 or more). A NaN or an
- * infinity in a row of A makes that row of C NaN. More than 8 rows take scratch on `stream`
+ * sums, C dense bf16 (fp32 when c_f32 != 0). M up to 2^30 - 128 (LS_ERR_UNSUPPORTED above); made for
+ * few tokens (M = 1 upwards), where it streams the weights once at 17/32 byte a value. A keeps its eight
+ * bits: values down to 2^-13 of the largest of their block of 32 enter exactly, smaller ones within 2^-22
+ * of that largest (2^-21 where it is 2^127 or more). A NaN or an infinity in a row of A makes that row
+ * of C NaN. More than 8 rows take scratch on `stream`
  * from the library's pool, as lsk_gemm_bf16 does (LS_ERR_OOM if refused). */
 ls_status lsk_gemm_bf16_mxfp4(const void* A_dev, int64_t lda, const void* b_codes_dev, const void* b_scales_dev,
                               void* C_dev, int32_t c_f32, int32_t M, int32_t N, int32_t K, void* stream);

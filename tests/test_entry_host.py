@@ -133,3 +133,19 @@ def test_strides_between_experts(lib, mx, gaps, status):
     if status != L.LS_OK:
         assert lib.fake_encodes() == lib.fake_pool_allocations() == lib.fake_launches() == 0
     assert moe(lib, mx, E=1, k=1, **gaps) == L.LS_OK, "one expert's strides are not read"
+
+
+@pytest.mark.parametrize("M,N,status", [
+    (2 ** 31 - 256, 8, L.LS_OK), (8, 2 ** 31 - 224, L.LS_OK), (2 ** 31 - 255, 8, L.LS_ERR_UNSUPPORTED),
+    (8, 2 ** 31 - 223, L.LS_ERR_UNSUPPORTED), (2 ** 31 - 1, 8, L.LS_ERR_UNSUPPORTED), (8, 2 ** 31 - 1, L.LS_ERR_UNSUPPORTED)])
+def test_rows_of_the_4_bit_product_stay_below_the_limit(lib, M, N, status):
+    """Tiles of 256 rows and 224 columns are counted in 32 bits."""
+    assert lib.lsk_gemm_mxfp4(*PTR[:5], 0, M, N, 32, None) == status
+    assert lib.fake_launches() == (status == L.LS_OK)
+
+
+@pytest.mark.parametrize("M,N,status", [(2 ** 30 - 128, 8, L.LS_OK), (2 ** 30 - 127, 8, L.LS_ERR_UNSUPPORTED),
+                                        (3, 2 ** 31 - 1, L.LS_OK)])
+def test_rows_of_the_bf16_product_stay_below_the_limit(lib, M, N, status):
+    assert lib.lsk_gemm_bf16_mxfp4(PTR[0], 32, PTR[1], PTR[2], PTR[3], 0, M, N, 32, None) == status
+    assert (lib.fake_launches() > 0) == (status == L.LS_OK)
