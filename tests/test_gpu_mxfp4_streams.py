@@ -82,3 +82,43 @@ def test_moe_layers_of_different_inputs_in_flight_on_three_streams(mx4):
     assert L.lsk_device_error() == 0
     for i, o in enumerate(outs):
         assert torch.equal(o, cases[i % 3][3])
+
+
+@pytest.mark.parametrize("M", [1, 12, 40, 200])
+def test_conversion_and_products_in_a_graph(M):
+    """Weights converted, read back and multiplied in one captured chain; the inputs change between replays."""
+    N, K = 900, 1400
+    w = torch.empty((N, K), dtype=torch.bfloat16, device="cuda")
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    codes, xcodes = (torch.empty((r, mx.code_pitch(K)), dtype=torch.uint8, device="cuda") for r in (N, M))
+    scales, xscales = (torch.empty((r, mx.scale_pitch(K)), dtype=torch.uint8, device="cuda") for r in (N, M))
+    back = torch.empty_like(w)
+    out, out4 = torch.empty((M, N), device="cuda"), torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+
+    def chain():
+        L.lsk_mxfp4_quantize(w, N, K, codes, scales)
+        L.lsk_gemm_bf16_mxfp4(x, codes, scales, out, M, N, K)
+        L.lsk_mxfp4_quantize(x, M, K, xcodes, xscales)
+        L.lsk_gemm_mxfp4(xcodes, xscales, codes, scales, out4, M, N, K)
+        L.lsk_mxfp4_dequantize(codes, scales, N, K, back)
+
+    def fill(i):
+        w.copy_(bf16_dev(rand_bf16((N, K), 70 + i)[0]))
+        x.copy_(bf16_dev(rand_bf16((M, K), 80 + i)[0]))
+
+    want = []
+    for i in range(3):
+        fill(i)
+        chain()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (out, out4, back)])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for i in (0, 1, 2, 0):
+        fill(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert L.lsk_device_error() == 0
+        for got, ref in zip((out, out4, back), want[i]):
+            assert torch.equal(got, ref)
