@@ -44,3 +44,15 @@ def test_non_finite_blocks_read_as_nan():
     assert s[0, :3].tolist() == [125, 255, 255]
     d = mx.decode(c, s, 96)
     assert np.array_equal(np.isnan(d[0]), np.arange(96) >= 32)
+
+
+def test_error_bound_of_each_range_of_magnitudes():
+    """Half a step: 1/4 of the scale below 2, 1/2 below 4, 1 up to 6; what saturates is off by its distance from 6."""
+    v = np.random.default_rng(1).standard_normal((200, 320)) * np.exp2(np.random.default_rng(2).integers(-8, 8, (200, 1)))
+    c, s = mx.encode(v)
+    step = np.ldexp(1.0, s[:, np.arange(320) // 32].astype(int) - 127)
+    a, err = np.abs(v) / step, np.abs(mx.decode(c, s, 320) - v) / step
+    bound = np.select([a < 2, a < 4, a <= 6], [0.25, 0.5, 1.0], a - 6)
+    assert np.all(err <= bound * (1 + 1e-12)) and a.max() < 8
+    for lo, hi in ((0, 2), (2, 4), (4, 6), (6, 8)):
+        assert ((a >= lo) & (a < hi)).sum() > 100
