@@ -2,8 +2,8 @@
 
 Each layer is y = x + sum_j w_j D_e(SiLU(G_e x) * (U_e x)) with a router of its own, and a head
 gives the logits of the vocabulary at the end. All matrices are quantised once on the device
-(lsk_mxfp4_quantize) and kept in pinned host memory, one blob a layer: a bf16 layer takes 3.76
-times its bytes of the host link. A step runs, per layer, the copy of a later layer's blob into
+(lsk_mxfp4_quantize) and kept in pinned host memory, one blob a layer: a bf16 layer takes 3.74
+times its bytes of the host link (default sizes). A step runs, per layer, the copy of a later layer's blob into
 the slot that has become free (copy stream) beside the router's product (lsk_gemm_bf16_mxfp4,
 fp32 logits) and the experts (lsk_moe_few) out of the active slot. The head stays on the device:
 a few tokens go through lsk_gemm_bf16_mxfp4, a prompt's many rows through lsk_gemm_mxfp4 with the

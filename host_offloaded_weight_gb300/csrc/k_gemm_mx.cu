@@ -21,8 +21,9 @@
 // What bounds it: the tensor core's reads of shared memory. Unpacked weights are 4 KB a product of K = 32 however few
 // the columns: a stage takes 263 clocks with 16 columns and 362 with 64, about 68 bytes a clock, where its bytes from
 // memory would take 175 of a busy SM's share; and tiles of 128 rows leave SMs without one (13824 rows: 108 of 152).
-// 1 token through 13824 x 5120 takes 9.8 us (3.9 TB/s), 32 tokens through 5120 x 13824 14.4 us, of which the split
-// kernel, the launch and the first load are 6.
+// 1 token through 13824 x 5120 takes 9.9 us (3.8 TB/s), 32 tokens through 5120 x 13824 15.2 us, of which the split
+// kernel, the launch and the first load are 6. Many rows are not what it is for: through 13824 x 5120, 128 rows take 23
+// us, 512 59, 1024 117 and 2048 234, where reading the weights back and the bf16 product take 65, 82, 107 and 180.
 #include <algorithm>
 #include <mutex>
 
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BQ>::THREADS, 1) gemm_mx_kernel(cons
                 const uint32_t tp = tmem + (uint32_t)(C::ACCS * C::ACC + s * C::SCALE_COLS), tq = tp + 4;
                 if (C::MMA_WARPS == 1) ready = bar_test(full((i + 1) % S), (uint32_t)((i + 1) / S) & 1u);
                 if (one) {
-scale_copy(tp, scale_desc(sc));
+                    scale_copy(tp, scale_desc(sc));
 #pragma unroll
                     for (int j = 0; j < C::PARTS; ++j) scale_copy(tq + 4 * j, scale_desc(sc + 512 * (1 + j)));
 #pragma unroll
@@ -579,9 +580,11 @@ int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // Tokens of a tile: the fewest columns that hold M, at most 128.
 int act_tile(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-// CTAs that share a tile along K (a cluster): few tiles leave SMs idle, and each further CTA costs
-// a pass of the sums through shared memory. In units of a scale group (512 values of K, about 0.7 us of an
-// SM's share of the memory): a CTA's groups, one to start, and three to join the sums.
+// CTAs that share a tile along K (a cluster): few tiles leave SMs idle, and joining the sums through shared memory takes
+// time of its own, taken as the same for any number of CTAs, since each adds its share of the tokens. In units of a scale
+// group (512 values of K, about 0.7 us of an SM's share of the memory): a CTA's groups, one to start, and three to join.
+// The three are from the form in which one CTA added all sums (4 us more at 32 tokens) and have not been fitted since;
+// with them K up to 2048 is never shared.
 int act_splits(int tiles, int groups, int max_split) {
     int best = 1;
     double least = groups + 1.0;

@@ -5,7 +5,7 @@
 // scales left out), and at 4 bits the products of a stage are shorter than its loads. A tile's shape decides: a pair of
 // CTAs shares a tile of 256 x BQ (cta_group::2), each SM loads 128 rows of A and BQ / 2 of B for 128 x BQ outputs. With
 // 256 x 224 a stage is 31 KB of rows and 3 KB of scales, about 560 of the 690 clocks that it takes (products: 450; the
-// tensor pipe is active 66 %). One CTA with 128 x 192 tiles loaded 41 KB for 24576 outputs in place of 28672. A wider
+// tensor pipe is active 66 %; what the other 130 are spent on has not been found). One CTA with 128 x 192 tiles loaded 41 KB for 24576 outputs in place of 28672. A wider
 // tile leaves no TMEM for a second accumulator.
 //
 // Structure (persistent pairs, one CTA an SM): warp 0 loads the CTA's operand rows by TMA (128-byte rows = 256
@@ -16,8 +16,9 @@
 // count at the first CTA's `full` barriers; what frees a stage, and what completes a tile, is signalled in both.
 // The scales have two sets of TMEM columns, taken in turn: the products of two stages before have to be complete.
 //
-// 2048 x 13824 x 5120: 50 us, 5.75 PFLOP/s (single CTAs: 63 us); 4096 x 4096 x 1024: 12.4 us (17.7); 333 x 1111 x
-// 1000: 4.8 us (10.5); 8192 x 8192 x 8192: 6.6 PFLOP/s. One team of scale warps in place of two: 54.5 us for the
+// 2048 x 13824 x 5120: 50.7 us, 5.7 PFLOP/s (single CTAs: 63 us); 4096 x 4096 x 1024: 12.4 us (17.7); 333 x 1111 x
+// 1000: 4.5 us (10.5); 8192 x 8192 x 8192: 6.6 PFLOP/s. fp32 results: 57, 15.7 and 4.8 us for the first three. 256 x 5120 x
+// 13824, 40 tiles for 76 pairs and nothing shared along K: 19 us. One team of scale warps in place of two: 54.5 us for the
 // first; results written by lanes in place of bulk stores: 14.1 us for the second. A ring of the scales' own and a warp
 // that copies them to TMEM, with 192 columns: 49.9 and 12.6 us, not worth their barriers.
 #include <algorithm>

@@ -187,7 +187,8 @@ ls_status lsk_moe_check(const int32_t* sel_dev, const int32_t* row_table_dev, co
  * s = floor(log2 max|v|) - 2, at least -127; elements E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
  * negatives), v 2^-s rounded to the nearest, ties to the even code, saturating at 6. An all-zero
  * block has scale byte 0. A block with a NaN or an infinity has scale byte 255 and reads back as
- * NaN. Weights in this form take 17/64 of their bf16 bytes (of a slot, and of the host link).
+ * NaN. Weights in this form take 17/64 of their bf16 bytes (of a slot, and of the host link) where K is a
+ * multiple of 512, and more with the padding (K = 768: 0.271).
  *
  * A matrix [rows, K]: codes, two a byte (even k in the low half), lsk_mxfp4_code_pitch(K) =
  * 64 ceil(K/128) bytes a row; scales, lsk_mxfp4_scale_pitch(K) = 16 ceil(K/512) bytes a row.
@@ -202,7 +203,7 @@ int64_t lsk_mxfp4_scale_pitch(int32_t K);
 ls_status lsk_mxfp4_quantize(const void* src_dev, int32_t src_f32, int64_t rows, int32_t K, int64_t ld,
                              void* codes_dev, void* scales_dev, void* stream);
 
-/* The values that the codes stand for, bf16 or fp32 (both exact), ld >= K elements between rows. */
+/* The values that the codes stand for, bf16 or fp32 (both exact for what lsk_mxfp4_quantize writes), ld >= K elements between rows. */
 ls_status lsk_mxfp4_dequantize(const void* codes_dev, const void* scales_dev, int64_t rows, int32_t K,
                                void* dst_dev, int32_t dst_f32, int64_t ld, void* stream);
 
@@ -215,7 +216,8 @@ ls_status lsk_gemm_mxfp4(const void* a_codes_dev, const void* a_scales_dev, cons
 
 /* C[M,N] = A[M,K] B[N,K]^T with A bf16 (lda >= K elements between rows) and B in MXFP4, fp32
  * sums, C dense bf16 (fp32 when c_f32 != 0). M up to 2^30 - 128 (LS_ERR_UNSUPPORTED above); made for
- * few tokens (M = 1 upwards), where it streams the weights once at 17/32 byte a value. A keeps its eight
+ * few tokens (M = 1 upwards), where it streams the weights once at 17/32 byte a value (from about 1000
+ * rows on, lsk_mxfp4_dequantize and lsk_gemm_bf16 take less time). A keeps its eight
  * bits: values down to 2^-13 of the largest of their block of 32 enter exactly, smaller ones within 2^-22
  * of that largest (2^-21 where it is 2^127 or more). A NaN or an infinity in a row of A makes that row
  * of C NaN. More than 8 rows take scratch on `stream`
@@ -246,15 +248,16 @@ typedef struct lsk_moe_experts {
 
 /* A whole MoE layer for a few tokens, in one cooperative launch (one CTA per SM):
  *   out[t] = r[t] + sum_{j<k} w[t,j] D_e (SiLU(G_e x[t]) * (U_e x[t])),  e = sel[t,j]
- * with sel and w as lsk_moe_route gives them from logits_dev [T, E] fp32 (the k largest, ties to the
+ * with sel and w as lsk_moe_route gives them from finite logits_dev [T, E] fp32 (the k largest, ties to the
  * lower expert, softmax over the chosen), r = resid_dev [T, H] fp32, or x_dev when that is NULL.
  * x_dev [T, H] bf16 (16-byte aligned), out_dev [T, H] bf16; out32_dev (may be NULL) gets the fp32
  * result. A NaN logit counts as the lowest one and makes its token NaN if it is chosen. An expert chosen with a
  * logit of -infinity takes no part: it is not read, and a token that has no other gets out = r, whatever x holds
- * (lsk_moe_route gives such an expert weight 0, and NaN weights to a token that has no other). Sums are fp32 in a fixed order. With bf16
- * experts the hidden activation is rounded once, to bf16. With MXFP4 experts it keeps twelve bits
- * and x all eight (as in lsk_gemm_bf16_mxfp4), relative to the largest of 32 neighbours. T <= 64, E <= 256, k <= 8 (LS_ERR_UNSUPPORTED above:
- * lsk_moe_route to lsk_moe_combine serve more tokens), H and F multiples of 8. Takes scratch on
+ * (lsk_moe_route gives such an expert weight 0, and NaN weights to a token that has no other). Sums are
+ * fp32 in a fixed order; SiLU takes the device's fast exponential (__expf). With bf16 experts the hidden
+ * activation is rounded once, to bf16. With MXFP4 experts it keeps twelve bits and x all eight (as in
+ * lsk_gemm_bf16_mxfp4), relative to the largest of 32 neighbours. T <= 64, E <= 256, k <= 8
+ * (LS_ERR_UNSUPPORTED above: lsk_moe_route to lsk_moe_combine serve more tokens), H and F multiples of 8. Takes scratch on
  * `stream` from the library's pool (LS_ERR_OOM if refused). */
 ls_status lsk_moe_few(const void* x_dev, const float* resid_dev, const float* logits_dev,
                       const lsk_moe_experts* experts, int32_t T, int32_t E, int32_t k, int32_t H, int32_t F,
