@@ -21,6 +21,7 @@ def _undefined(path):
 
 @pytest.fixture(scope="module")
 def fake_path(tmp_path_factory):
+    B.build()          # the objects, where they are older than their sources
     d = tmp_path_factory.mktemp("fake")
     objs = [os.path.join(B.BUILD, os.path.splitext(s)[0] + ".o") for s in B.SOURCES if s not in LEFT_OUT]
     include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B._nvcc()))), "include")
