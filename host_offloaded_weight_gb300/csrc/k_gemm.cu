@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 #include <unordered_map>
 
 namespace ls {
@@ -86,6 +87,15 @@ struct GemmParams {
     uint64_t mbar_limit_ns;  // bound of every internal mbarrier wait
     int pdl;                 // host side: launch with programmatic stream serialization
     int splits;              // EPI_PARTIAL: K slices; slice s of tile t is work item s * num_tiles + t
+};
+
+// A product with low-rank adapters beside it (see k_gemm_lora.cu): after its k-blocks a tile takes, for each adapter with
+// a row in it, blocks of h [256 rows, cw] (two terms, one after the other) with the cw columns of the adapter's `up`.
+struct LoraGemmParams : GemmParams {
+    CUtensorMap tmH, tmUp, tmUp2;
+    const int* lora_count;   // [row tile] adapters
+    const int* lora_list;    // [row tile][lora_cap] which; -1: not finite, read as zeros
+    int lora_cap, lora_cw, lora_chunks, lora_parts, lora_rank;
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -229,6 +239,12 @@ __device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr) {
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
+}
+
+// The same with rows of cw = 16, 32 or 64 bf16 values and the swizzle of that width.
+__device__ __forceinline__ uint64_t make_sdesc_narrow(uint32_t saddr, int cw) {
+    const uint64_t layout = cw == 64 ? 2 : cw == 32 ? 4 : 6;
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(cw) << 32) | ((uint64_t)1 << 46) | (layout << 61);
 }
 
 // ------------------------------------------------------------------ tile mapping
@@ -705,6 +721,14 @@ __device__ __forceinline__ void tma_load_2d_2sm(uint32_t dst, const CUtensorMap*
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar_cluster)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_2sm(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int c0, int c1,
+                                                int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
                  : "memory");
@@ -812,8 +836,9 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     return v;
 }
 
-template <int EPI, bool DUAL, int BN, bool ONE = false>
-__global__ void __launch_bounds__(s2_threads(EPI), 1) gemm_bf16_tc2(const __grid_constant__ GemmParams p) {
+template <int EPI, bool DUAL, int BN, bool ONE = false, bool LORA = false>
+__global__ void __launch_bounds__(s2_threads(EPI), 1)
+    gemm_bf16_tc2(const __grid_constant__ std::conditional_t<LORA, LoraGemmParams, GemmParams> p) {
     static_assert(BN % 32 == 0 && BN >= 64 && BN <= 256 && (!DUAL || BN == 256), "tile width");
     static_assert(!ONE || s2_out_f32(EPI), "one-tile layout: residual epilogues");
     extern __shared__ uint8_t smem_raw[];
@@ -861,7 +886,9 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1) gemm_bf16_tc2(const __grid
     tc_fence_before();
     cluster_sync();  // barriers of both CTAs initialised, TMEM allocated in both
     tc_fence_after();
-    grid_dep_wait();
+    // With adapters the kernels before are this call's own, begun when everything earlier was complete: only what they
+    // write has to be waited for, where it is read.
+    if (!LORA) grid_dep_wait();
     const uint32_t tmem_base = *tmem_slot;
     const int num_m2 = (p.M + 255) / 256;
     const int num_tiles = num_m2 * p.num_n_tiles;  // num_n_tiles counts BN (dual: 128) columns
@@ -874,6 +901,7 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1) gemm_bf16_tc2(const __grid
             int it = 0;
             uint32_t issued_mask = 0;
             bool ok = true;
+            [[maybe_unused]] bool waited = false;
             for (int t = cluster_id; t < num_tiles && ok; t += n_clusters) {
                 const int m2 = t % num_m2, n = t / num_m2;
                 const int a_row = m2 * 256 + (int)rank * 128;
@@ -895,7 +923,31 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1) gemm_bf16_tc2(const __grid
                     tma_load_2d_2sm(sb, &p.tmB, leader_full, kb * BK, b_row);
                     issued_mask |= 1u << s;
                 }
+                if constexpr (LORA) {
+                    if (!waited) grid_dep_wait();
+                    waited = true;
+                    const int more = ok ? p.lora_count[m2] * p.lora_parts * 2 : 0, cw = p.lora_cw;
+                    for (int e = 0; e < more; ++e, ++it) {
+                        const int s = it % S2_STAGES;
+                        if (!mbar_wait(empty_bar(s), ((uint32_t)(it / S2_STAGES) & 1u) ^ 1u, p.err, 1, p.mbar_limit_ns)) {
+                            ok = false;
+                            s_abort = 1;
+                            break;
+                        }
+                        const int part = (e >> 1) % p.lora_parts, j = (e >> 1) / p.lora_parts, half = part / p.lora_chunks;
+                        const int a = p.lora_list[(int64_t)m2 * p.lora_cap + j];
+                        const uint32_t sa = base + s * S2_STAGE, leader_full = mapa(full_bar(s), 0);
+                        if (leader) mbar_expect_tx(full_bar(s), 2 * (128 + BN / 2) * cw * 2);
+                        tma_load_2d_2sm(sa, &p.tmH, leader_full, 0, (int)((((int64_t)m2 * p.lora_cap * p.lora_parts * 2) + e) * 256) + (int)rank * 128);
+                        // out of bounds: zeros, for an adapter that is not finite and for the other half of a gate/up tile
+                        const bool none = a < 0 || (DUAL && half != (int)rank);
+                        tma_load_3d_2sm(sa + S2_A, half ? &p.tmUp2 : &p.tmUp, leader_full, part % p.lora_chunks * cw,
+                                        none ? p.N : DUAL ? n * 128 : b_row, max(a, 0));
+                        issued_mask |= 1u << s;
+                    }
+                }
             }
+            if (LORA && !waited) grid_dep_wait();
             grid_dep_launch();  // every load is issued: the next kernel may start placing CTAs
             // the leader's full barrier tracks both CTAs' loads: drain there (leader only)
             if (leader)
@@ -910,6 +962,7 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1) gemm_bf16_tc2(const __grid
             constexpr uint32_t IDESC = make_idesc(256, BN);
             int it = 0, tcount = 0;
             bool ok = true;
+            [[maybe_unused]] bool waited = false;
             for (int t = cluster_id; t < num_tiles && ok; t += n_clusters, ++tcount) {
                 const int buf = tcount & 1;
                 const uint32_t tph = (uint32_t)(tcount >> 1) & 1u;
@@ -935,6 +988,25 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1) gemm_bf16_tc2(const __grid
                         umma2_bf16(d, make_sdesc(sa + kk * 32), make_sdesc(sb + kk * 32), IDESC,
                                    (kb > 0 || kk > 0) ? 1u : 0u);
                     umma2_commit_both(empty_bar(s));
+                }
+                if constexpr (LORA) {
+                    if (!waited) grid_dep_wait();
+                    waited = true;
+                    const int more = ok ? p.lora_count[t % num_m2] * p.lora_parts * 2 : 0, cw = p.lora_cw;
+                    for (int e = 0; e < more; ++e, ++it) {
+                        const int s = it % S2_STAGES;
+                        if (!mbar_wait(full_bar(s), (uint32_t)(it / S2_STAGES) & 1u, p.err, 3, p.mbar_limit_ns)) {
+                            ok = false;
+                            s_abort = 1;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = base + s * S2_STAGE;
+                        const int left = min(cw, p.lora_rank - (e >> 1) % p.lora_parts % p.lora_chunks * cw);
+                        for (int kk = 0; kk < (left + 15) / 16; ++kk)
+                            umma2_bf16(d, make_sdesc_narrow(sa + kk * 32, cw), make_sdesc_narrow(sa + S2_A + kk * 32, cw), IDESC, 1u);
+                        umma2_commit_both(empty_bar(s));
+                    }
                 }
                 if (ok) umma2_commit_both(tfull_bar(buf));
             }
@@ -1289,9 +1361,9 @@ cudaError_t launch_t(const GemmParams& p, int grid, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int EPI, bool DUAL, int BN, bool ONE = false>
-cudaError_t launch_t2(const GemmParams& p, int clusters, cudaStream_t s) {
-    auto kern = gemm_bf16_tc2<EPI, DUAL, BN, ONE>;
+template <int EPI, bool DUAL, int BN, bool ONE = false, class P = GemmParams>
+cudaError_t launch_t2(const P& p, int clusters, cudaStream_t s) {
+    auto kern = gemm_bf16_tc2<EPI, DUAL, BN, ONE, std::is_same_v<P, LoraGemmParams>>;
     static SmemAllowance allowed;
     const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), s2_smem_bytes(EPI, BN, ONE));
     if (e != cudaSuccess) return e;
@@ -1312,8 +1384,8 @@ cudaError_t launch_t2(const GemmParams& p, int clusters, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int EPI, bool ONE = false>
-cudaError_t launch_t2_bn(const GemmParams& p, int bn, int clusters, cudaStream_t s) {
+template <int EPI, bool ONE = false, class P = GemmParams>
+cudaError_t launch_t2_bn(const P& p, int bn, int clusters, cudaStream_t s) {
     switch (bn) {
         case 256: return launch_t2<EPI, false, 256, ONE>(p, clusters, s);
         case 224: return launch_t2<EPI, false, 224, ONE>(p, clusters, s);
@@ -1521,6 +1593,55 @@ cudaError_t launch_gemm_bf16(const GemmDesc& d, int max_ctas, cudaStream_t s) {
                            : launch_t<EPI_SWIGLU, true, false>(p, grid, s);
         case EPI_SCALE_F32:
             return grouped ? launch_t<EPI_SCALE_F32, false, true>(p, grid, s) : cudaErrorInvalidValue;
+    }
+    return cudaErrorInvalidValue;
+}
+
+// The pair kernel with its adapters' columns. The maps of the blocks and of `up` are made for each call.
+cudaError_t launch_gemm_bf16_lora(const GemmDesc& d, const LoraArgs& l, int64_t h_rows, cudaStream_t s) {
+    const bool dual = d.epi == EPI_SWIGLU;
+    LoraGemmParams p;
+    memset(&p, 0, sizeof(p));
+    const int bn = dual ? 256 : gemm_pair_tile_n(d.M, d.N), b_box = dual ? 128 : bn / 2;
+    if (!cached_tmap(&p.tmA, d.A, d.M, d.K, d.lda, 128) || !cached_tmap(&p.tmB, d.B, d.b_rows, d.K, d.ldb, b_box) ||
+        !cached_tmap(&p.tmC, MapSpec{d.C, d.M, d.N, d.ldc, 32, 32, 2, 64}) ||
+        (d.C32 && !cached_tmap(&p.tmC32, MapSpec{d.C32, d.M, d.N, d.ldc, 32, 32, 4, 128})) ||
+        !lora_map(&p.tmH, l.h, h_rows, l.cw, l.cw, 128, 0, 0) ||
+        !lora_map(&p.tmUp, l.up, d.N, l.rank, l.cw, b_box, l.n, l.up_stride) ||
+        (dual && !lora_map(&p.tmUp2, l.up2, d.N, l.rank, l.cw, b_box, l.n, l.up_stride)))
+        return cudaErrorInvalidValue;
+    p.M = d.M;
+    p.N = d.N;
+    p.K = d.K;
+    p.num_n_tiles = (d.N + (dual ? 128 : bn) - 1) / (dual ? 128 : bn);
+    p.num_k_blocks = (d.K + BK - 1) / BK;
+    p.b2_row_off = d.b2_row_off;
+    p.bias = static_cast<const __nv_bfloat16*>(d.bias);
+    p.resid = d.resid;
+    p.resid_f32 = d.resid_f32 ? 1 : 0;
+    p.ldr = d.ldr;
+    p.C = d.C;
+    p.ldc = d.ldc;
+    p.C32 = static_cast<float*>(d.C32);
+    p.err = d.err_word;
+    p.mbar_limit_ns = MBAR_LIMIT_NS;
+    p.pdl = 1;
+    p.lora_count = l.count;
+    p.lora_list = l.list;
+    p.lora_cap = l.cap;
+    p.lora_cw = l.cw;
+    p.lora_chunks = l.chunks;
+    p.lora_parts = l.parts;
+    p.lora_rank = l.rank;
+    const int64_t tiles = (d.M + 255ll) / 256 * p.num_n_tiles;
+    if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
+    const int clusters = (int)std::min<int64_t>(std::max(1, gemm_num_sms() / 2), tiles);
+    switch (d.epi) {
+        case EPI_STORE: return launch_t2_bn<EPI_STORE, false>(p, bn, clusters, s);
+        case EPI_BIAS_GELU: return launch_t2_bn<EPI_BIAS_GELU, false>(p, bn, clusters, s);
+        case EPI_BIAS_RESID: return launch_t2_bn<EPI_BIAS_RESID, false>(p, bn, clusters, s);
+        case EPI_RESID: return launch_t2_bn<EPI_RESID, false>(p, bn, clusters, s);
+        case EPI_SWIGLU: return launch_t2<EPI_SWIGLU, true, 256>(p, clusters, s);
     }
     return cudaErrorInvalidValue;
 }

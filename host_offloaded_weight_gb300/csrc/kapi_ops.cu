@@ -1,4 +1,4 @@
-// C entry points of the 4-bit and few-token operators (see ls_kernels.h).
+// C entry points of the 4-bit, few-token and per-row operators (see ls_kernels.h).
 #include <cuda_runtime.h>
 
 #include "kernels.h"
@@ -38,6 +38,7 @@ struct Scratch {
 constexpr int32_t MX_MAX_K = 1 << 24;
 // Rows are counted in 32 bits, whole tiles of them (256 rows of A and 224 of B; 128 rows of A twice).
 constexpr int32_t MX_MAX_M = 0x7fffffff - 255, MX_MAX_N = 0x7fffffff - 223, ACT_MAX_M = (1 << 30) - 128;
+constexpr int32_t LORA_MAX_M = 0x7fffffff - 255;  // tiles of 256 rows and columns
 
 }  // namespace
 
@@ -143,6 +144,57 @@ ls_status lsk_moe_few(const void* x, const float* resid, const float* logits, co
     Scratch ws((cudaStream_t)stream);
     if (!ws.take(moe_few_ws_bytes(mx, T, k, H, F))) return LS_ERR_OOM;
     return status_of(launch_moe_few(d, ws.p, entry_error_word(), (cudaStream_t)stream));
+}
+
+ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A, const void* B, int64_t b_rows, int32_t b2_row_off,
+                             const lsk_lora* l, const int32_t* ids, const void* bias, const void* resid, int32_t resid_f32,
+                             void* C, void* C32, int32_t M, int32_t N, int32_t K, void* stream) {
+    const bool dual = epilogue == LSK_EPI_SWIGLU, has_bias = epilogue == LSK_EPI_BIAS_GELU || epilogue == LSK_EPI_BIAS_RESID;
+    const bool has_resid = epilogue == LSK_EPI_BIAS_RESID || epilogue == LSK_EPI_RESID;
+    if (epilogue < LSK_EPI_STORE || epilogue > LSK_EPI_RESID || !l || M < 0 || N < 8 || K < 8 || (N % 8) || (K % 8) || K > MX_MAX_K)
+        return LS_ERR_INVALID_ARG;
+    if (b2_row_off < 0 || b_rows < (dual ? (int64_t)b2_row_off + N : N) || l->n < 1 || l->rank < 8 || (l->rank % 8)) return LS_ERR_INVALID_ARG;
+    if (M > LORA_MAX_M || N > LORA_MAX_M || l->rank > LORA_MAX_RANK || b_rows > 0x7fffffffll) return LS_ERR_UNSUPPORTED;
+    if (M == 0) return LS_OK;
+    const int64_t down_bytes = 2ll * l->rank * K * (dual ? 2 : 1), up_bytes = 2ll * N * l->rank;
+    const int64_t ds = l->n == 1 ? down_bytes : l->down_stride, us = l->n == 1 ? up_bytes : l->up_stride;
+    if (!A || !B || !ids || !C || !l->down || !l->up || (dual && !l->up2) || (has_bias && !bias) || (has_resid && !resid) || (C32 && !has_resid))
+        return LS_ERR_INVALID_ARG;
+    if (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(ids, 4) || !aligned(l->down, 16) || !aligned(l->up, 16) ||
+        (dual && !aligned(l->up2, 16)) || !aligned(l->scale, 4) || (has_bias && !aligned(bias, 16)) || (has_resid && !aligned(resid, 16)) ||
+        !aligned(C32, 16))
+        return LS_ERR_INVALID_ARG;
+    if (ds < down_bytes || us < up_bytes || (ds % 16) || (us % 16) || ds >= (1ll << 40) || us >= (1ll << 40)) return LS_ERR_INVALID_ARG;
+    LoraArgs p = {};
+    p.x = static_cast<const __nv_bfloat16*>(A);
+    p.ids = ids;
+    p.down = l->down;
+    p.up = l->up;
+    p.up2 = dual ? l->up2 : nullptr;
+    p.scale = l->scale;
+    p.down_stride = ds;
+    p.up_stride = us;
+    p.T = M;
+    p.N = N;
+    p.K = K;
+    p.n = l->n;
+    p.rank = l->rank;
+    if (!lora_plan(p, dual)) return LS_ERR_UNSUPPORTED;
+    GemmDesc d;
+    d.epi = epilogue;
+    d.A = A; d.lda = K; d.a_rows = M;
+    d.B = B; d.ldb = K; d.b_rows = b_rows;
+    d.b2_row_off = b2_row_off;
+    d.bias = has_bias ? bias : nullptr;
+    d.resid = has_resid ? resid : nullptr; d.ldr = N;
+    d.resid_f32 = resid_f32 != 0;
+    d.C = C; d.ldc = N;
+    d.C32 = C32;
+    d.M = M; d.N = N; d.K = K;
+    d.err_word = entry_error_word();
+    Scratch ws((cudaStream_t)stream);
+    if (!ws.take(lora_ws_bytes(p))) return LS_ERR_OOM;
+    return status_of(launch_gemm_lora(d, p, ws.p, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 // Internal kernel launchers of the layer-streaming library (not part of the C ABI).
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -123,6 +124,38 @@ int gemm_split_k(int64_t M, int64_t N, int64_t K, int epi);
 // Workspace bytes the split needs (0 when not split); at most GEMM_SPLITK_WS_MAX.
 int64_t gemm_split_ws_bytes(int64_t M, int64_t N, int64_t K, int epi);
 int64_t gemm_split_ws_max();
+
+// ---------------------------------------------------------------- low-rank adapters beside a shared projection
+constexpr int LORA_FEW_ROWS = 128, LORA_MAX_RANK = 256;
+struct LoraArgs {
+    // of the caller
+    const __nv_bfloat16* x;   // [T, K]
+    const int* ids;           // [T]
+    const void* down;         // n matrices [rank, K] (gate/up pair: [2 rank, K]), down_stride bytes apart
+    const void* up;           // n matrices [N, rank], up_stride bytes apart
+    const void* up2;          // gate/up pair: the same of the up projection
+    const float* scale;       // [n], or NULL: 1
+    int64_t down_stride, up_stride;
+    int T, N, K, n, rank;
+    // by lora_plan. h as blocks [tile][adapter of the tile][part][term] of tile_rows x cw values; a part is cw of
+    // the rank's columns, the gate's `chunks` parts first
+    int cw, chunks, parts, tile_rows, cap, check_parts;
+    int64_t tiles;
+    // in scratch
+    int* count;               // [tiles] adapters of a tile
+    int* list;                // [tiles][cap] which; -1: one that is not finite
+    uint8_t* bad;             // [n][check_parts]
+    __nv_bfloat16* h;
+};
+bool lora_plan(LoraArgs& p, bool dual);  // false: more blocks than can be counted
+int64_t lora_ws_bytes(const LoraArgs& p);
+// d: the shared product (dense, as for launch_gemm_bf16; b_rows given); ws: lora_ws_bytes, 256-byte aligned.
+cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStream_t s);
+// [rows, cols] of dense bf16 in boxes of box_cols (16, 32 or 64: the swizzle of that width) x box_rows; with n > 0 a third
+// dimension of n matrices `stride` bytes apart.
+bool lora_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int box_cols, int box_rows, int64_t n, int64_t stride);
+// The product of more than LORA_FEW_ROWS rows, after the kernels that write the blocks (h_rows rows of them).
+cudaError_t launch_gemm_bf16_lora(const GemmDesc& d, const LoraArgs& p, int64_t h_rows, cudaStream_t s);
 
 // ---------------------------------------------------------------- MoE
 cudaError_t launch_moe_route(const float* logits, int n_layers, int T, int E, int k, int* sel,

@@ -76,6 +76,11 @@ class lsk_moe_experts(C.Structure):
                 ("gate_scale_stride", C.c_int64), ("down_scale_stride", C.c_int64)]
 
 
+class lsk_lora(C.Structure):
+    _fields_ = [("n", C.c_int32), ("rank", C.c_int32), ("down", C.c_void_p), ("up", C.c_void_p), ("up2", C.c_void_p),
+                ("scale", C.c_void_p), ("down_stride", C.c_int64), ("up_stride", C.c_int64)]
+
+
 class ls_kernel_time(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("launches", C.c_int64), ("total_ms", C.c_double)]
 
@@ -159,6 +164,7 @@ _sig = {
     "lsk_gemm_mxfp4": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "lsk_gemm_bf16_mxfp4": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "lsk_moe_few": (_I32, [_P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "lsk_gemm_lora_bf16": (_I32, [_I32, _P, _P, _I64, _I32, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _P]),
     "ls_helper_share": (C.c_double, [_I64]),
     "ls_host_alloc": (_I32, [_U64, C.POINTER(_P)]),
     "ls_host_free": (_I32, [_P]),
@@ -766,3 +772,59 @@ def lsk_moe_few(x, logits, gate, up, down, T: int, E: int, k: int, H: int, F: in
     pr = 0 if resid is None else _values(resid, 1, "resid")
     p32 = 0 if out32 is None else _values(out32, 1, "out32")
     return _check(_lib.lsk_moe_few(px, pr, pl, w, T, E, k, H, F, po, p32, _stream(stream)))
+
+
+# ------------------------------------------------------------------ products whose weights differ by rows
+class LoraAdapters:
+    """The adapters of one projection as the library takes them, and references to their tensors."""
+
+    def __init__(self, down, up, up2=None, scale=None):
+        for t, what in ((down, "down"), (up, "up")) + (() if up2 is None else ((up2, "up2"),)):
+            if _dtype_code(t) != LS_DTYPE_BF16:
+                raise TypeError(f"{what} has to be bf16, not {t.dtype}")
+            if t.dim() != 3:
+                raise ValueError(f"{what} has to be [adapters, rows, columns]")
+            _expert_rows(t, what)
+        n, rank = up.shape[0], up.shape[2]
+        rows = rank if up2 is None else 2 * rank
+        if down.shape[0] != n or down.shape[1] != rows or (up2 is not None and up2.shape != up.shape):
+            raise ValueError("the adapters' matrices do not belong together")
+        if up2 is not None and n > 1 and up2.stride(0) != up.stride(0):
+            raise ValueError("up and up2 need the same distance between adapters")
+        self.N, self.K, self.two = up.shape[1], down.shape[2], up2 is not None
+        self.keep = (down, up, up2, scale)
+        if scale is not None and scale.shape != (n,):
+            raise ValueError("scale has to be [adapters]")
+        self.c = lsk_lora(n, rank, down.data_ptr(), up.data_ptr(), _ptr(up2), 0 if scale is None else _values(scale, 1, "scale"),
+                          2 * down.stride(0), 2 * up.stride(0))
+        self.ref = C.addressof(self.c)
+
+
+def lsk_lora_adapters(down, up, up2=None, scale=None) -> LoraAdapters:
+    """Adapters beside a projection [N, K]: down [n, rank, K] and up [n, N, rank] bf16 (the gate/up pair: down [n, 2 rank, K], the
+    gate's rows first, and up2 [n, N, rank]), scale [n] float32 or None. Adapters may lie apart; the rows of each are dense."""
+    return LoraAdapters(down, up, up2, scale)
+
+
+def _ids(t, what: str, need: int):
+    """Address of a dense int32 tensor of at least `need` values; raw addresses and None pass."""
+    if getattr(t, "dtype", None) is not None:
+        if "int32" not in str(t.dtype) or "uint" in str(t.dtype):
+            raise TypeError(f"{what} has to be int32, not {t.dtype}")
+        _dense(t, what)
+        if t.numel() < need:
+            raise ValueError(f"{what} has {t.numel()} values, not {need}")
+    return _ptr(t)
+
+
+def lsk_gemm_lora_bf16(epilogue: int, A, B, adapters: LoraAdapters, ids, C_out, M: int, N: int, K: int, bias=None, resid=None,
+                       b_rows: int | None = None, b2_row_off: int = 0, C32=None, stream=None) -> int:
+    """lsk_gemm_bf16 with the adapter ids[t] (int32 [M], none where it is not one of the adapters') beside row t's product."""
+    if adapters.N != N or adapters.K != K or adapters.two != (epilogue == LSK_EPI_SWIGLU):
+        raise ValueError("these adapters are for another projection")
+    rows = b_rows if b_rows is not None else B.shape[0]
+    rf32 = 0 if resid is None else _is_f32(resid)
+    return _check(_lib.lsk_gemm_lora_bf16(
+        epilogue, _values(A, 0, "A"), _values(B, 0, "B"), rows, b2_row_off, adapters.ref, _ids(ids, "ids", M),
+        0 if bias is None else _values(bias, 0, "bias"), 0 if resid is None else _values(resid, rf32, "resid"), rf32,
+        _values(C_out, 0, "C_out"), 0 if C32 is None else _values(C32, 1, "C32"), M, N, K, _stream(stream)))

@@ -263,6 +263,39 @@ ls_status lsk_moe_few(const void* x_dev, const float* resid_dev, const float* lo
                       const lsk_moe_experts* experts, int32_t T, int32_t E, int32_t k, int32_t H, int32_t F,
                       void* out_dev, float* out32_dev, void* stream);
 
+/* ---- products whose weights differ by rows -------------------------------------------- */
+
+/* Low-rank adapters of one projection, resident together: `down` [rank, K] and `up` [N, rank] of each, bf16, row-major and
+ * dense, an adapter's matrix a fixed number of bytes after the one before (multiples of 16). For LSK_EPI_SWIGLU, down is
+ * [2 rank, K], the gate's rows first, `up` is the gate's and up2 the other projection's (its matrices up_stride apart too).
+ * rank is a multiple of 8 up to 256: adapters of a lower rank are padded with zeros. scale_dev [n] fp32 multiplies an
+ * adapter's part (NULL: 1). Matrices are 16-byte aligned; with one adapter the strides are not read. */
+typedef struct lsk_lora {
+    int32_t n;
+    int32_t rank;
+    const void* down;
+    const void* up;
+    const void* up2;
+    const float* scale;
+    int64_t down_stride;
+    int64_t up_stride;
+} lsk_lora;
+
+/* lsk_gemm_bf16 with an adapter of its own for each row:
+ *   C[t] = epilogue(A[t] B^T + scale_a (A[t] down_a^T) up_a^T),  a = ids_dev[t]
+ * and nothing added where ids_dev[t] is not one of 0 .. n-1 (say, -1). All epilogues, arguments and alignments of
+ * lsk_gemm_bf16; with LSK_EPI_SWIGLU the gate's and the other projection's parts are added before the SiLU and the product.
+ * Sums are fp32 in a fixed order; A[t] down_a^T, scaled, enters the second product as two bf16 terms (16 bits). Rows of
+ * one adapter cost least side by side (a tile takes up to 256 rows and pays for each adapter among them). An adapter with a
+ * NaN or an infinity in `up` or up2 makes its own rows NaN; rows of others are as if it were not there. Takes scratch on
+ * `stream` from the library's pool (LS_ERR_OOM if refused): 4 rank bytes, rounded up, for each row of a tile and each
+ * adapter that it could hold, min(n, 256) of them. K up to 2^24. LS_ERR_UNSUPPORTED for ranks above 256 or more scratch rows
+ * than 2^31. */
+ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A_dev, const void* B_dev, int64_t b_rows, int32_t b2_row_off,
+                             const lsk_lora* adapters, const int32_t* ids_dev, const void* bias_dev,
+                             const void* resid_dev, int32_t resid_f32, void* C_dev, void* C32_dev, int32_t M, int32_t N,
+                             int32_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
