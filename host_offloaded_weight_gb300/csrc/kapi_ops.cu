@@ -197,4 +197,47 @@ ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A, const void* B, int
     return status_of(launch_gemm_lora(d, p, ws.p, (cudaStream_t)stream));
 }
 
+ls_status lsk_gemm_grouped_bf16_mxfp4(int32_t epilogue, const void* A, int64_t a_rows, const void* b_codes, const void* b_scales,
+                                      const void* b2_codes, const void* b2_scales, int64_t code_stride, int64_t scale_stride,
+                                      const int32_t* bounds, int32_t n_groups, const int32_t* row_table, const float* row_weight,
+                                      int32_t gather_k, void* C, int32_t M, int32_t N, int32_t K, void* stream) {
+    const bool dual = epilogue == LSK_EPI_SWIGLU, scaled = epilogue == LSK_EPI_SCALE_F32;
+    if ((epilogue != LSK_EPI_STORE && !dual && !scaled) || M < 0 || N < 1 || K < 8 || (K % 8) || K > MX_MAX_K || n_groups < 1 || gather_k < 0 ||
+        a_rows < 0 || (gather_k == 0 && a_rows < M))
+        return LS_ERR_INVALID_ARG;
+    if (n_groups > GROUPED_MX_MAX_GROUPS || M > (1 << 30) || N > MX_MAX_N) return LS_ERR_UNSUPPORTED;
+    if (M == 0) return LS_OK;
+    if (!A || !b_codes || !b_scales || (dual && (!b2_codes || !b2_scales)) || !bounds || !C || ((scaled || gather_k > 0) && !row_table) ||
+        (scaled && !row_weight))
+        return LS_ERR_INVALID_ARG;
+    const int64_t code_bytes = N * mx_code_pitch(K), scale_bytes = N * mx_scale_pitch(K);
+    const int64_t cs = n_groups == 1 ? code_bytes : code_stride, ss = n_groups == 1 ? scale_bytes : scale_stride;
+    if (!aligned(A, 16) || !aligned(b_codes, 32) || !aligned(b_scales, 16) || (dual && (!aligned(b2_codes, 32) || !aligned(b2_scales, 16))) ||
+        !aligned(bounds, 4) || !aligned(row_table, 4) || !aligned(row_weight, 4) || !aligned(C, scaled ? 4 : 2) || cs < code_bytes ||
+        ss < scale_bytes || (cs % 32) || (ss % 16) || cs >= (1ll << 40) || ss >= (1ll << 40))
+        return LS_ERR_INVALID_ARG;
+    GroupedMxDesc d;
+    d.epi = epilogue;
+    d.A = A;
+    d.a_rows = a_rows;
+    d.b_codes = b_codes;
+    d.b_scales = b_scales;
+    d.b2_codes = b2_codes;
+    d.b2_scales = b2_scales;
+    d.code_stride = cs;
+    d.scale_stride = ss;
+    d.bounds = bounds;
+    d.n_groups = n_groups;
+    d.row_table = row_table;
+    d.row_weight = row_weight;
+    d.gather_k = gather_k;
+    d.C = C;
+    d.M = M;
+    d.N = N;
+    d.K = K;
+    Scratch ws((cudaStream_t)stream);
+    if (!ws.take(grouped_mx_ws_bytes(M, K))) return LS_ERR_OOM;
+    return status_of(launch_gemm_grouped_mx(d, ws.p, entry_error_word(), (cudaStream_t)stream));
+}
+
 }  // extern "C"

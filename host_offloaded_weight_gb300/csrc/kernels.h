@@ -231,6 +231,28 @@ struct MoeFewDesc {
 int64_t moe_few_ws_bytes(bool mx, int T, int k, int H, int F);
 cudaError_t launch_moe_few(const MoeFewDesc& d, void* ws, uint32_t* err, cudaStream_t s);
 
+// ---------------------------------------------------------------- bf16 x MXFP4, grouped rows
+constexpr int GROUPED_MX_MAX_GROUPS = 256;
+struct GroupedMxDesc {
+    int epi = EPI_STORE;            // EPI_STORE, EPI_SWIGLU or EPI_SCALE_F32
+    const void* A = nullptr;        // [a_rows, K] bf16, 16-byte aligned
+    int64_t a_rows = 0;
+    const void* b_codes = nullptr;  // n_groups matrices [N, K], code_stride and scale_stride bytes apart
+    const void* b_scales = nullptr;
+    const void* b2_codes = nullptr; // EPI_SWIGLU: the up matrices
+    const void* b2_scales = nullptr;
+    int64_t code_stride = 0, scale_stride = 0;
+    const int* bounds = nullptr;    // [n_groups + 1]
+    int n_groups = 0;
+    const int* row_table = nullptr; // [M]
+    const float* row_weight = nullptr;
+    int gather_k = 0;               // > 0: sorted row i is A's row row_table[i] / gather_k
+    void* C = nullptr;
+    int M = 0, N = 0, K = 0;
+};
+int64_t grouped_mx_ws_bytes(int64_t M, int64_t K);
+cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* err, cudaStream_t s);
+
 // ---------------------------------------------------------------- shared by the standalone entry points
 uint32_t* entry_error_word();       // device address of the word behind lsk_device_error
 cudaMemPool_t entry_scratch_pool();  // the current device's pool for short-lived scratch; NULL if refused

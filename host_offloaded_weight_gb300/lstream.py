@@ -165,6 +165,7 @@ _sig = {
     "lsk_gemm_bf16_mxfp4": (_I32, [_P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "lsk_moe_few": (_I32, [_P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "lsk_gemm_lora_bf16": (_I32, [_I32, _P, _P, _I64, _I32, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _P]),
+    "lsk_gemm_grouped_bf16_mxfp4": (_I32, [_I32, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _I32, _P, _P, _I32, _P, _I32, _I32, _I32, _P]),
     "ls_helper_share": (C.c_double, [_I64]),
     "ls_host_alloc": (_I32, [_U64, C.POINTER(_P)]),
     "ls_host_free": (_I32, [_P]),
@@ -828,3 +829,30 @@ def lsk_gemm_lora_bf16(epilogue: int, A, B, adapters: LoraAdapters, ids, C_out, 
         epilogue, _values(A, 0, "A"), _values(B, 0, "B"), rows, b2_row_off, adapters.ref, _ids(ids, "ids", M),
         0 if bias is None else _values(bias, 0, "bias"), 0 if resid is None else _values(resid, rf32, "resid"), rf32,
         _values(C_out, 0, "C_out"), 0 if C32 is None else _values(C32, 1, "C32"), M, N, K, _stream(stream)))
+
+
+def _packed(codes, scales, what: str):
+    """Stacked MXFP4 matrices' addresses and the bytes between them."""
+    for t, name in ((codes, what + "_codes"), (scales, what + "_scales")):
+        if t.itemsize != 1:
+            raise TypeError(f"{name} has to be bytes, not {t.dtype}")
+        _expert_rows(t, name)
+    return codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0)
+
+
+def lsk_gemm_grouped_bf16_mxfp4(epilogue: int, A, B_codes, B_scales, group_bounds, n_groups: int, C_out, M: int, N: int, K: int,
+                                B2_codes=None, B2_scales=None, row_table=None, row_weight=None, gather_k: int = 0,
+                                stream=None) -> int:
+    """Rows sorted by group through the groups' MXFP4 matrices: B_codes [n_groups, N, code pitch] and B_scales [n_groups, N, scale pitch]
+    (LSK_EPI_SWIGLU: B2 likewise), A [rows, K] bf16, group_bounds [n_groups + 1] and row_table [M] int32, row_weight [M] float32,
+    C_out [M, N] bf16, float32 for LSK_EPI_SCALE_F32; all but the groups dense. gather_k > 0: row i is A's row row_table[i] // gather_k."""
+    bc, bs, cs, ss = _packed(B_codes, B_scales, "B")
+    b2c = b2s = 0
+    if B2_codes is not None:
+        b2c, b2s, c2, s2 = _packed(B2_codes, B2_scales, "B2")
+        if (c2 != cs or s2 != ss) and n_groups > 1:
+            raise ValueError("B and B2 need the same distance between groups")
+    return _check(_lib.lsk_gemm_grouped_bf16_mxfp4(
+        epilogue, _values(A, 0, "A"), A.shape[0], bc, bs, b2c, b2s, cs, ss, _ids(group_bounds, "group_bounds", n_groups + 1), n_groups,
+        0 if row_table is None else _ids(row_table, "row_table", M), 0 if row_weight is None else _values(row_weight, 1, "row_weight"),
+        gather_k, _values(C_out, int(epilogue == LSK_EPI_SCALE_F32), "C_out"), M, N, K, _stream(stream)))

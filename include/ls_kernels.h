@@ -296,6 +296,25 @@ ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A_dev, const void* B_
                              const void* resid_dev, int32_t resid_f32, void* C_dev, void* C32_dev, int32_t M, int32_t N,
                              int32_t K, void* stream);
 
+/* lsk_gemm_grouped_bf16 with MXFP4 matrices, for any number of rows (lsk_moe_few serves up to 64 tokens in one launch):
+ * sorted row i of group g, group_bounds_dev[g] <= i < group_bounds_dev[g+1], meets matrix g of b_codes_dev and
+ * b_scales_dev, n_groups matrices [N, K] code_stride and scale_stride bytes apart. Row i is row i of A_dev [a_rows, K], or row
+ * row_table_dev[i] / gather_k of it when gather_k > 0, which leaves out lsk_moe_gather (rows outside A count as zero).
+ *   LSK_EPI_STORE      C[i] = a_i B_g^T                              -> bf16 [M, N], sorted rows
+ *   LSK_EPI_SWIGLU     C[i] = SiLU(a_i B_g^T) * (a_i B2_g^T)          -> bf16 [M, N], sorted rows
+ *   LSK_EPI_SCALE_F32  C[row_table[i]] = row_weight[row_table[i]] * a_i B_g^T -> fp32 [M, N]  (entries outside 0 .. M-1 are skipped)
+ * M: rows of the table and of C. Groups may be empty; rows of C that belong to no group are left as they were. A's values enter as
+ * in lsk_gemm_bf16_mxfp4 (exact down to 2^-13 of the largest of their block of 32, within 2^-22 of that largest below); sums are
+ * fp32 in a fixed order, SiLU takes __expf. Any K and N from 1 up where A's rows are 16-byte aligned (K a multiple of 8);
+ * bounds outside 0 .. M are cut to it. Codes 32-byte aligned, strides of them multiples of 32 bytes; scales, A and strides of
+ * scales 16; with one group the strides are not read. n_groups <= 256, M up to 2^30 (LS_ERR_UNSUPPORTED above). Takes scratch on
+ * `stream` from the library's pool, 2 M (K + K / 32) bytes and the padding (LS_ERR_OOM if refused). */
+ls_status lsk_gemm_grouped_bf16_mxfp4(int32_t epilogue, const void* A_dev, int64_t a_rows, const void* b_codes_dev,
+                                      const void* b_scales_dev, const void* b2_codes_dev, const void* b2_scales_dev,
+                                      int64_t code_stride, int64_t scale_stride, const int32_t* group_bounds_dev,
+                                      int32_t n_groups, const int32_t* row_table_dev, const float* row_weight_dev,
+                                      int32_t gather_k, void* C_dev, int32_t M, int32_t N, int32_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
