@@ -22,7 +22,8 @@ using namespace tc;
 constexpr int TILE_P = 128, P_BYTES = TILE_P * 128;
 constexpr int CHUNK = 16;                    // rows of a box: 32 columns with both terms
 constexpr int CHUNK_BYTES = 2 * CHUNK * 128;
-constexpr int TEAM = 4, EPI_WARPS = 4;
+constexpr int TEAM = 4, EPI_WARPS = 8;
+constexpr int PAIR = 16;                     // gate/up tiles: rows of one matrix side by side
 constexpr int MAX_G = GROUPED_MX_MAX_GROUPS;
 
 // MAXC: chunks of a tile at most.
@@ -33,12 +34,12 @@ struct Cfg {
     static constexpr int Q_BYTES = MAXC * CHUNK_BYTES;
     static constexpr int SCALE_BYTES = (1 + PARTS) * 512;
     static constexpr int STAGE = (P_BYTES + Q_BYTES + SCALE_BYTES + 1023) / 1024 * 1024;
-    static constexpr int X_BYTES = 2 * 8 * 64 * 4;             // gate/up: the up rows' sums on their way to the gate rows' warps
-    static constexpr int FIT = (232448 - 1024 - 1024 - X_BYTES - 4 * (MAX_G + 1)) / STAGE;
+    static constexpr int BLOCKS = (MAXC * CHUNK + 31) / 32;    // of 32 rows
+    static constexpr int FIT = (232448 - 1024 - 1024 - 4 * (MAX_G + 1)) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT / 2 * 2 : 8;
     static constexpr int TEAMS = 2, RUN = STAGES >= 5 ? 4 : 2; // scale warps: teams take turns of RUN stages
     static constexpr int SCALE_COLS = 4 * (1 + PARTS);
-    static constexpr int SMEM = STAGES * STAGE + X_BYTES + 1024 + 512;
+    static constexpr int SMEM = STAGES * STAGE + 1024 + 512;
     static constexpr int FIRST_EPI = 2 + TEAM * TEAMS, THREADS = 32 * (FIRST_EPI + EPI_WARPS);
     static constexpr int TMEM_COLS = 512;
     static_assert(2 * BQ + STAGES * SCALE_COLS <= 512, "tensor memory: two accumulators and each stage's scales");
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
-    const uint32_t bars = base + S * C::STAGE + C::X_BYTES;
+    const uint32_t bars = base + S * C::STAGE;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (S + s); };
     auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
@@ -174,8 +175,14 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             auto weights = [&](int st, int k) {
                 const uint32_t at = base + st * C::STAGE;
                 bar_expect(full(st), bytes);
-                tma_3d(at, &p.map_p, full(st), k * 128, tl.p0, tl.g);  // boxes of 64 rows
-                tma_3d(at + P_BYTES / 2, p.dual ? &p.map_p2 : &p.map_p, full(st), k * 128, p.dual ? tl.p0 : tl.p0 + 64, tl.g);
+                if (p.dual) {
+                    for (int i = 0; i < TILE_P / 2; i += PAIR) {
+                        tma_3d(at + 2 * i * 128, &p.map_p, full(st), k * 128, tl.p0 + i, tl.g);
+                        tma_3d(at + (2 * i + PAIR) * 128, &p.map_p2, full(st), k * 128, tl.p0 + i, tl.g);
+                    }
+                } else {
+                    tma_3d(at, &p.map_p, full(st), k * 128, tl.p0, tl.g);
+                }
             };
             auto rows = [&](int st, int k) {
                 const uint32_t at = base + st * C::STAGE + P_BYTES;
@@ -288,8 +295,8 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             }
             const int64_t at = 4ll * RUN * u.run;
             const int r = 32 * w + lane;
-            const bool second = p.dual && r >= 64;
-            const int row = tl.p0 + (second ? r - 64 : r);
+            const bool second = p.dual && (r & PAIR);
+            const int row = tl.p0 + (p.dual ? r / (2 * PAIR) * PAIR + (r & (PAIR - 1)) : r);
             words((second ? p.scale_p2 : p.scale_p) + tl.g * p.scale_stride + (int64_t)row * p.scale_pitch + at, row < p.N, to[0]);
 #pragma unroll
             for (int j = 0; j < C::PARTS; ++j) {
@@ -327,52 +334,70 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         }
     } else {
         // ------------------------------------------------------------ results
-        const int q = warp & 3, row = 32 * q + lane;  // q: the TMEM lane quarter that this warp can read
-        float* swap = reinterpret_cast<float*>(gbase + S * C::STAGE);
-        bool dead = false;  // an aborted warp goes through the same steps without waits and results
-        int turn = 0, n = 0;
+        // Two warps a TMEM lane quarter, each with every second group of eight rows. A lane has a weight row, an output column.
+        // Gate/up tiles alternate: 16 gate rows, the 16 up rows of the same columns, so that a lane's partner is 16 lanes away;
+        // each of the two finishes half of the group's rows.
+        const int q = warp & 3, half = (warp - C::FIRST_EPI) >> 2, row = 32 * q + lane;  // q: the lane quarter that this warp can read
+        const bool upper = lane & 16;
+        int n = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
             const Tile tl = tile_at<MAXC>(p, first, t);
             const int b = n & 1;
-            if (!dead && (!bar_wait_warp(acc_full(b), (uint32_t)(n >> 1) & 1u, p.err, 4) || stop)) {
+            // places and weights of the rows, read while the products run: lane l has rows l, 32 + l, ...
+            int to[C::BLOCKS];
+            float w[C::BLOCKS];
+            if (p.epi == EPI_SCALE_F32) {
+#pragma unroll
+                for (int c = 0; c < C::BLOCKS; ++c) {
+                    to[c] = 32 * c + lane < tl.rows ? __ldg(p.row_table + tl.row + 32 * c + lane) : -1;
+                    if (to[c] >= p.M) to[c] = -1;
+                    w[c] = to[c] >= 0 ? __ldg(p.row_weight + to[c]) : 0.f;
+                }
+            }
+            if (!bar_wait_warp(acc_full(b), (uint32_t)(n >> 1) & 1u, p.err, 4) || stop) {
                 stop = 1;
-                dead = true;
+                break;
             }
             fence_after_sync();
             const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::BQ);
+            const int col = tl.p0 + (p.dual ? 16 * q + (lane & 15) : row);
+#pragma unroll
+            for (int c = 0; c < C::BLOCKS; ++c) {
 #pragma unroll 1
-            for (int i0 = 0; i0 < tl.rows; i0 += 8) {
-                uint32_t x[8], y[8];
-                const uint32_t c = at + (uint32_t)(i0 / CHUNK * 32 + i0 % CHUNK);
-                tmem_load8(c, x);
-                tmem_load8(c + CHUNK, y);
-                tmem_load_wait();
-                float v[8];
+                for (int g = half; g < 4; g += 2) {
+                    const int i0 = 32 * c + 8 * g;
+                    if (i0 >= tl.rows) break;
+                    uint32_t x[8], y[8];
+                    const uint32_t a = at + (uint32_t)(i0 / CHUNK * 32 + i0 % CHUNK);
+                    tmem_load8(a, x);
+                    tmem_load8(a + CHUNK, y);
+                    tmem_load_wait();
+                    float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(y[j]) + __uint_as_float(x[j]);  // the smaller term first
-                int col = tl.p0 + row;
-                if (p.dual) {
-                    float* xs = swap + (turn++ & 1) * 8 * 64 + (row & 63);
-                    if (q >= 2) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) xs[64 * j] = v[j];
-                    }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    if (q >= 2) continue;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = v[j] / (1.f + __expf(-v[j])) * xs[64 * j];
-                }
-                if (col >= p.N || dead) continue;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = tl.row + i0 + j;
-                    if (i0 + j >= tl.rows) continue;
+                    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(y[j]) + __uint_as_float(x[j]);  // the smaller term first
                     if (p.epi == EPI_SCALE_F32) {
-                        const int to = p.row_table[i];
-                        if (to < 0 || to >= p.M) continue;
-                        static_cast<float*>(p.C)[(int64_t)to * p.N + col] = p.row_weight[to] * v[j];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int r = __shfl_sync(0xffffffffu, to[c], 8 * g + j);
+                            const float wr = __shfl_sync(0xffffffffu, w[c], 8 * g + j);
+                            if (r >= 0 && col < p.N) static_cast<float*>(p.C)[(int64_t)r * p.N + col] = wr * v[j];
+                        }
                     } else {
-                        static_cast<__nv_bfloat16*>(p.C)[(int64_t)i * p.N + col] = __float2bfloat16_rn(v[j]);
+                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + (int64_t)(tl.row + i0) * p.N + col;
+                        const int rows = col < p.N ? tl.rows - i0 : 0;
+                        if (p.dual) {
+                            if (upper) out += 4ll * p.N;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 4], 16);
+                                const float gate = upper ? other : v[j], up = upper ? v[j + 4] : other;
+                                if (j + (upper ? 4 : 0) < rows) out[(int64_t)j * p.N] = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (j < rows) out[(int64_t)j * p.N] = __float2bfloat16_rn(v[j]);
+                        }
                     }
                 }
             }
@@ -390,47 +415,50 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
 }
 
 // The two terms of the rows in sorted order, [2][M][pitch] bytes and their scales likewise; with k > 0 row i is row table[i] / k
-// of a, rows outside a are zero. A thread takes 8 values, four lanes a block.
+// of a, rows outside a are zero. A thread takes 8 values, four lanes a block; a CTA a run of the array's units.
 __global__ void __launch_bounds__(256)
 split_sorted_kernel(const __nv_bfloat16* __restrict__ a, const int* __restrict__ table, int k, int64_t a_rows, int M, int K, uint32_t per_row,
-                    uint8_t* __restrict__ terms, uint8_t* __restrict__ scales, int scale_pitch) {
+                    uint32_t rows_a_cta, uint8_t* __restrict__ terms, uint8_t* __restrict__ scales, int scale_pitch) {
     grid_wait();
     grid_release();  // everything earlier is complete: the product may start on the weights
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t total = (int64_t)M * per_row;
-    const int row = (int)(i / per_row);
-    const uint32_t g = (uint32_t)(i % per_row);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (i < total) {
-        const int64_t from = k > 0 ? table[row] / k : row;
-        if (from >= 0 && from < a_rows) v = row8(a + from * K, (int)g * 8, K, 1);
-    }
-    uint2 o1, o2;
-    uint32_t b1, b2;
-    split8(v, o1, o2, b1, b2);
-    if (i >= total) return;
-    reinterpret_cast<uint2*>(terms)[i] = o1;
-    reinterpret_cast<uint2*>(terms)[i + total] = o2;
-    if ((g & 3) == 0) {
-        uint8_t* s1 = scales + (int64_t)row * scale_pitch;
-        uint8_t* s2 = s1 + (int64_t)M * scale_pitch;
-        s1[g >> 2] = (uint8_t)b1;
-        s2[g >> 2] = (uint8_t)b2;
-        if (g + 4 == per_row)
-            for (int j = (int)(per_row >> 2); j < scale_pitch; ++j) s1[j] = s2[j] = 0;
+    const int row0 = (int)(blockIdx.x * rows_a_cta);
+    const uint32_t units = min((int)rows_a_cta, M - row0) * per_row, most = (units + 31) & ~31u;
+    const int64_t total = (int64_t)M * per_row, at = (int64_t)row0 * per_row;
+    for (uint32_t i = threadIdx.x; i < most; i += 256) {  // whole warps: a block's lanes work together
+        const uint32_t r = i / per_row, g = i - r * per_row;
+        const int row = row0 + (int)r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < units) {
+            const int64_t from = k > 0 ? __ldg(table + row) / k : row;
+            if (from >= 0 && from < a_rows) v = row8(a + from * K, (int)g * 8, K, 1);
+        }
+        uint2 o1, o2;
+        uint32_t b1, b2;
+        split8(v, o1, o2, b1, b2);
+        if (i >= units) continue;
+        reinterpret_cast<uint2*>(terms)[at + i] = o1;
+        reinterpret_cast<uint2*>(terms)[at + i + total] = o2;
+        if ((g & 3) == 0) {
+            uint8_t* s1 = scales + (int64_t)row * scale_pitch;
+            uint8_t* s2 = s1 + (int64_t)M * scale_pitch;
+            s1[g >> 2] = (uint8_t)b1;
+            s2[g >> 2] = (uint8_t)b2;
+            if (g + 4 == per_row)
+                for (int j = (int)(per_row >> 2); j < scale_pitch; ++j) s1[j] = s2[j] = 0;
+        }
     }
 }
 
 // ------------------------------------------------------------------ host side
 int64_t up128(int64_t n) { return (n + 127) / 128 * 128; }
 
-// MXFP4 codes of n matrices [rows, pitch bytes], `stride` bytes apart, unpacked to a byte a value, in boxes of 128 values x 64 rows.
-bool map_weights(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int64_t n, int64_t stride) {
+// MXFP4 codes of n matrices [rows, pitch bytes], `stride` bytes apart, unpacked to a byte a value, in boxes of 128 values x box_rows.
+bool map_weights(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int64_t n, int64_t stride, int box_rows) {
     const MxEncodeFn fn = mx_encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)(2 * pitch), (cuuint64_t)rows, (cuuint64_t)n};
     cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)stride};
-    cuuint32_t box[3] = {128, 64, 1};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
     cuuint32_t one[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -479,8 +507,9 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     uint8_t* scales = terms + 2 * M * kp;
     p.dual = d.epi == EPI_SWIGLU;
     p.epi = d.epi;
-    if (!map_weights(&p.map_p, d.b_codes, d.N, mx_code_pitch(d.K), d.n_groups, d.code_stride) ||
-        (p.dual && !map_weights(&p.map_p2, d.b2_codes, d.N, mx_code_pitch(d.K), d.n_groups, d.code_stride)) ||
+    const int box = p.dual ? PAIR : TILE_P;
+    if (!map_weights(&p.map_p, d.b_codes, d.N, mx_code_pitch(d.K), d.n_groups, d.code_stride, box) ||
+        (p.dual && !map_weights(&p.map_p2, d.b2_codes, d.N, mx_code_pitch(d.K), d.n_groups, d.code_stride, box)) ||
         !map_terms(&p.map_q, terms, M, kp))
         return cudaErrorInvalidValue;
     p.scale_p = static_cast<const uint8_t*>(d.b_scales);
@@ -500,8 +529,8 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     p.C = d.C;
     p.err = err;
     const uint32_t per_row = (uint32_t)(kp / 8);
-    const int64_t blocks = (M * per_row + 255) / 256;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    const uint32_t rows_a_cta = std::max<uint32_t>(1, 1024 / per_row);  // about 1024 units
+    const int64_t blocks = (M + rows_a_cta - 1) / rows_a_cta;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(256);
@@ -512,7 +541,7 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, split_sorted_kernel, static_cast<const __nv_bfloat16*>(d.A), d.gather_k > 0 ? d.row_table : nullptr,
-                                             d.gather_k, d.a_rows, d.M, d.K, per_row, terms, scales, p.scale_pitch);
+                                             d.gather_k, d.a_rows, d.M, d.K, per_row, rows_a_cta, terms, scales, p.scale_pitch);
     if (e != cudaSuccess) return e;
     // rows of a tile at most: groups of 32 rows and fewer are bound by the weights' bytes and want more stages of them in flight
     const bool small = M <= 32ll * d.n_groups;
