@@ -94,7 +94,8 @@ struct GemmParams {
 struct LoraGemmParams : GemmParams {
     CUtensorMap tmH, tmUp, tmUp2;
     const int* lora_count;   // [row tile] adapters
-    const int* lora_list;    // [row tile][lora_cap] which; -1: not finite, read as zeros
+    const int* lora_list;    // [row tile][lora_cap] which
+    const uint8_t* lora_notes;  // [adapter][16] not all zero: not finite, read as zeros (its third term of h is NaN)
     int lora_cap, lora_cw, lora_chunks, lora_parts, lora_rank;
 };
 
@@ -926,24 +927,40 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                 if constexpr (LORA) {
                     if (!waited) grid_dep_wait();
                     waited = true;
-                    const int more = ok ? p.lora_count[m2] * p.lora_parts * 2 : 0, cw = p.lora_cw;
-                    for (int e = 0; e < more; ++e, ++it) {
-                        const int s = it % S2_STAGES;
-                        if (!mbar_wait(empty_bar(s), ((uint32_t)(it / S2_STAGES) & 1u) ^ 1u, p.err, 1, p.mbar_limit_ns)) {
-                            ok = false;
-                            s_abort = 1;
-                            break;
+                    const int count = ok ? p.lora_count[m2] : 0, cw = p.lora_cw;
+                    const int* list = p.lora_list + (int64_t)m2 * p.lora_cap;
+                    for (int j0 = 0; j0 < count && ok; j0 += 8) {
+                        int next[8];  // adapters, those that are not finite as -1 - a: eight loads in flight
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) next[i] = j0 + i < count ? list[j0 + i] : list[j0];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(p.lora_notes + 16ll * next[i]);
+                            if (v.x | v.y | v.z | v.w) next[i] = -1 - next[i];
                         }
-                        const int part = (e >> 1) % p.lora_parts, j = (e >> 1) / p.lora_parts, half = part / p.lora_chunks;
-                        const int a = p.lora_list[(int64_t)m2 * p.lora_cap + j];
-                        const uint32_t sa = base + s * S2_STAGE, leader_full = mapa(full_bar(s), 0);
-                        if (leader) mbar_expect_tx(full_bar(s), 2 * (128 + BN / 2) * cw * 2);
-                        tma_load_2d_2sm(sa, &p.tmH, leader_full, 0, (int)((((int64_t)m2 * p.lora_cap * p.lora_parts * 2) + e) * 256) + (int)rank * 128);
-                        // out of bounds: zeros, for an adapter that is not finite and for the other half of a gate/up tile
-                        const bool none = a < 0 || (DUAL && half != (int)rank);
-                        tma_load_3d_2sm(sa + S2_A, half ? &p.tmUp2 : &p.tmUp, leader_full, part % p.lora_chunks * cw,
-                                        none ? p.N : DUAL ? n * 128 : b_row, max(a, 0));
-                        issued_mask |= 1u << s;
+                        const int end = min(8, count - j0) * p.lora_parts * 2;
+                        for (int e = 0; e < end; ++e, ++it) {
+                            const int s = it % S2_STAGES;
+                            if (!mbar_wait(empty_bar(s), ((uint32_t)(it / S2_STAGES) & 1u) ^ 1u, p.err, 1, p.mbar_limit_ns)) {
+                                ok = false;
+                                s_abort = 1;
+                                break;
+                            }
+                            const int part = (e >> 1) % p.lora_parts, i = (e >> 1) / p.lora_parts, half = part / p.lora_chunks;
+                            int a = next[0];
+#pragma unroll
+                            for (int o = 1; o < 8; ++o) a = o == i ? next[o] : a;
+                            const uint32_t sa = base + s * S2_STAGE, leader_full = mapa(full_bar(s), 0);
+                            if (leader) mbar_expect_tx(full_bar(s), 2 * (128 + BN / 2) * cw * 2);
+                            const int64_t block = ((int64_t)m2 * p.lora_cap + j0 + i) * p.lora_parts + part;
+                            tma_load_2d_2sm(sa, &p.tmH, leader_full, 0,
+                                            (int)((block * LORA_TERMS + (a < 0 ? 2 : e & 1)) * 256) + (int)rank * 128);
+                            // out of bounds: zeros, for an adapter that is not finite and for the other half of a gate/up tile
+                            const bool none = a < 0 || (DUAL && half != (int)rank);
+                            tma_load_3d_2sm(sa + S2_A, half ? &p.tmUp2 : &p.tmUp, leader_full, part % p.lora_chunks * cw,
+                                            none ? p.N : DUAL ? n * 128 : b_row, max(a, 0));
+                            issued_mask |= 1u << s;
+                        }
                     }
                 }
             }
@@ -1628,6 +1645,7 @@ cudaError_t launch_gemm_bf16_lora(const GemmDesc& d, const LoraArgs& l, int64_t 
     p.pdl = 1;
     p.lora_count = l.count;
     p.lora_list = l.list;
+    p.lora_notes = l.notes;
     p.lora_cap = l.cap;
     p.lora_cw = l.cw;
     p.lora_chunks = l.chunks;

@@ -1,16 +1,14 @@
 // A shared projection with low-rank adapters of many requests beside it:
 //   C[t] = epi(W x_t + s_a up_a (down_a x_t)),  a = ids[t]  (none for a row whose id is not an adapter's)
 //
-// Three launches, each released by the one before as soon as it runs:
-//   1. lora_check_kernel reads the `up` matrices of the adapters in use and notes those that hold a NaN or an infinity.
-//   2. lora_down_kernel writes h_t = s_a down_a x_t as blocks: one for each tile of rows and each adapter with a row in
-//      it, zero in the rows of others.
-//   3. the shared product, which takes a block with its adapter's `up` as some more columns of K. Its loads of the
-//      shared weights start at once; only these last columns wait for the blocks.
+// Two launches. lora_rows_kernel writes h_t = s_a down_a x_t as blocks: one for each tile of rows and each adapter with a row in
+// it, zero in the rows of others. The shared product then takes a block with its adapter's `up` as some more columns of K. It
+// starts as soon as the first kernel's CTAs run: its loads of the shared weights need nothing of it, only these last columns do.
 // h is kept as two bf16 terms (16 bits: the first term alone would be off by 2^-9, more than the fp32 sums lose).
 //
-// 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests. Its `up`
-// is therefore read out of bounds, which gives zeros, and its own rows of h are NaN: they come out NaN, no others do.
+// 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests. Other CTAs of the
+// first kernel look over the `up` matrices of the adapters in use (bytes that the product then finds in L2). One that is not finite is
+// read out of bounds, which gives zeros, against a third term that is NaN in its own rows: they come out NaN, no others do.
 //
 // Up to 128 rows (gemm_lora_few_kernel, below): the weights are the left operand (128 rows a tile) and the tokens the
 // right one, 16 to 128 columns. More rows: the pair kernel of k_gemm.cu.
@@ -26,37 +24,41 @@ using namespace tc;
 
 constexpr int DOWN_THREADS = 256, DOWN_WARPS = 8, SUB = 16;  // rows of a CTA of the down kernel
 constexpr int MAX_TILE = 256;
+constexpr int MAX_SLICES = 8;         // of K
 
-// ------------------------------------------------------------------ are the adapters in use finite?
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {  // two bf16
     return (uint32_t)((w & 0x7f80u) == 0x7f80u) | (uint32_t)((w & 0x7f800000u) == 0x7f800000u);
 }
-__global__ void __launch_bounds__(256) lora_check_kernel(const __grid_constant__ LoraArgs p) {
-    grid_release();
-    const int a = (int)blockIdx.x / p.check_parts, part = (int)blockIdx.x % p.check_parts;
+
+// A part of an adapter's `up` matrices: its notes, 16 bytes an adapter, are nonzero where a value is not finite.
+__device__ __forceinline__ void look_over(const LoraArgs& p, int cta) {
+    const int a = cta / p.check_parts, part = cta % p.check_parts;
     int used = 0;
-    for (int t = threadIdx.x; t < p.T; t += 256) used |= p.ids[t] == a;
+#pragma unroll 4
+    for (int t = threadIdx.x; t < p.T; t += DOWN_THREADS) used |= __ldg(p.ids + t) == a;
     if (!__syncthreads_or(used)) return;
     const int64_t units = (int64_t)p.N * p.rank / 8;  // of 16 bytes
     const int64_t u0 = units * part / p.check_parts, u1 = units * (part + 1) / p.check_parts;
     uint32_t bad = 0;
     for (int half = 0; half < (p.up2 ? 2 : 1); ++half) {
         const uint4* u = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(half ? p.up2 : p.up) + a * p.up_stride);
-#pragma unroll 4
-        for (int64_t i = u0 + threadIdx.x; i < u1; i += 256) {
+#pragma unroll 8
+        for (int64_t i = u0 + threadIdx.x; i < u1; i += DOWN_THREADS) {
             const uint4 v = __ldg(u + i);
             bad |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
         }
     }
     bad = __syncthreads_or((int)bad);
-    if (threadIdx.x == 0) p.bad[(int64_t)a * p.check_parts + part] = bad ? 1 : 0;
+    const int bytes = 16 / p.check_parts;
+    if (threadIdx.x < bytes) p.notes[16ll * a + part * bytes + threadIdx.x] = bad ? 1 : 0;
 }
 
 // ------------------------------------------------------------------ h
-// A CTA has 16 rows of a tile and 8 NT columns of h, for one adapter of the tile after the other: m16n8k16 products
-// (bound by the loads: the shared product's tensor core form would want 128 rows and a TMA ring for 16 columns), K dealt
-// to eight warps, whose sums are added in their order. A lane's 16 bytes of a row of x and of `down` are the same eight
-// values of K, so which of them a product calls its first does not matter: a warp's load takes 64 bytes of each of eight rows.
+// A CTA has 16 of the rows that an adapter has in a tile, 8 NT columns of h and a slice of K (a cluster has all of it), for one
+// adapter of the tile after the other: m16n8k16 products (bound by the loads: the shared product's tensor core form would want 128 rows and a TMA ring for 16
+// columns), K dealt to eight warps. The sums of the warps and of the cluster's CTAs are added in their order. A lane's 16 bytes of
+// a row of x and of `down` are the same eight values of K, so which of them a product calls its first does not matter: a warp's
+// load takes 64 bytes of each of eight rows.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -64,21 +66,34 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 template <int NT>
-__global__ void __launch_bounds__(DOWN_THREADS) lora_down_kernel(const __grid_constant__ LoraArgs p) {
-    constexpr int COLS = 8 * NT;
+__global__ void __launch_bounds__(DOWN_THREADS) lora_rows_kernel(const __grid_constant__ LoraArgs p) {
+    constexpr int COLS = 8 * NT, UNITS = SUB * COLS / 2;  // units: two columns of a row
     __shared__ __align__(16) int s_ids[MAX_TILE];
     __shared__ int s_list[MAX_TILE];
-    __shared__ int s_warp[DOWN_WARPS + 1];
+    __shared__ int s_warp[2][DOWN_WARPS];
+    __shared__ int s_rows[SUB];
     __shared__ float s_sum[DOWN_WARPS][SUB][COLS + 1];
+    __shared__ float2 s_red[2][UNITS + MAX_SLICES];
     grid_release();
+    if ((int)blockIdx.x >= p.rows_ctas) {
+        look_over(p, (int)blockIdx.x - p.rows_ctas);
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int subs = p.tile_rows / SUB, tile = (int)blockIdx.x / subs, row0 = (int)blockIdx.x % subs * SUB;
-    const int t0 = tile * p.tile_rows;
+    // slices (a cluster) innermost, then columns, slots, 16 rows
+    int at = (int)blockIdx.x;
+    const int slice = at % p.slices;
+    at /= p.slices;
+    const int col0 = at % p.col_ctas * COLS;
+    at /= p.col_ctas;
+    const int slot = at % p.slots;
+    at /= p.slots;
+    const int subs = p.tile_rows / SUB, tile = at / subs, row0 = at % subs * SUB, t0 = tile * p.tile_rows;
 
     // the tile's adapters, in the order of their first rows
     int id = -1;
     if (tid < p.tile_rows && t0 + tid < p.T) {
-        id = p.ids[t0 + tid];
+        id = __ldg(p.ids + t0 + tid);
         if (id < 0 || id >= p.n) id = -1;
     }
     s_ids[tid] = id;
@@ -89,35 +104,47 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_kernel(const __grid_co
         if ((v.x == id) || (u + 1 < tid && v.y == id) || (u + 2 < tid && v.z == id) || (u + 3 < tid && v.w == id)) first = false;
     }
     const uint32_t vote = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) s_warp[warp + 1] = __popc(vote);
-    if (tid == 0) s_warp[0] = 0;
+    if (lane == 0) s_warp[1][warp] = __popc(vote);
     __syncthreads();
     int before = 0, count = 0;
     for (int w = 0; w < DOWN_WARPS; ++w) {
-        if (w < warp) before += s_warp[w + 1];
-        count += s_warp[w + 1];
+        if (w < warp) before += s_warp[1][w];
+        count += s_warp[1][w];
     }
     if (first) s_list[before + __popc(vote & ((1u << lane) - 1u))] = id;
     __syncthreads();
-    grid_wait();  // the notes on the adapters
+    const bool writes_list = row0 == 0 && col0 == 0 && slot == 0 && slice == 0;
+    if (writes_list) {
+        if (tid < count) p.list[(int64_t)tile * p.cap + tid] = s_list[tid];
+        if (tid == 0) p.count[tile] = count;
+    }
+    if (p.slices > 1) cluster_barrier();  // the others' shared memory is there
 
     const int g = lane >> 2, q = lane & 3;
-    const int col0 = (int)blockIdx.z * COLS;                 // of the block's columns: parts of width cw, side by side
-    const int part = col0 / p.cw, half = part / p.chunks, c0 = col0 % p.cw, r0 = part % p.chunks * p.cw + c0;
-    for (int j = (int)blockIdx.y; j < count; j += (int)gridDim.y) {
+    const int part = col0 / p.cw, half = part / p.chunks, c0 = col0 % p.cw, r0 = part % p.chunks * p.cw + c0;  // parts of width cw, side by side
+    const int k_first = slice * p.slice_k, k_end = min(p.K, k_first + p.slice_k);
+    auto owner_first = [&](int o) { return (UNITS * o + p.slices - 1) / p.slices; };  // a CTA of the cluster finishes these units and up
+    const int own0 = owner_first(slice), own1 = owner_first(slice + 1);
+    int turn = 0;
+    for (int j = slot; j < count; j += p.slots, ++turn) {
         const int a = s_list[j];
-        bool bad = false;
-        for (int i = 0; i < p.check_parts; ++i) bad = bad || p.bad[(int64_t)a * p.check_parts + i];
-        if (row0 == 0 && col0 == 0 && tid == 0) {
-            p.list[(int64_t)tile * p.cap + j] = bad ? -1 : a;
-            if (j == 0) p.count[tile] = count;
+        // the adapter's rows row0, row0 + 1, ... of the tile, of however many it has
+        const uint32_t mine = __ballot_sync(0xffffffffu, s_ids[tid] == a);
+        if (lane == 0) s_warp[turn & 1][warp] = __popc(mine);
+        __syncthreads();
+        int rank = __popc(mine & ((1u << lane) - 1u)) - row0, rows = -row0;
+        for (int w = 0; w < DOWN_WARPS; ++w) {
+            if (w < warp) rank += s_warp[turn & 1][w];
+            rows += s_warp[turn & 1][w];
         }
-        const bool on0 = s_ids[row0 + g] == a, on1 = s_ids[row0 + g + 8] == a;
-        const bool any = __any_sync(0xffffffffu, on0 || on1);   // the same in every warp
-        float acc[NT][4] = {};
-        if (any && !bad) {
-            const __nv_bfloat16* x0 = p.x + (int64_t)(t0 + row0 + g) * p.K;
-            const __nv_bfloat16* x1 = x0 + 8 * (int64_t)p.K;
+        if (s_ids[tid] == a && rank >= 0 && rank < SUB) s_rows[rank] = tid;
+        __syncthreads();
+        const bool any = rows > 0;   // the same in the cluster
+        if (any) {
+            const bool on0 = g < rows, on1 = g + 8 < rows;
+            float acc[NT][4] = {};
+            const __nv_bfloat16* x0 = p.x + (int64_t)(t0 + (on0 ? s_rows[g] : 0)) * p.K;
+            const __nv_bfloat16* x1 = p.x + (int64_t)(t0 + (on1 ? s_rows[g + 8] : 0)) * p.K;
             const uint8_t* down = static_cast<const uint8_t*>(p.down) + a * p.down_stride;
             const __nv_bfloat16* d[NT];
             bool in[NT];
@@ -129,12 +156,12 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_kernel(const __grid_co
             }
             const uint4 zero = make_uint4(0, 0, 0, 0);
             constexpr int U = NT <= 2 ? 4 : 2;
-            for (int k0 = 32 * warp + 8 * q; k0 < p.K + 8 * q; k0 += 32 * DOWN_WARPS * U) {
+            for (int k0 = k_first + 32 * warp; k0 < k_end; k0 += 32 * DOWN_WARPS * U) {
                 uint4 va[U], vb[U], vd[U][NT];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int k = k0 + 32 * DOWN_WARPS * u;
-                    const bool k_in = k < p.K;  // K is a multiple of 8
+                    const int k = k0 + 32 * DOWN_WARPS * u + 8 * q;
+                    const bool k_in = k < k_end;  // K and the slices are multiples of 8
                     va[u] = on0 && k_in ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : zero;
                     vb[u] = on1 && k_in ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : zero;
 #pragma unroll
@@ -148,8 +175,6 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_kernel(const __grid_co
                         mma16816(acc[n], va[u].z, vb[u].z, va[u].w, vb[u].w, vd[u][n].z, vd[u][n].w);
                     }
             }
-        }
-        if (any) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 s_sum[warp][g][8 * n + 2 * q] = acc[n][0];
@@ -157,37 +182,63 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_down_kernel(const __grid_co
                 s_sum[warp][g + 8][8 * n + 2 * q] = acc[n][2];
                 s_sum[warp][g + 8][8 * n + 2 * q + 1] = acc[n][3];
             }
-        }
-        __syncthreads();
-        const float scale = p.scale ? p.scale[a] : 1.f;
-        const int64_t block = (((int64_t)tile * p.cap + j) * p.parts + part) * 2;
-        for (int i = tid; i < SUB * COLS / 2; i += DOWN_THREADS) {
-            const int r = i / (COLS / 2), c = i % (COLS / 2) * 2;
-            uint32_t hi = 0, lo = 0;
-            if (any && s_ids[row0 + r] == a) {
+            __syncthreads();
+            float2* red = s_red[turn & 1];
+            for (int i = tid; i < UNITS; i += DOWN_THREADS) {
+                const int r = i / (COLS / 2), c = i % (COLS / 2) * 2;
+                float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float v = 0.f;
-                    if (r0 + c + e < p.rank) {
-#pragma unroll
-                        for (int w = 0; w < DOWN_WARPS; ++w) v += s_sum[w][r][c + e];
-                        v *= scale;
-                        if (bad) v = __uint_as_float(0x7fc00000u);
-                    }
-                    float t1 = __bfloat162float(__float2bfloat16_rn(v));
-                    if (isinf(t1) && !isinf(v)) t1 = __bfloat162float(__float2bfloat16_rz(v));
-                    const float t2 = isfinite(t1) ? v - t1 : 0.f;
-                    hi |= (__float_as_uint(t1) >> 16) << (16 * e);
-                    lo |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(t2)) << (16 * e);
+                for (int w = 0; w < DOWN_WARPS; ++w) {
+                    v.x += s_sum[w][r][c];
+                    v.y += s_sum[w][r][c + 1];
+                }
+                if (p.slices == 1) {
+                    red[i] = v;
+                } else {
+                    const int o = i * p.slices / UNITS, o0 = owner_first(o), share = owner_first(o + 1) - o0;
+                    const uint32_t to = cluster_addr(smem_addr(red + slice * share + i - o0), o);
+                    st_cluster(to, v.x);
+                    st_cluster(to + 4, v.y);
                 }
             }
-            uint32_t* to = reinterpret_cast<uint32_t*>(p.h + (block * p.tile_rows + row0 + r) * p.cw + c0 + c);
-            to[0] = hi;
-            to[(int64_t)p.tile_rows * p.cw / 2] = lo;
+            if (p.slices > 1) cluster_barrier();
+            else __syncthreads();
         }
-        __syncthreads();
+        const float scale = p.scale ? p.scale[a] : 1.f;
+        const float2* red = s_red[turn & 1];
+        const int64_t block = (((int64_t)tile * p.cap + j) * p.parts + part) * LORA_TERMS;
+        const int64_t term = (int64_t)p.tile_rows * p.cw / 2;
+        for (int i = own0 + tid; i < own1; i += DOWN_THREADS) {
+            const int r = i / (COLS / 2), c = i % (COLS / 2) * 2;
+            uint32_t* to = reinterpret_cast<uint32_t*>(p.h + block * p.tile_rows * p.cw + c0 + c);
+            // rows row0 and up of the tile that are not the adapter's are zero
+            if (s_ids[row0 + r] != a) {
+                uint32_t* z = to + (int64_t)(row0 + r) * p.cw / 2;
+                z[0] = z[term] = z[2 * term] = 0;
+            }
+            if (r >= rows) continue;
+            float2 v = make_float2(0.f, 0.f);
+            for (int o = 0; o < p.slices; ++o) {
+                const float2 x = red[o * (own1 - own0) + i - own0];
+                v.x += x.x;
+                v.y += x.y;
+            }
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float h = r0 + c + e < p.rank ? (e ? v.y : v.x) * scale : 0.f;
+                float t1 = __bfloat162float(__float2bfloat16_rn(h));
+                if (isinf(t1) && !isinf(h)) t1 = __bfloat162float(__float2bfloat16_rz(h));
+                const float t2 = isfinite(t1) ? h - t1 : 0.f;
+                hi |= (__float_as_uint(t1) >> 16) << (16 * e);
+                lo |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(t2)) << (16 * e);
+            }
+            to += (int64_t)s_rows[r] * p.cw / 2;
+            to[0] = hi;
+            to[term] = lo;
+            to[2 * term] = 0x7fc07fc0u;  // NaN
+        }
     }
-    if (count == 0 && row0 == 0 && col0 == 0 && blockIdx.y == 0 && tid == 0) p.count[tile] = 0;
 }
 
 // ------------------------------------------------------------------ the shared product, few rows
@@ -221,6 +272,7 @@ struct FewLora {
     int cw, chunks, parts, rank;   // columns of a part of h; parts of a rank, of a block
     const int* count;
     const int* list;
+    const uint8_t* notes;
     const __nv_bfloat16* bias;
     const void* resid;
     int resid_f32;
@@ -263,6 +315,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
     const uint32_t done = bars + 8u * (2 * S + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (2 * S + 5));
     __shared__ volatile int stop;
+    __shared__ int s_list[LORA_FEW_ROWS];  // adapters; those that are not finite as -1 - a
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -288,8 +341,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
     if (p.splits > 1) cluster_barrier();
     else __syncthreads();
     fence_after_sync();
-    // The kernel before this one and the one before that are this call's own, and the first of them began when everything
-    // earlier was complete: the weights and the rows of x may be read at once, only the blocks have to be waited for.
+    // The kernel before this one is this call's own and began when everything earlier was complete: the weights and the rows
+    // of x may be read at once, only the blocks have to be waited for.
     const uint32_t tmem = *tmem_slot;
     const int slice = (int)blockIdx.x % p.splits, tile0 = (int)blockIdx.x / p.splits, step = (int)gridDim.x / p.splits;
     const int k0 = (int)((int64_t)slice * p.k_stages / p.splits), k1 = (int)((int64_t)(slice + 1) * p.k_stages / p.splits);
@@ -329,12 +382,19 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
             if (!ok) break;
             if (more < 0) {
                 grid_wait();
-                more = *p.count * p.parts;
+                const int count = *p.count;
+                for (int j = lane; j < count; j += 32) {
+                    const int a = p.list[j];
+                    const uint4 n = *reinterpret_cast<const uint4*>(p.notes + 16ll * a);
+                    s_list[j] = n.x | n.y | n.z | n.w ? -1 - a : a;
+                }
+                __syncwarp();
+                more = count * p.parts;
             }
             const int up_bytes = TILE_P * p.cw * 2;
             for (int e = slice; e < more && turn(); e += p.splits, next()) {
                 const int j = e / p.parts, part = e % p.parts, half = part / p.chunks, col = part % p.chunks * p.cw;
-                const int a = p.list[j];
+                const int a = s_list[j];
                 if (!one) continue;
                 const uint32_t at = base + s * F::STAGE;
                 bar_expect(full(s), up_bytes + 2 * NQ * p.cw * 2);
@@ -343,7 +403,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 const CUtensorMap* up = half ? &p.map_up2 : &p.map_up;
                 tma_3d(at, up, full(s), col, a < 0 || half ? none : n0, max(a, 0));
                 tma_3d(at + up_bytes / 2, up, full(s), col, a < 0 || (p.dual && !half) ? none : p.dual ? n0 : n0 + 64, max(a, 0));
-                tma_2d(at + P_BYTES, &p.map_h, full(s), 0, e * 2 * NQ);  // both terms
+                tma_2d(at + P_BYTES, &p.map_h, full(s), 0, (e * LORA_TERMS + (a < 0 ? 2 : 0)) * NQ);  // two terms; the third with the next block's first
             }
         }
         if (more < 0) grid_wait();
@@ -544,11 +604,30 @@ cudaLaunchConfig_t config(dim3 grid, int threads, int smem, cudaStream_t s, cuda
 }
 
 template <int NT>
-cudaError_t launch_down(const LoraArgs& p, int64_t subs, int z, cudaStream_t s) {
-    cudaLaunchAttribute at[1];
-    const int64_t y = std::min<int64_t>(p.cap, std::max<int64_t>(1, 1024 / std::max<int64_t>(1, subs * z)));
-    const cudaLaunchConfig_t cfg = config(dim3((unsigned)subs, (unsigned)y, (unsigned)z), DOWN_THREADS, 0, s, at, true);
-    return cudaLaunchKernelEx(&cfg, lora_down_kernel<NT>, p);
+cudaError_t launch_rows(LoraArgs& p, cudaStream_t s) {
+    const int64_t subs = p.tiles * (p.tile_rows / SUB);
+    p.col_ctas = p.parts * p.cw / (8 * NT);
+    // Slices of 1024 and more values of K, what a CTA's eight warps have in flight at a time; no more than fill the SMs twice
+    // with CTAs that have work: one for each adapter with few rows, one for each 16 rows else.
+    const int64_t busy = p.col_ctas * (p.tile_rows == 256 ? subs : std::min<int64_t>(p.cap, p.T));
+    p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (p.K + 1023) / 1024, 2 * gemm_num_sms() / busy}));
+    p.slice_k = ((p.K + p.slices - 1) / p.slices + 31) / 32 * 32;
+    const int64_t each = subs * p.col_ctas * p.slices;
+    p.slots = (int)std::min<int64_t>(p.cap, std::max<int64_t>(1, 1024 / each));
+    const int64_t rows = each * p.slots, looks = ((int64_t)p.n * p.check_parts + p.slices - 1) / p.slices * p.slices;
+    if (rows + looks > 0x7fffffffll) return cudaErrorInvalidValue;
+    p.rows_ctas = (int)rows;
+    auto kern = lora_rows_kernel<NT>;
+    static SmemCarveout wide;
+    wide.ask(reinterpret_cast<const void*>(kern));
+    cudaLaunchAttribute at[2];
+    cudaLaunchConfig_t cfg = config(dim3((unsigned)(rows + looks)), DOWN_THREADS, 0, s, at, false);
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = p.slices;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.numAttrs = p.slices > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int NQ>
@@ -573,16 +652,16 @@ cudaError_t launch_few(FewLora& p, int rows, cudaStream_t s) {
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {  // of a call's scratch
-    int64_t count, list, bad, h, bytes;
+    int64_t count, list, notes, h, bytes;
 };
 
 Layout layout(const LoraArgs& p) {
     Layout l;
     l.count = 0;
     l.list = up256(4 * p.tiles);
-    l.bad = l.list + up256(4 * p.tiles * p.cap);
-    l.h = l.bad + up256((int64_t)p.n * p.check_parts);
-    l.bytes = l.h + p.tiles * p.cap * p.parts * 4ll * p.tile_rows * p.cw;
+    l.notes = l.list + up256(4 * p.tiles * p.cap);
+    l.h = l.notes + up256(16ll * p.n);
+    l.bytes = l.h + p.tiles * p.cap * p.parts * 2ll * LORA_TERMS * p.tile_rows * p.cw;
     return l;
 }
 
@@ -607,11 +686,11 @@ bool lora_plan(LoraArgs& p, bool dual) {
     p.tile_rows = p.T <= LORA_FEW_ROWS ? few_rows(p.T) : 256;
     p.tiles = ((int64_t)p.T + p.tile_rows - 1) / p.tile_rows;
     p.cap = std::min(p.n, p.tile_rows);
-    // 64 KB and more of an adapter's matrix for each CTA that looks it over
-    p.check_parts = (int)std::min<int64_t>(32, std::max<int64_t>(1, (int64_t)p.N * p.rank * 2 / 65536));
+    // CTAs that look an adapter over, 16 KB and more each
+    p.check_parts = 1;
+    while (p.check_parts < 16 && (int64_t)p.N * p.rank * 2 / p.check_parts > 24576) p.check_parts *= 2;
     // blocks are rows of one tensor map, counted in 32 bits
-    return p.tiles * p.cap * p.parts * 2 * p.tile_rows <= 0x7fffffffll && (int64_t)p.n * p.check_parts <= 0x7fffffffll &&
-           p.tiles * (p.tile_rows / SUB) <= 0x7fffffffll;
+    return p.tiles * p.cap * p.parts * LORA_TERMS * p.tile_rows <= 0x7fffffffll && (int64_t)p.n * p.check_parts <= 0x3fffffffll;
 }
 
 int64_t lora_ws_bytes(const LoraArgs& p) { return layout(p).bytes; }
@@ -622,21 +701,13 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     uint8_t* w = static_cast<uint8_t*>(ws);
     p.count = reinterpret_cast<int*>(w + l.count);
     p.list = reinterpret_cast<int*>(w + l.list);
-    p.bad = w + l.bad;
+    p.notes = w + l.notes;
     p.h = reinterpret_cast<__nv_bfloat16*>(w + l.h);
-    cudaLaunchAttribute at[1];
-    const cudaLaunchConfig_t cfg = config(dim3(p.n * p.check_parts), 256, 0, s, at, false);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, lora_check_kernel, p);
-    if (e != cudaSuccess) return e;
     const bool few = p.tile_rows != 256;
-    const int64_t subs = p.tiles * (p.tile_rows / SUB);
-    const int cols = p.parts * p.cw;
     // few rows: more CTAs of 16 columns each, and room beside the product's shared memory
-    if (p.cw == 16 || few) e = launch_down<2>(p, subs, cols / 16, s);
-    else if (p.cw == 32) e = launch_down<4>(p, subs, cols / 32, s);
-    else e = launch_down<8>(p, subs, cols / 64, s);
+    const cudaError_t e = p.cw == 16 || few ? launch_rows<2>(p, s) : p.cw == 32 ? launch_rows<4>(p, s) : launch_rows<8>(p, s);
     if (e != cudaSuccess) return e;
-    const int64_t h_rows = p.tiles * p.cap * p.parts * 2 * p.tile_rows;
+    const int64_t h_rows = p.tiles * p.cap * p.parts * LORA_TERMS * p.tile_rows;
     if (!few) return launch_gemm_bf16_lora(d, p, h_rows, s);
     FewLora f;
     memset(&f, 0, sizeof(f));
@@ -658,6 +729,7 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     f.rank = p.rank;
     f.count = p.count;
     f.list = p.list;
+    f.notes = p.notes;
     f.bias = static_cast<const __nv_bfloat16*>(d.bias);
     f.resid = d.resid;
     f.resid_f32 = d.resid_f32;
