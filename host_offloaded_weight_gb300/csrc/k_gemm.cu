@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                             if (leader) mbar_expect_tx(full_bar(s), 2 * (128 + BN / 2) * cw * 2);
                             const int64_t block = ((int64_t)m2 * p.lora_cap + j0 + i) * p.lora_parts + part;
                             tma_load_2d_2sm(sa, &p.tmH, leader_full, 0,
-                                            (int)((block * LORA_TERMS + (a < 0 ? 2 : e & 1)) * 256) + (int)rank * 128);
+                                            (int)((block * 3 + (a < 0 ? 2 : e & 1)) * 256) + (int)rank * 128);
                             // out of bounds: zeros, for an adapter that is not finite and for the other half of a gate/up tile
                             const bool none = a < 0 || (DUAL && half != (int)rank);
                             tma_load_3d_2sm(sa + S2_A, half ? &p.tmUp2 : &p.tmUp, leader_full, part % p.lora_chunks * cw,

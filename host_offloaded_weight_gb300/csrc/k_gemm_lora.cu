@@ -6,12 +6,13 @@
 // starts as soon as the first kernel's CTAs run: its loads of the shared weights need nothing of it, only these last columns do.
 // h is kept as two bf16 terms (16 bits: the first term alone would be off by 2^-9, more than the fp32 sums lose).
 //
-// 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests. Other CTAs of the
-// first kernel look over the `up` matrices of the adapters in use (bytes that the product then finds in L2). One that is not finite is
-// read out of bounds, which gives zeros, against a third term that is NaN in its own rows: they come out NaN, no others do.
+// 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests.
 //
 // Up to 128 rows (gemm_lora_few_kernel, below): the weights are the left operand (128 rows a tile) and the tokens the
-// right one, 16 to 128 columns. More rows: the pair kernel of k_gemm.cu.
+// right one, 16 to 128 columns. Each part of `up` is looked over in shared memory before its product.
+// More rows: the pair kernel of k_gemm.cu, whose operands lie in two SMs. Other CTAs of the first kernel look over the `up`
+// matrices of the adapters in use (bytes that the product then finds in L2). One that is not finite is read out of bounds, which
+// gives zeros, against a third term that is NaN in its own rows: they come out NaN, no others do.
 #include <algorithm>
 
 #include "kernels.h"
@@ -22,74 +23,122 @@ namespace {
 
 using namespace tc;
 
-constexpr int DOWN_THREADS = 256, DOWN_WARPS = 8, SUB = 16;  // rows of a CTA of the down kernel
+constexpr int ROWS_THREADS = 256, ROWS_MAX_STAGES = 16;
 constexpr int MAX_TILE = 256;
 constexpr int MAX_SLICES = 8;         // of K
+constexpr int LOOK_CTAS = 192;        // that look adapters over, at most
 
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {  // two bf16
     return (uint32_t)((w & 0x7f80u) == 0x7f80u) | (uint32_t)((w & 0x7f800000u) == 0x7f800000u);
 }
 
-// A part of an adapter's `up` matrices: its notes, 16 bytes an adapter, are nonzero where a value is not finite.
-__device__ __forceinline__ void look_over(const LoraArgs& p, int cta) {
-    const int a = cta / p.check_parts, part = cta % p.check_parts;
-    int used = 0;
-#pragma unroll 4
-    for (int t = threadIdx.x; t < p.T; t += DOWN_THREADS) used |= __ldg(p.ids + t) == a;
-    if (!__syncthreads_or(used)) return;
-    const int64_t units = (int64_t)p.N * p.rank / 8;  // of 16 bytes
-    const int64_t u0 = units * part / p.check_parts, u1 = units * (part + 1) / p.check_parts;
-    uint32_t bad = 0;
-    for (int half = 0; half < (p.up2 ? 2 : 1); ++half) {
-        const uint4* u = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(half ? p.up2 : p.up) + a * p.up_stride);
-#pragma unroll 8
-        for (int64_t i = u0 + threadIdx.x; i < u1; i += DOWN_THREADS) {
-            const uint4 v = __ldg(u + i);
-            bad |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
-        }
-    }
-    bad = __syncthreads_or((int)bad);
-    const int bytes = 16 / p.check_parts;
-    if (threadIdx.x < bytes) p.notes[16ll * a + part * bytes + threadIdx.x] = bad ? 1 : 0;
+// 16 bytes, or zeros. Volatile, so that the loads of a step are all issued before its first product: left to the compiler they
+// waited for one another.
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16* at, bool on) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(at), "r"((int)on));
+    return v;
 }
+
+// The notes on the adapters in use, 16 bytes each: nonzero where a value of its `up` matrices is not finite. Which are in use is
+// known by the low bits of their numbers (others that share them are looked over too).
+__device__ __forceinline__ void look_over(const LoraArgs& p, int cta, int ctas) {
+    constexpr int BITS = 4096;
+    __shared__ uint32_t s_used[BITS / 32];
+    if (threadIdx.x < BITS / 32) s_used[threadIdx.x] = 0;
+    __syncthreads();
+    for (int64_t t0 = threadIdx.x; t0 < p.T; t0 += 8 * ROWS_THREADS) {
+        uint32_t a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = (uint32_t)__ldg(p.ids + min(t0 + i * ROWS_THREADS, (int64_t)p.T - 1)) % BITS;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i == 0 || a[i] != a[i - 1]) atomicOr(&s_used[a[i] / 32], 1u << (a[i] % 32));
+    }
+    __syncthreads();
+    const int64_t units = (int64_t)p.N * p.rank / 8;  // of 16 bytes
+    const int bytes = 16 / p.check_parts;
+    for (int64_t i = cta; i < (int64_t)p.n * p.check_parts; i += ctas) {
+        const int a = (int)(i / p.check_parts), part = (int)(i % p.check_parts);
+        if (!(s_used[a % BITS / 32] >> (a % 32) & 1)) continue;
+        const int64_t u0 = units * part / p.check_parts, u1 = units * (part + 1) / p.check_parts;
+        uint32_t bad = 0;
+        for (int half = 0; half < (p.up2 ? 2 : 1); ++half) {
+            const uint4* u = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(half ? p.up2 : p.up) + a * p.up_stride);
+            for (int64_t k0 = u0 + threadIdx.x; k0 < u1; k0 += 8 * ROWS_THREADS) {
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = load16(reinterpret_cast<const __nv_bfloat16*>(u + k0 + i * ROWS_THREADS), k0 + i * ROWS_THREADS < u1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bad |= not_finite(v[i].x) | not_finite(v[i].y) | not_finite(v[i].z) | not_finite(v[i].w);
+            }
+        }
+        bad = __syncthreads_or((int)bad);
+        if (threadIdx.x < bytes) p.notes[16ll * a + part * bytes + threadIdx.x] = bad ? 1 : 0;
+    }
+}
+
+__device__ __forceinline__ uint64_t narrow_desc(uint32_t addr, int cw);
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate);
 
 // ------------------------------------------------------------------ h
-// A CTA has 16 of the rows that an adapter has in a tile, 8 NT columns of h and a slice of K (a cluster has all of it), for one
-// adapter of the tile after the other: m16n8k16 products (bound by the loads: the shared product's tensor core form would want 128 rows and a TMA ring for 16
-// columns), K dealt to eight warps. The sums of the warps and of the cluster's CTAs are added in their order. A lane's 16 bytes of
-// a row of x and of `down` are the same eight values of K, so which of them a product calls its first does not matter: a warp's
-// load takes 64 bytes of each of eight rows.
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// A cluster of CTAs, a slice of K each, has a run of a tile's rows (all of a few-row tile, half of a full one) and up to 128 columns
+// of h, for one adapter of the tile after the other: `down` is the left operand of the products (its rows, 128 with what lies
+// behind them, whose results nobody reads), the rows of x, all of them, the right one. The CTAs' sums are added through their shared
+// memory, each CTA finishing its share of the groups of eight rows, in the order of the CTAs. Bound by the latencies of its steps:
+// ids, first loads, sums.
+// (Register products, m16n8k16, from plain loads of a row's 64 bytes by four lanes took 55 to 110 us for 2048 rows of 5120.)
+constexpr int ROWS_PROD = 0, ROWS_MMA = 1, ROWS_EPI = 2;   // warps; four of the epilogue
 
-template <int NT>
-__global__ void __launch_bounds__(DOWN_THREADS) lora_rows_kernel(const __grid_constant__ LoraArgs p) {
-    constexpr int COLS = 8 * NT, UNITS = SUB * COLS / 2;  // units: two columns of a row
+__global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_constant__ LoraArgs p) {
+    extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) int s_ids[MAX_TILE];
     __shared__ int s_list[MAX_TILE];
-    __shared__ int s_warp[2][DOWN_WARPS];
-    __shared__ int s_rows[SUB];
-    __shared__ float s_sum[DOWN_WARPS][SUB][COLS + 1];
-    __shared__ float2 s_red[2][UNITS + MAX_SLICES];
-    grid_release();
+    __shared__ int s_warp[ROWS_THREADS / 32];
+    __shared__ uint32_t s_tmem;
+    __shared__ __align__(8) uint64_t s_bars[2 * ROWS_MAX_STAGES + 1];
+    __shared__ volatile int stop;
+    if (p.tile_rows != 256) grid_release();
     if ((int)blockIdx.x >= p.rows_ctas) {
-        look_over(p, (int)blockIdx.x - p.rows_ctas);
+        look_over(p, (int)blockIdx.x - p.rows_ctas, (int)gridDim.x - p.rows_ctas);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // slices (a cluster) innermost, then columns, slots, 16 rows
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
+    const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+    const int S = p.stages, down_bytes = p.block_cols * 128, stage = down_bytes + p.run * 128;
+    float* red = reinterpret_cast<float*>(smem_raw + (base - raw) + S * stage);
+    const uint32_t bars = smem_addr(s_bars);
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (ROWS_MAX_STAGES + s); };
+    const uint32_t acc_full = bars + 8u * 2 * ROWS_MAX_STAGES;
+    // slices (a cluster) innermost, then runs of columns, slots, runs of rows
     int at = (int)blockIdx.x;
     const int slice = at % p.slices;
     at /= p.slices;
-    const int col0 = at % p.col_ctas * COLS;
-    at /= p.col_ctas;
+    const int col0 = at % p.col_runs * 128;   // of an adapter's columns: parts of width cw side by side
+    at /= p.col_runs;
     const int slot = at % p.slots;
     at /= p.slots;
-    const int subs = p.tile_rows / SUB, tile = at / subs, row0 = at % subs * SUB, t0 = tile * p.tile_rows;
+    const int runs = p.tile_rows / p.run, tile = at / runs, row0 = at % runs * p.run, t0 = tile * p.tile_rows;
 
+    if (tid == 0) {
+        stop = 0;
+        for (int s = 0; s < S; ++s) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        bar_init(acc_full, 1);
+        bar_init_fence();
+        tma_desc_prefetch(&p.map_x);
+        tma_desc_prefetch(&p.map_down);
+    }
+    if (warp == ROWS_MMA) tmem_get(smem_addr(&s_tmem), p.tmem_cols);
     // the tile's adapters, in the order of their first rows
     int id = -1;
     if (tid < p.tile_rows && t0 + tid < p.T) {
@@ -98,146 +147,191 @@ __global__ void __launch_bounds__(DOWN_THREADS) lora_rows_kernel(const __grid_co
     }
     s_ids[tid] = id;
     __syncthreads();
-    bool first = id >= 0;
-    for (int u = 0; first && u < tid; u += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(s_ids + u);
-        if ((v.x == id) || (u + 1 < tid && v.y == id) || (u + 2 < tid && v.z == id) || (u + 3 < tid && v.w == id)) first = false;
+    // not the first of its adapter: one of the rows before it is the same (rows of a request lie together: mostly the last one)
+    bool first = id >= 0 && !(tid > 0 && s_ids[tid - 1] == id);
+    if (first) {
+        uint32_t seen = 0;
+#pragma unroll 8
+        for (int u = 0; u < tid; u += 4) {
+            const int4 v = *reinterpret_cast<const int4*>(s_ids + u);
+            seen |= (uint32_t)(v.x == id) | (uint32_t)(u + 1 < tid && v.y == id) | (uint32_t)(u + 2 < tid && v.z == id) | (uint32_t)(u + 3 < tid && v.w == id);
+        }
+        first = !seen;
     }
+    __syncwarp();
     const uint32_t vote = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) s_warp[1][warp] = __popc(vote);
+    if (lane == 0) s_warp[warp] = __popc(vote);
     __syncthreads();
     int before = 0, count = 0;
-    for (int w = 0; w < DOWN_WARPS; ++w) {
-        if (w < warp) before += s_warp[1][w];
-        count += s_warp[1][w];
+    for (int w = 0; w < ROWS_THREADS / 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        count += s_warp[w];
     }
     if (first) s_list[before + __popc(vote & ((1u << lane) - 1u))] = id;
+    fence_before_sync();
     __syncthreads();
-    const bool writes_list = row0 == 0 && col0 == 0 && slot == 0 && slice == 0;
-    if (writes_list) {
+    fence_after_sync();
+    if (row0 == 0 && col0 == 0 && slot == 0 && slice == 0) {
         if (tid < count) p.list[(int64_t)tile * p.cap + tid] = s_list[tid];
         if (tid == 0) p.count[tile] = count;
     }
-    if (p.slices > 1) cluster_barrier();  // the others' shared memory is there
-
-    const int g = lane >> 2, q = lane & 3;
-    const int part = col0 / p.cw, half = part / p.chunks, c0 = col0 % p.cw, r0 = part % p.chunks * p.cw + c0;  // parts of width cw, side by side
-    const int k_first = slice * p.slice_k, k_end = min(p.K, k_first + p.slice_k);
-    auto owner_first = [&](int o) { return (UNITS * o + p.slices - 1) / p.slices; };  // a CTA of the cluster finishes these units and up
-    const int own0 = owner_first(slice), own1 = owner_first(slice + 1);
-    int turn = 0;
-    for (int j = slot; j < count; j += p.slots, ++turn) {
+    const uint32_t tmem = s_tmem;
+    const int k0 = (int)((int64_t)slice * p.k_stages / p.slices), k1 = (int)((int64_t)(slice + 1) * p.k_stages / p.slices);
+    // (divisions by numbers that only the launch knows take 150 clocks each: counters and shifts below)
+    const int log_cw = p.cw == 16 ? 4 : p.cw == 32 ? 5 : 6;
+    const int cols = min(128, p.parts * p.cw - col0), part0 = col0 >> log_cw, parts = cols >> log_cw;
+    const int groups = p.run / 8, own_groups = (groups + p.slices - 1) / p.slices;
+    const int q = warp & 3, col = 32 * q + lane;   // the epilogue: q the TMEM lane quarter that a warp can read, col the lane's column
+    const int part = part0 + (col >> log_cw);
+    const int rows = min(p.run, p.T - t0 - row0);  // rows that exist (zero and less: none)
+    int it = 0, turn = 0;                          // stages and adapters so far
+    int ring = 0;                                  // the place of the next stage, and the parity of its use
+    uint32_t parity = 0;
+    if (p.slices > 1) cluster_barrier_smem();           // the others' shared memory is there
+    for (int j = slot; j < count; j += p.slots) {
         const int a = s_list[j];
-        // the adapter's rows row0, row0 + 1, ... of the tile, of however many it has
-        const uint32_t mine = __ballot_sync(0xffffffffu, s_ids[tid] == a);
-        if (lane == 0) s_warp[turn & 1][warp] = __popc(mine);
-        __syncthreads();
-        int rank = __popc(mine & ((1u << lane) - 1u)) - row0, rows = -row0;
-        for (int w = 0; w < DOWN_WARPS; ++w) {
-            if (w < warp) rank += s_warp[turn & 1][w];
-            rows += s_warp[turn & 1][w];
-        }
-        if (s_ids[tid] == a && rank >= 0 && rank < SUB) s_rows[rank] = tid;
-        __syncthreads();
-        const bool any = rows > 0;   // the same in the cluster
+        bool mine = false;
+        for (int r = tid; r < rows; r += ROWS_THREADS) mine = mine || s_ids[row0 + r] == a;
+        const bool any = __syncthreads_or(mine);   // the same in the cluster
         if (any) {
-            const bool on0 = g < rows, on1 = g + 8 < rows;
-            float acc[NT][4] = {};
-            const __nv_bfloat16* x0 = p.x + (int64_t)(t0 + (on0 ? s_rows[g] : 0)) * p.K;
-            const __nv_bfloat16* x1 = p.x + (int64_t)(t0 + (on1 ? s_rows[g + 8] : 0)) * p.K;
-            const uint8_t* down = static_cast<const uint8_t*>(p.down) + a * p.down_stride;
-            const __nv_bfloat16* d[NT];
-            bool in[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int r = r0 + 8 * n + g;
-                in[n] = r < p.rank;
-                d[n] = reinterpret_cast<const __nv_bfloat16*>(down) + ((int64_t)half * p.rank + (in[n] ? r : 0)) * p.K;
-            }
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            constexpr int U = NT <= 2 ? 4 : 2;
-            for (int k0 = k_first + 32 * warp; k0 < k_end; k0 += 32 * DOWN_WARPS * U) {
-                uint4 va[U], vb[U], vd[U][NT];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int k = k0 + 32 * DOWN_WARPS * u + 8 * q;
-                    const bool k_in = k < k_end;  // K and the slices are multiples of 8
-                    va[u] = on0 && k_in ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : zero;
-                    vb[u] = on1 && k_in ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : zero;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) vd[u][n] = in[n] && k_in ? __ldg(reinterpret_cast<const uint4*>(d[n] + k)) : zero;
+            auto step = [&]() {
+                if (++ring == S) {
+                    ring = 0;
+                    parity ^= 1u;
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma16816(acc[n], va[u].x, vb[u].x, va[u].y, vb[u].y, vd[u][n].x, vd[u][n].y);
-                        mma16816(acc[n], va[u].z, vb[u].z, va[u].w, vb[u].w, vd[u][n].z, vd[u][n].w);
+            };
+            if (warp == ROWS_PROD) {
+                const bool one = elect_one();
+                for (int k = k0; k < k1; ++k, step()) {
+                    const int s = ring;
+                    if (!bar_wait_warp(empty(s), parity ^ 1u, p.err, 1)) {
+                        stop = 1;
+                        break;
                     }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                s_sum[warp][g][8 * n + 2 * q] = acc[n][0];
-                s_sum[warp][g][8 * n + 2 * q + 1] = acc[n][1];
-                s_sum[warp][g + 8][8 * n + 2 * q] = acc[n][2];
-                s_sum[warp][g + 8][8 * n + 2 * q + 1] = acc[n][3];
-            }
-            __syncthreads();
-            float2* red = s_red[turn & 1];
-            for (int i = tid; i < UNITS; i += DOWN_THREADS) {
-                const int r = i / (COLS / 2), c = i % (COLS / 2) * 2;
-                float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < DOWN_WARPS; ++w) {
-                    v.x += s_sum[w][r][c];
-                    v.y += s_sum[w][r][c + 1];
+                    if (one) {
+                        const uint32_t to = base + s * stage;
+                        bar_expect(full(s), cols * 128 + p.run * 128);
+                        for (int i = 0; i < parts; ++i) {
+                            const int half = part0 + i >= p.chunks;
+                            tma_4d(to + i * p.cw * 128, &p.map_down, full(s), k * 64, (part0 + i - half * p.chunks) * p.cw, half, a);
+                        }
+                        tma_2d(to + down_bytes, &p.map_x, full(s), k * 64, t0 + row0);
+                    }
+                    __syncwarp();
                 }
-                if (p.slices == 1) {
-                    red[i] = v;
-                } else {
-                    const int o = i * p.slices / UNITS, o0 = owner_first(o), share = owner_first(o + 1) - o0;
-                    const uint32_t to = cluster_addr(smem_addr(red + slice * share + i - o0), o);
-                    st_cluster(to, v.x);
-                    st_cluster(to + 4, v.y);
+            } else if (warp == ROWS_MMA) {
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.run >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+                const bool one = elect_one();
+                for (int k = k0; k < k1; ++k, step()) {
+                    const int s = ring;
+                    if (!bar_wait_warp(full(s), parity, p.err, 3)) {
+                        stop = 1;
+                        break;
+                    }
+                    fence_after_sync();
+                    if (one) {
+                        const uint32_t sp = base + s * stage;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16(tmem, operand_desc(sp + 32 * i), operand_desc(sp + down_bytes + 32 * i), idesc, k > k0 || i ? 1u : 0u);
+                        mma_commit(empty(s));
+                    }
+                    __syncwarp();
+                }
+                if (one) mma_commit(acc_full);
+                __syncwarp();
+            }
+            it += k1 - k0;
+        }
+        const bool reads = warp >= ROWS_EPI && warp < ROWS_EPI + 4 && 32 * q < cols;
+        const uint32_t mine_at = tmem + ((uint32_t)(q * 32) << 16);
+        const float scale = any && p.scale ? __ldg(p.scale + a) : 1.f;
+        const int64_t block = ((int64_t)tile * p.cap + j) * p.parts + part, term = (int64_t)p.tile_rows * p.cw;
+        __nv_bfloat16* const h = p.h + (block * p.terms * p.tile_rows + row0) * p.cw + (col & (p.cw - 1));
+        auto sums = [&](int g, float (&v)[8]) {
+            uint32_t x[8];
+            tmem_load8(mine_at + 8 * g, x);
+            tmem_load_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[i]);
+        };
+        // Two rounds over this CTA's groups of rows: zeros in the rows of others, while the loads are on their way, then h in the
+        // adapter's own.
+        for (int round = 0; round < 2; ++round) {
+            if (round == 1) {
+                if (!any) break;
+                const bool done = bar_wait_warp(acc_full, (uint32_t)turn & 1u, p.err, 4);   // every warp: nobody is ahead by an adapter
+                if (!done) stop = 1;
+                if (j + p.slots >= count) grid_release();
+                fence_after_sync();
+                ++turn;
+                if (p.slices > 1) {
+                    if (reads)
+                        for (int g = 0, owner = 0, l = 0; g < groups && 8 * g < rows; ++g) {  // l: the owner's groups before this one
+                            if (owner != slice) {
+                                float v[8];
+                                sums(g, v);
+                                const int at = ((slice - (slice > owner)) * own_groups + l) * 8 * p.block_cols + col;
+                                const uint32_t to = cluster_addr(smem_addr(red + at), owner);
+                                if (col < cols)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) st_cluster(to + i * p.block_cols * 4, v[i]);
+                            }
+                            if (++owner == p.slices) {
+                                owner = 0;
+                                ++l;
+                            }
+                        }
+                    __syncwarp();
+                    cluster_barrier_smem();
                 }
             }
-            if (p.slices > 1) cluster_barrier();
-            else __syncthreads();
-        }
-        const float scale = p.scale ? p.scale[a] : 1.f;
-        const float2* red = s_red[turn & 1];
-        const int64_t block = (((int64_t)tile * p.cap + j) * p.parts + part) * LORA_TERMS;
-        const int64_t term = (int64_t)p.tile_rows * p.cw / 2;
-        for (int i = own0 + tid; i < own1; i += DOWN_THREADS) {
-            const int r = i / (COLS / 2), c = i % (COLS / 2) * 2;
-            uint32_t* to = reinterpret_cast<uint32_t*>(p.h + block * p.tile_rows * p.cw + c0 + c);
-            // rows row0 and up of the tile that are not the adapter's are zero
-            if (s_ids[row0 + r] != a) {
-                uint32_t* z = to + (int64_t)(row0 + r) * p.cw / 2;
-                z[0] = z[term] = z[2 * term] = 0;
-            }
-            if (r >= rows) continue;
-            float2 v = make_float2(0.f, 0.f);
-            for (int o = 0; o < p.slices; ++o) {
-                const float2 x = red[o * (own1 - own0) + i - own0];
-                v.x += x.x;
-                v.y += x.y;
-            }
-            uint32_t hi = 0, lo = 0;
+            if (!reads) continue;
+#pragma unroll 1
+            for (int g = slice, l = 0; g < groups; g += p.slices, ++l) {
+                float v[8] = {};
+                if (round == 1 && 8 * g < rows) {
+                    sums(g, v);
+                    for (int o = 0; o < p.slices - 1; ++o) {
+                        const float* from = red + (o * own_groups + l) * 8 * p.block_cols + (col < cols ? col : 0);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float h = r0 + c + e < p.rank ? (e ? v.y : v.x) * scale : 0.f;
-                float t1 = __bfloat162float(__float2bfloat16_rn(h));
-                if (isinf(t1) && !isinf(h)) t1 = __bfloat162float(__float2bfloat16_rz(h));
-                const float t2 = isfinite(t1) ? h - t1 : 0.f;
-                hi |= (__float_as_uint(t1) >> 16) << (16 * e);
-                lo |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(t2)) << (16 * e);
+                        for (int i = 0; i < 8; ++i) v[i] += from[i * p.block_cols];
+                    }
+                }
+                // the rows of this round
+                uint32_t which = __ballot_sync(0xffffffffu, lane < 8 && s_ids[row0 + 8 * g + (lane & 7)] == a);
+                if (round == 0) which ^= 0xffu;
+                if (col >= cols) continue;
+                __nv_bfloat16* to = h + 8 * g * p.cw;
+#pragma unroll
+                for (int i = 0; i < 8; ++i, to += p.cw) {
+                    const float w = round ? v[i] * scale : 0.f;
+                    float t1 = __bfloat162float(__float2bfloat16_rn(w));
+                    if (isinf(t1) && !isinf(w)) t1 = __bfloat162float(__float2bfloat16_rz(w));
+                    const __nv_bfloat16 t2 = __float2bfloat16_rn(isfinite(t1) ? w - t1 : 0.f);
+                    if (which >> i & 1) {
+                        to[0] = __float2bfloat16_rn(t1);
+                        to[term] = t2;
+                        if (p.terms == 3) to[2 * term] = __ushort_as_bfloat16(round ? 0x7fc0 : 0);
+                    }
+                }
             }
-            to += (int64_t)s_rows[r] * p.cw / 2;
-            to[0] = hi;
-            to[term] = lo;
-            to[2 * term] = 0x7fc07fc0u;  // NaN
         }
+        fence_before_sync();
+        __syncwarp();
+        if (j + p.slots >= count) break;
+        // the next adapter's sums go where these were read
+        if (p.slices > 1 && any) cluster_barrier_smem();
+        else __syncthreads();
+        fence_after_sync();
+    }
+    if (stop && warp == ROWS_PROD)  // an aborted CTA waits for its own copies before it exits
+        for (int i = 0; i < S && i < it; ++i) bar_wait(full(i), (uint32_t)((it - 1 - (it - 1 - i) % S) / S) & 1u, p.err, 5);
+    fence_before_sync();
+    __syncthreads();
+    if (warp == ROWS_MMA) {
+        fence_after_sync();
+        tmem_free(tmem, p.tmem_cols);
     }
 }
 
@@ -251,17 +345,25 @@ constexpr int TILE_P = 128, P_BYTES = TILE_P * 128, FEW_EPI = 4, FEW_THREADS = 3
 
 template <int NQ>
 struct Few {
-    static constexpr int Q_BYTES = 2 * NQ * 128;                  // an adapter stage's two terms
+    static constexpr int PACK = NQ <= 32 ? 2 : 1;                 // an adapter stage's blocks: PACK 64 / cw term rows of x's size
+    static constexpr int Q_BYTES = PACK * NQ * 128;
     static constexpr int STAGE = P_BYTES + Q_BYTES;
-    static constexpr int MAX_SPLIT = NQ <= 16 ? 8 : NQ <= 64 ? 4 : 2;
-    static constexpr int RED_BYTES = (MAX_SPLIT - 1) * NQ * TILE_P * 4;
+    static constexpr int MAX_SPLIT = NQ <= 16 ? 8 : 4;
+    // the others' sums of the groups of eight tokens that this CTA of n finishes
+    static constexpr int red(int n) { return (n - 1) * ((NQ / 8 + n - 1) / n) * 8 * TILE_P * 4; }
+    static constexpr int most_red() {
+        int most = 0;
+        for (int n = 2; n <= MAX_SPLIT; ++n) most = red(n) > most ? red(n) : most;
+        return most;
+    }
+    static constexpr int RED_BYTES = most_red();
     static constexpr int X_BYTES = 2 * 8 * 64 * 4;                // SwiGLU: the up rows' sums on their way to the gate rows' warps
-    // the kernels before it need room on the same SM
+    // the kernel before it needs room on the same SM
     static constexpr int FIT = (200 * 1024 - RED_BYTES - X_BYTES - 1024 - 512) / STAGE;
     static constexpr int STAGES = FIT < 9 ? FIT : 9;
     static constexpr int SMEM = STAGES * STAGE + RED_BYTES + X_BYTES + 1024 + 512;
     static constexpr int COLS = 2 * NQ < 32 ? 32 : 2 * NQ;        // of tensor memory: two accumulators
-    static_assert(STAGES >= 2 && SMEM <= 232448, "shared memory");
+    static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory");
 };
 
 struct FewLora {
@@ -269,10 +371,11 @@ struct FewLora {
     int M, N, K;
     int k_stages, tiles, splits;
     int dual, b2_row_off, epi;
-    int cw, chunks, parts, rank;   // columns of a part of h; parts of a rank, of a block
+    int cw, chunks, parts, rank;   // columns of a part of h; parts of a rank, of an adapter
+    int pack, halves;              // blocks of a stage; 2: a stage has one term of one block
     const int* count;
     const int* list;
-    const uint8_t* notes;
+    const int* ids;
     const __nv_bfloat16* bias;
     const void* resid;
     int resid_f32;
@@ -295,6 +398,28 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// A CTA's adapter stages: every so many stages of the tile's; first: the stage's first block, part `part` of adapter j of the
+// tile. p.pack blocks and both their terms, or (halves = 2) one term of one block.
+struct Blocks {
+    const FewLora& p;
+    int all, first, term, j, part;
+    __device__ __forceinline__ Blocks(const FewLora& q, int slice, int count) : p(q), all(count), first(0), term(0), j(0), part(0) { step(slice); }
+    __device__ __forceinline__ void step(int stages) {
+        if (p.halves == 2) {
+            term += stages;
+            stages = term >> 1;
+            term &= 1;
+        } else {
+            stages *= p.pack;
+        }
+        first += stages;
+        for (part += stages; part >= p.parts; part -= p.parts) ++j;
+    }
+    __device__ __forceinline__ void next() { step(p.splits); }
+    __device__ __forceinline__ bool left() const { return first < all; }
+    __device__ __forceinline__ int blocks() const { return min(p.pack, all - first); }
+};
+
 // GELU(v) = v Phi(v), SiLU(v) = v / (1 + e^-v)
 __device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.f + erff(v * 0.70710678118654752f)); }
 __device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
@@ -313,9 +438,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
     auto acc_full = [&](int b) { return bars + 8u * (2 * S + b); };
     auto acc_empty = [&](int b) { return bars + 8u * (2 * S + 2 + b); };
     const uint32_t done = bars + 8u * (2 * S + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (2 * S + 5));
+    auto checked = [&](int s) { return bars + 8u * (2 * S + 5 + s); };  // an adapter stage's values are finite
+    const uint32_t based = bars + 8u * (3 * S + 5);                     // a tile's stages of the shared weights have all arrived
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (3 * S + 6));
     __shared__ volatile int stop;
-    __shared__ int s_list[LORA_FEW_ROWS];  // adapters; those that are not finite as -1 - a
+    __shared__ int s_list[LORA_FEW_ROWS];  // the loading warp's copy of the adapters
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -323,12 +450,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
         for (int s = 0; s < S; ++s) {
             bar_init(full(s), 1);
             bar_init(empty(s), 1);
+            bar_init(checked(s), FEW_EPI);
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(acc_full(b), 1);
             bar_init(acc_empty(b), FEW_EPI);
         }
         bar_init(done, 1);
+        bar_init(based, 1);
         bar_init_fence();
         tma_desc_prefetch(&p.map_w);
         tma_desc_prefetch(&p.map_x);
@@ -375,35 +504,40 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 if (!one) continue;
                 const uint32_t at = base + s * F::STAGE;
                 bar_expect(full(s), P_BYTES + NQ * 128);
-                tma_2d(at, &p.map_w, full(s), k * 64, n0);  // boxes of 64 rows
-                tma_2d(at + P_BYTES / 2, &p.map_w, full(s), k * 64, p.dual ? p.b2_row_off + n0 : n0 + 64);
+                tma_2d(at, &p.map_w, full(s), k * 64, n0);  // a box of 128 rows, or two of 64
+                if (p.dual) tma_2d(at + P_BYTES / 2, &p.map_w, full(s), k * 64, p.b2_row_off + n0);
                 tma_2d(at + P_BYTES, &p.map_x, full(s), k * 64, 0);
             }
             if (!ok) break;
             if (more < 0) {
                 grid_wait();
                 const int count = *p.count;
-                for (int j = lane; j < count; j += 32) {
-                    const int a = p.list[j];
-                    const uint4 n = *reinterpret_cast<const uint4*>(p.notes + 16ll * a);
-                    s_list[j] = n.x | n.y | n.z | n.w ? -1 - a : a;
-                }
+                for (int j = lane; j < count; j += 32) s_list[j] = p.list[j];
                 __syncwarp();
                 more = count * p.parts;
             }
-            const int up_bytes = TILE_P * p.cw * 2;
-            for (int e = slice; e < more && turn(); e += p.splits, next()) {
-                const int j = e / p.parts, part = e % p.parts, half = part / p.chunks, col = part % p.chunks * p.cw;
-                const int a = s_list[j];
+            const int up_bytes = TILE_P * p.cw * 2, h_bytes = NQ * p.cw * 2;
+            Blocks at_block(p, slice, more);
+            for (; at_block.left() && turn(); at_block.next(), next()) {
                 if (!one) continue;
                 const uint32_t at = base + s * F::STAGE;
-                bar_expect(full(s), up_bytes + 2 * NQ * p.cw * 2);
-                // out of bounds: zeros, for an adapter that is not finite and for the other half of a SwiGLU tile
-                const int none = p.N;
-                const CUtensorMap* up = half ? &p.map_up2 : &p.map_up;
-                tma_3d(at, up, full(s), col, a < 0 || half ? none : n0, max(a, 0));
-                tma_3d(at + up_bytes / 2, up, full(s), col, a < 0 || (p.dual && !half) ? none : p.dual ? n0 : n0 + 64, max(a, 0));
-                tma_2d(at + P_BYTES, &p.map_h, full(s), 0, (e * LORA_TERMS + (a < 0 ? 2 : 0)) * NQ);  // two terms; the third with the next block's first
+                const int blocks = at_block.blocks(), terms = 3 - p.halves;
+                bar_expect(full(s), blocks * (up_bytes + terms * h_bytes));
+                int j = at_block.j, part = at_block.part;
+                for (int i = 0; i < blocks; ++i) {
+                    const int half = part >= p.chunks, col = (part - (half ? p.chunks : 0)) * p.cw, a = s_list[j];
+                    // out of bounds: zeros, for the other half of a SwiGLU tile
+                    const CUtensorMap* up = half ? &p.map_up2 : &p.map_up;
+                    const uint32_t to = at + i * up_bytes;
+                    tma_3d(to, up, full(s), col, half ? p.N : n0, a);
+                    if (p.dual) tma_3d(to + up_bytes / 2, up, full(s), col, half ? n0 : p.N, a);
+                    // both terms side by side, or the one
+                    tma_2d(at + P_BYTES + i * terms * h_bytes, &p.map_h, full(s), 0, ((at_block.first + i) * 2 + at_block.term) * NQ);
+                    if (++part == p.parts) {
+                        part = 0;
+                        ++j;
+                    }
+                }
             }
         }
         if (more < 0) grid_wait();
@@ -419,6 +553,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
         constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NQ >> 3) << 17) | ((uint32_t)(TILE_P >> 4) << 24);
         const bool one = elect_one();
         int n = 0, it = 0, more = -1;
+        uint32_t uses = 0;
         bool ok = true;
         for (int tile = tile0; ok && tile < p.tiles; tile += step, ++n) {
             const int b = n & 1;
@@ -447,18 +582,35 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 __syncwarp();
                 add = 1;
             }
+            if (one && ok) bar_arrive(based);
             if (ok && more < 0) {
                 grid_wait();
                 more = *p.count * p.parts;
             }
-            for (int e = slice; ok && e < more && ready(); e += p.splits, ++it) {
-                const uint32_t sp = base + it % S * F::STAGE, sq = sp + P_BYTES;
-                const int left = min(p.cw, p.rank - e % p.parts % p.chunks * p.cw), steps = (left + 15) / 16;
+            const int up_bytes = TILE_P * p.cw * 2, h_bytes = NQ * p.cw * 2;
+            Blocks at_block(p, slice, more);
+            for (; ok && at_block.left(); at_block.next(), ++it) {
+                const int s = it % S;
+                if (!bar_wait_warp(checked(s), uses >> s & 1u, p.err, 9)) {  // the stage's uses for adapters have a count of their own
+                    ok = false;
+                    stop = 1;
+                    break;
+                }
+                uses ^= 1u << s;
+                fence_after_sync();
+                const uint32_t sp = base + s * F::STAGE, sq = sp + P_BYTES;
+                const int blocks = at_block.blocks(), terms = 3 - p.halves;
                 if (one) {
-                    for (int i = 0; i < steps; ++i) {
-                        const uint64_t a = narrow_desc(sp + 32 * i, p.cw);
-                        mma_bf16(d, a, narrow_desc(sq + 32 * i, p.cw), IDESC, i ? 1u : add);
-                        mma_bf16(d, a, narrow_desc(sq + NQ * p.cw * 2 + 32 * i, p.cw), IDESC, 1u);
+                    int part = at_block.part;
+                    for (int i = 0; i < blocks; ++i) {
+                        const int chunk = part >= p.chunks ? part - p.chunks : part, steps = (min(p.cw, p.rank - chunk * p.cw) + 15) / 16;
+                        for (int k = 0; k < steps; ++k)
+                            for (int t = 0; t < terms; ++t) {
+                                mma_bf16(d, narrow_desc(sp + i * up_bytes + 32 * k, p.cw), narrow_desc(sq + (i * terms + t) * h_bytes + 32 * k, p.cw),
+                                         IDESC, add);
+                                add = 1;
+                            }
+                        if (++part == p.parts) part = 0;
                     }
                     mma_commit(empty(it % S));
                 }
@@ -474,7 +626,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
     } else {
         // ------------------------------------------------------------ results
         const int q = warp & 3, row = 32 * q + lane;  // q: the TMEM lane quarter that this warp can read
-        const int groups = (p.M + 7) / 8;
+        const int groups = (p.M + 7) / 8, own_groups = (NQ / 8 + p.splits - 1) / p.splits;
         float* red = reinterpret_cast<float*>(gbase + S * F::STAGE);
         float* swap = reinterpret_cast<float*>(gbase + S * F::STAGE + F::RED_BYTES);
         // An aborted warp goes through the same steps, without waits and results: the others meet it at the barrier below.
@@ -496,19 +648,25 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
             }
             if (col >= p.N || dead) return;
             const bool has_bias = p.epi == EPI_BIAS_GELU || p.epi == EPI_BIAS_RESID;
+            const bool has_resid = p.epi == EPI_BIAS_RESID || p.epi == EPI_RESID;
             const float bias = has_bias ? __bfloat162float(p.bias[col]) : 0.f;
+            const int64_t at = (int64_t)8 * g * p.N + col;
+            float r[8] = {};
+            if (has_resid) {  // all loads before the first store: the residual may be what C32 or C overwrites
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (8 * g + j < p.M)
+                        r[j] = p.resid_f32 ? static_cast<const float*>(p.resid)[at + (int64_t)j * p.N]
+                                           : __bfloat162float(static_cast<const __nv_bfloat16*>(p.resid)[at + (int64_t)j * p.N]);
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int t = 8 * g + j;
-                if (t >= p.M) continue;
-                const int64_t at = (int64_t)t * p.N + col;
-                float r = v[j] + bias;
-                if (p.epi == EPI_BIAS_GELU) r = gelu(r);
-                if (p.epi == EPI_BIAS_RESID || p.epi == EPI_RESID) {
-                    r += p.resid_f32 ? static_cast<const float*>(p.resid)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.resid)[at]);
-                    if (p.C32) p.C32[at] = r;
-                }
-                p.C[at] = __float2bfloat16_rn(r);
+                if (8 * g + j >= p.M) continue;
+                float y = v[j] + bias;
+                if (p.epi == EPI_BIAS_GELU) y = gelu(y);
+                y += r[j];
+                if (has_resid && p.C32) p.C32[at + (int64_t)j * p.N] = y;
+                p.C[at + (int64_t)j * p.N] = __float2bfloat16_rn(y);
             }
         };
         auto sums = [&](int b, int g, float (&v)[8]) {
@@ -518,24 +676,78 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(x[j]);
         };
-        int n = 0;
+        int n = 0, it = 0, more = -1;
         for (int tile = tile0; tile < p.tiles; tile += step, ++n) {
             const int b = n & 1;
+            // Adapter stages first pass by these warps, a quarter each. 0 times infinity is NaN: a value that is not finite would
+            // reach rows of other adapters. It becomes zero, and the adapter's own rows of h NaN.
+            // (A wait by parity cannot tell a use of a stage from the one two before it: these warps have not seen the uses for the
+            // shared weights, so they first hear that all of those are over.)
+            it += k1 - k0;
+            if (!dead && !bar_wait_warp(based, (uint32_t)n & 1u, p.err, 10)) {
+                stop = 1;
+                dead = true;
+            }
+            if (more < 0) {
+                grid_wait();
+                more = *p.count * p.parts;
+            }
+            const int up_bytes = TILE_P * p.cw * 2, h_bytes = NQ * p.cw * 2, terms = 3 - p.halves;
+            Blocks at_block(p, slice, more);
+            for (; at_block.left(); at_block.next(), ++it) {
+                const int s = it % S;
+                if (dead || !bar_wait_warp(full(s), (uint32_t)(it / S) & 1u, p.err, 8)) {
+                    stop = 1;
+                    dead = true;
+                    continue;
+                }
+                int j = at_block.j, part = at_block.part;
+                for (int i = 0; i < at_block.blocks(); ++i) {
+                    uint8_t* v = gbase + s * F::STAGE + i * up_bytes + q * (up_bytes / 4);
+                    uint32_t bad = 0;
+#pragma unroll 4
+                    for (int o = lane * 16; o < up_bytes / 4; o += 512) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(v + o);
+                        bad |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
+                    }
+                    if (__any_sync(0xffffffffu, bad)) {
+                        for (int o = lane * 2; o < up_bytes / 4; o += 64) {
+                            uint16_t* w = reinterpret_cast<uint16_t*>(v + o);
+                            if ((*w & 0x7f80) == 0x7f80) *w = 0;
+                        }
+                        const int a = p.list[j];
+                        uint8_t* h = gbase + s * F::STAGE + P_BYTES + i * terms * h_bytes;  // its rows, whatever the order within one
+                        for (int t = 0; t < p.M; ++t)
+                            if (p.ids[t] == a && lane < p.cw / 2) *reinterpret_cast<uint32_t*>(h + (t * p.cw + lane * 2) * 2) = 0x7fc07fc0u;
+                    }
+                    if (++part == p.parts) {
+                        part = 0;
+                        ++j;
+                    }
+                }
+                fence_smem_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(checked(s));
+            }
             if (!dead && (!bar_wait_warp(acc_full(b), (uint32_t)(n >> 1) & 1u, p.err, 4) || stop)) {
                 stop = 1;
                 dead = true;
             }
             fence_after_sync();
 #pragma unroll 1
-            for (int g = 0; g < groups; ++g) {
-                const int owner = g % p.splits;
+            for (int g = 0, owner = -1, l = 0; g < groups; ++g) {  // l: the owner's groups before this one
+                if (++owner == p.splits) {
+                    owner = 0;
+                    ++l;
+                }
                 if (p.splits > 1 && owner == slice) continue;
                 float v[8];
                 sums(b, g, v);
                 if (p.splits == 1) {
                     finish(tile * rows, g, v);
                 } else {
-                    const uint32_t to = cluster_addr(base + S * F::STAGE + ((slice - (slice > owner)) * NQ + 8 * g) * TILE_P * 4, owner);
+                    const int at = (slice - (slice > owner)) * own_groups + l;
+                    const uint32_t to = cluster_addr(base + S * F::STAGE + at * 8 * TILE_P * 4, owner);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) st_cluster(to + (j * TILE_P + row) * 4, v[j]);
                 }
@@ -550,13 +762,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
             cluster_barrier();
             fence_after_sync();
 #pragma unroll 1
-            for (int g = slice; g < groups; g += p.splits) {
+            for (int g = slice, l = 0; g < groups; g += p.splits, ++l) {
                 float v[8];
                 sums(0, g, v);
 #pragma unroll 1
                 for (int o = 0; o < p.splits - 1; ++o)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += red[(o * NQ + 8 * g + j) * TILE_P + row];
+                    for (int j = 0; j < 8; ++j) v[j] += red[((o * own_groups + l) * 8 + j) * TILE_P + row];
                 finish(tile0 * rows, g, v);
             }
         }
@@ -574,6 +786,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
 }
 
 // ------------------------------------------------------------------ host side
+// The `down` matrices [n][two][rank, K] in boxes of 64 values x cw rows, 128-byte swizzle.
+bool map_down(CUtensorMap* m, const LoraArgs& p, int two) {
+    const MxEncodeFn fn = mx_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)p.K, (cuuint64_t)p.rank, (cuuint64_t)two, (cuuint64_t)p.n};
+    cuuint64_t strides[3] = {(cuuint64_t)p.K * 2, (cuuint64_t)p.K * 2 * p.rank, (cuuint64_t)p.down_stride};
+    cuuint32_t box[4] = {64, (cuuint32_t)p.cw, 1, 1};
+    cuuint32_t one[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.down), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int few_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 // CTAs (a cluster) that share a tile along K: a CTA's stages (64 values of K, about a third of a microsecond each), and
@@ -603,31 +827,41 @@ cudaLaunchConfig_t config(dim3 grid, int threads, int smem, cudaStream_t s, cuda
     return cfg;
 }
 
-template <int NT>
-cudaError_t launch_rows(LoraArgs& p, cudaStream_t s) {
-    const int64_t subs = p.tiles * (p.tile_rows / SUB);
-    p.col_ctas = p.parts * p.cw / (8 * NT);
-    // Slices of 1024 and more values of K, what a CTA's eight warps have in flight at a time; no more than fill the SMs twice
-    // with CTAs that have work: one for each adapter with few rows, one for each 16 rows else.
-    const int64_t busy = p.col_ctas * (p.tile_rows == 256 ? subs : std::min<int64_t>(p.cap, p.T));
-    p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (p.K + 1023) / 1024, 2 * gemm_num_sms() / busy}));
-    p.slice_k = ((p.K + p.slices - 1) / p.slices + 31) / 32 * 32;
-    const int64_t each = subs * p.col_ctas * p.slices;
-    p.slots = (int)std::min<int64_t>(p.cap, std::max<int64_t>(1, 1024 / each));
-    const int64_t rows = each * p.slots, looks = ((int64_t)p.n * p.check_parts + p.slices - 1) / p.slices * p.slices;
+// The grid of lora_rows_kernel and its maps.
+cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
+    const int cols = p.parts * p.cw;
+    p.run = std::min(p.tile_rows, 128);
+    p.block_cols = std::min(cols, 128);
+    p.col_runs = (cols + 127) / 128;
+    p.k_stages = (p.K + 63) / 64;
+    p.tmem_cols = std::max(32, p.run);
+    // 64 KB and more of loads in flight; the products read 128 rows of the last stage's left operand, whatever lies behind it
+    const int stage = (p.block_cols + p.run) * 128;
+    p.stages = std::max(3, std::min(ROWS_MAX_STAGES, 65536 / stage));
+    // A cluster for each run of rows and columns and each adapter that there may be (few rows) or two (a full tile has few), over
+    // slices of 96 KB and more; as many as are resident together, two an SM.
+    const bool few = p.tile_rows != 256;
+    const int64_t runs = p.tiles * (p.tile_rows / p.run) * p.col_runs, room = 2 * gemm_num_sms() - (few ? 0 : LOOK_CTAS / 2);
+    p.slots = few ? (int)std::min<int64_t>(p.cap, p.T) : std::min(p.cap, 2);
+    p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (int64_t)p.k_stages * stage / 98304, room / (runs * p.slots)}));
+    const int groups = p.run / 8, red = (p.slices - 1) * ((groups + p.slices - 1) / p.slices) * 8 * p.block_cols * 4;
+    const int smem = 1024 + p.stages * stage + std::max(red, 128 * 128);
+    const int64_t rows = runs * p.slots * p.slices, most = std::max<int64_t>(LOOK_CTAS / 6, std::min<int64_t>(LOOK_CTAS, 2 * gemm_num_sms() - rows));
+    const int64_t looks = few ? 0 : std::min<int64_t>((most + p.slices - 1) / p.slices, ((int64_t)p.n * p.check_parts + p.slices - 1) / p.slices) * p.slices;
     if (rows + looks > 0x7fffffffll) return cudaErrorInvalidValue;
     p.rows_ctas = (int)rows;
-    auto kern = lora_rows_kernel<NT>;
-    static SmemCarveout wide;
-    wide.ask(reinterpret_cast<const void*>(kern));
+    if (!lora_map(&p.map_x, p.x, p.T, p.K, 64, p.run, 0, 0) || !map_down(&p.map_down, p, dual ? 2 : 1)) return cudaErrorInvalidValue;
+    static SmemAllowance allowed;
+    const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(lora_rows_kernel), smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t cfg = config(dim3((unsigned)(rows + looks)), DOWN_THREADS, 0, s, at, false);
+    cudaLaunchConfig_t cfg = config(dim3((unsigned)(rows + looks)), ROWS_THREADS, smem, s, at, false);
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = p.slices;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.numAttrs = p.slices > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, lora_rows_kernel, p);
 }
 
 template <int NQ>
@@ -638,6 +872,8 @@ cudaError_t launch_few(FewLora& p, int rows, cudaStream_t s) {
     const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), F::SMEM);
     if (e != cudaSuccess) return e;
     p.tiles = (p.N + rows - 1) / rows;
+    p.pack = std::max(1, F::PACK * 32 / p.cw);
+    p.halves = F::PACK * 32 / p.cw ? 1 : 2;  // 2 where rows of 64 columns meet more than 32 tokens
     p.splits = few_splits(p.tiles, p.k_stages, F::MAX_SPLIT);
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = config(dim3(p.splits > 1 ? p.tiles * p.splits : std::min(p.tiles, gemm_num_sms())), FEW_THREADS, F::SMEM, s, at, true);
@@ -661,7 +897,7 @@ Layout layout(const LoraArgs& p) {
     l.list = up256(4 * p.tiles);
     l.notes = l.list + up256(4 * p.tiles * p.cap);
     l.h = l.notes + up256(16ll * p.n);
-    l.bytes = l.h + p.tiles * p.cap * p.parts * 2ll * LORA_TERMS * p.tile_rows * p.cw;
+    l.bytes = l.h + p.tiles * p.cap * p.parts * 2ll * p.terms * p.tile_rows * p.cw;
     return l;
 }
 
@@ -690,7 +926,8 @@ bool lora_plan(LoraArgs& p, bool dual) {
     p.check_parts = 1;
     while (p.check_parts < 16 && (int64_t)p.N * p.rank * 2 / p.check_parts > 24576) p.check_parts *= 2;
     // blocks are rows of one tensor map, counted in 32 bits
-    return p.tiles * p.cap * p.parts * LORA_TERMS * p.tile_rows <= 0x7fffffffll && (int64_t)p.n * p.check_parts <= 0x3fffffffll;
+    p.terms = p.tile_rows == 256 ? 3 : 2;
+    return p.tiles * p.cap * p.parts * p.terms * p.tile_rows <= 0x7fffffffll && (int64_t)p.n * p.check_parts <= 0x3fffffffll;
 }
 
 int64_t lora_ws_bytes(const LoraArgs& p) { return layout(p).bytes; }
@@ -704,17 +941,17 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     p.notes = w + l.notes;
     p.h = reinterpret_cast<__nv_bfloat16*>(w + l.h);
     const bool few = p.tile_rows != 256;
-    // few rows: more CTAs of 16 columns each, and room beside the product's shared memory
-    const cudaError_t e = p.cw == 16 || few ? launch_rows<2>(p, s) : p.cw == 32 ? launch_rows<4>(p, s) : launch_rows<8>(p, s);
+    const cudaError_t e = launch_rows(p, dual, s);
     if (e != cudaSuccess) return e;
-    const int64_t h_rows = p.tiles * p.cap * p.parts * LORA_TERMS * p.tile_rows;
+    const int64_t h_rows = p.tiles * p.cap * p.parts * p.terms * p.tile_rows;
     if (!few) return launch_gemm_bf16_lora(d, p, h_rows, s);
+    const int rows = dual ? TILE_P / 2 : TILE_P;
     FewLora f;
     memset(&f, 0, sizeof(f));
-    if (!lora_map(&f.map_w, d.B, d.b_rows, d.K, 64, 64, 0, 0) || !lora_map(&f.map_x, d.A, d.M, d.K, 64, p.tile_rows, 0, 0) ||
-        !lora_map(&f.map_h, p.h, h_rows, p.cw, p.cw, 2 * p.tile_rows, 0, 0) ||
-        !lora_map(&f.map_up, p.up, d.N, p.rank, p.cw, 64, p.n, p.up_stride) ||
-        (dual && !lora_map(&f.map_up2, p.up2, d.N, p.rank, p.cw, 64, p.n, p.up_stride)))
+    if (!lora_map(&f.map_w, d.B, d.b_rows, d.K, 64, rows, 0, 0) || !lora_map(&f.map_x, d.A, d.M, d.K, 64, p.tile_rows, 0, 0) ||
+        !lora_map(&f.map_h, p.h, h_rows, p.cw, p.cw, (p.cw == 64 && p.tile_rows > 32 ? 1 : 2) * p.tile_rows, 0, 0) ||
+        !lora_map(&f.map_up, p.up, d.N, p.rank, p.cw, rows, p.n, p.up_stride) ||
+        (dual && !lora_map(&f.map_up2, p.up2, d.N, p.rank, p.cw, rows, p.n, p.up_stride)))
         return cudaErrorInvalidValue;
     f.M = d.M;
     f.N = d.N;
@@ -729,14 +966,13 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     f.rank = p.rank;
     f.count = p.count;
     f.list = p.list;
-    f.notes = p.notes;
+    f.ids = p.ids;
     f.bias = static_cast<const __nv_bfloat16*>(d.bias);
     f.resid = d.resid;
     f.resid_f32 = d.resid_f32;
     f.C = static_cast<__nv_bfloat16*>(d.C);
     f.C32 = static_cast<float*>(d.C32);
     f.err = d.err_word;
-    const int rows = dual ? 64 : 128;
     switch (p.tile_rows) {
         case 16: return launch_few<16>(f, rows, s);
         case 32: return launch_few<32>(f, rows, s);

@@ -540,8 +540,6 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    static SmemCarveout wide;
-    wide.ask(reinterpret_cast<const void*>(split_sorted_kernel));
     const cudaError_t e = cudaLaunchKernelEx(&cfg, split_sorted_kernel, static_cast<const __nv_bfloat16*>(d.A), d.gather_k > 0 ? d.row_table : nullptr,
                                              d.gather_k, d.a_rows, d.M, d.K, per_row, rows_a_cta, terms, scales, p.scale_pitch);
     if (e != cudaSuccess) return e;

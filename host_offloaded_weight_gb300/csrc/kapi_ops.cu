@@ -1,6 +1,8 @@
 // C entry points of the 4-bit, few-token and per-row operators (see ls_kernels.h).
 #include <cuda_runtime.h>
 
+#include <string.h>
+
 #include "kernels.h"
 #include "ls_kernels.h"
 
@@ -165,7 +167,8 @@ ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A, const void* B, int
         !aligned(C32, 16))
         return LS_ERR_INVALID_ARG;
     if (ds < down_bytes || us < up_bytes || (ds % 16) || (us % 16) || ds >= (1ll << 40) || us >= (1ll << 40)) return LS_ERR_INVALID_ARG;
-    LoraArgs p = {};
+    LoraArgs p;
+    memset(&p, 0, sizeof(p));
     p.x = static_cast<const __nv_bfloat16*>(A);
     p.ids = ids;
     p.down = l->down;
@@ -179,6 +182,7 @@ ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A, const void* B, int
     p.K = K;
     p.n = l->n;
     p.rank = l->rank;
+    p.err = entry_error_word();
     if (!lora_plan(p, dual)) return LS_ERR_UNSUPPORTED;
     GemmDesc d;
     d.epi = epilogue;

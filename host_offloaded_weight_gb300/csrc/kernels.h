@@ -116,19 +116,6 @@ struct SmemAllowance {
         return set;
     }
 };
-// The largest shared-memory carveout for a kernel that the next one is to start beside: an SM that runs a kernel with a
-// smaller one has to be empty before it takes a CTA with more shared memory. A hint: a refusal is not an error.
-struct SmemCarveout {
-    std::atomic<uint64_t> asked{0};  // by device
-    void ask(const void* kernel) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return;
-        if (asked.load(std::memory_order_relaxed) >> dev & 1) return;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-            cudaGetLastError();
-        asked.fetch_or(1ull << dev, std::memory_order_relaxed);
-    }
-};
 // Tile width (output columns) of the dense pair-CTA GEMM for an M x N output.
 int gemm_pair_tile_n(int64_t M, int64_t N);
 // K slices of a dense single-CTA GEMM (M <= 128, not the gate/up pair): 1 when it is not split.
@@ -140,7 +127,6 @@ int64_t gemm_split_ws_max();
 
 // ---------------------------------------------------------------- low-rank adapters beside a shared projection
 constexpr int LORA_FEW_ROWS = 128, LORA_MAX_RANK = 256;
-constexpr int LORA_TERMS = 3;  // of h: two that add up to it, and NaN in the adapter's rows
 struct LoraArgs {
     // of the caller
     const __nv_bfloat16* x;   // [T, K]
@@ -153,10 +139,13 @@ struct LoraArgs {
     int T, N, K, n, rank;
     // by lora_plan. h as blocks [tile][adapter of the tile][part][term] of tile_rows x cw values; a part is cw of
     // the rank's columns, the gate's `chunks` parts first
-    int cw, chunks, parts, tile_rows, cap, check_parts;
+    // Terms: two that add up to h, and for the pair kernel a third, NaN in the adapter's rows.
+    int cw, chunks, parts, tile_rows, cap, check_parts, terms;
     int64_t tiles;
     // the first kernel's grid
-    int rows_ctas, slots, col_ctas, slices, slice_k;
+    CUtensorMap map_x, map_down;
+    int run, block_cols, col_runs, k_stages, tmem_cols, stages, slots, slices, rows_ctas;
+    uint32_t* err;
     // in scratch
     int* count;               // [tiles] adapters of a tile
     int* list;                // [tiles][cap] which
