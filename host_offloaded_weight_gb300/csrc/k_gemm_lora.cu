@@ -182,7 +182,6 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     const int cols = min(128, p.parts * p.cw - col0), part0 = col0 >> log_cw, parts = cols >> log_cw;
     const int groups = p.run / 8, own_groups = (groups + p.slices - 1) / p.slices;
     const int q = warp & 3, col = 32 * q + lane;   // the epilogue: q the TMEM lane quarter that a warp can read, col the lane's column
-    const int part = part0 + (col >> log_cw);
     const int rows = min(p.run, p.T - t0 - row0);  // rows that exist (zero and less: none)
     int it = 0, turn = 0;                          // stages and adapters so far
     int ring = 0;                                  // the place of the next stage, and the parity of its use
@@ -243,79 +242,77 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             }
             it += k1 - k0;
         }
-        const bool reads = warp >= ROWS_EPI && warp < ROWS_EPI + 4 && 32 * q < cols;
-        const uint32_t mine_at = tmem + ((uint32_t)(q * 32) << 16);
+        // this CTA's rows and columns, two columns a thread: row r is row (r & 7) of its r / 8th group
+        const int own = groups > slice ? (groups - slice + p.slices - 1) / p.slices * 8 : 0, log_units = 31 - __clz(cols) - 1;
         const float scale = any && p.scale ? __ldg(p.scale + a) : 1.f;
-        const int64_t block = ((int64_t)tile * p.cap + j) * p.parts + part, term = (int64_t)p.tile_rows * p.cw;
-        __nv_bfloat16* const h = p.h + (block * p.terms * p.tile_rows + row0) * p.cw + (col & (p.cw - 1));
-        auto sums = [&](int g, float (&v)[8]) {
-            uint32_t x[8];
-            tmem_load8(mine_at + 8 * g, x);
-            tmem_load_wait();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[i]);
-        };
-        // Two rounds over this CTA's groups of rows: zeros in the rows of others, while the loads are on their way, then h in the
-        // adapter's own.
-        for (int round = 0; round < 2; ++round) {
-            if (round == 1) {
-                if (!any) break;
-                const bool done = bar_wait_warp(acc_full, (uint32_t)turn & 1u, p.err, 4);   // every warp: nobody is ahead by an adapter
-                if (!done) stop = 1;
-                if (j + p.slots >= count) grid_release();
-                fence_after_sync();
-                ++turn;
-                if (p.slices > 1) {
-                    if (reads)
-                        for (int g = 0, owner = 0, l = 0; g < groups && 8 * g < rows; ++g) {  // l: the owner's groups before this one
-                            if (owner != slice) {
-                                float v[8];
-                                sums(g, v);
-                                const int at = ((slice - (slice > owner)) * own_groups + l) * 8 * p.block_cols + col;
-                                const uint32_t to = cluster_addr(smem_addr(red + at), owner);
-                                if (col < cols)
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) st_cluster(to + i * p.block_cols * 4, v[i]);
-                            }
-                            if (++owner == p.slices) {
-                                owner = 0;
-                                ++l;
-                            }
-                        }
-                    __syncwarp();
-                    cluster_barrier_smem();
-                }
+        const int64_t term = (int64_t)p.tile_rows * p.cw / 2;
+        auto each = [&](auto f) {   // f(row of the run, local row, column, where its pair of h goes)
+            for (int u = tid; u < own << log_units; u += ROWS_THREADS) {
+                const int l = u >> log_units, c = (u - (l << log_units)) * 2, r = (slice + (l >> 3) * p.slices) * 8 + (l & 7);
+                const int64_t block = ((int64_t)tile * p.cap + j) * p.parts + part0 + (c >> log_cw);
+                f(r, l, c, reinterpret_cast<uint32_t*>(p.h + (block * p.terms * p.tile_rows + row0 + r) * p.cw + (c & (p.cw - 1))));
             }
-            if (!reads) continue;
-#pragma unroll 1
-            for (int g = slice, l = 0; g < groups; g += p.slices, ++l) {
-                float v[8] = {};
-                if (round == 1 && 8 * g < rows) {
-                    sums(g, v);
-                    for (int o = 0; o < p.slices - 1; ++o) {
-                        const float* from = red + (o * own_groups + l) * 8 * p.block_cols + (col < cols ? col : 0);
+        };
+        __syncwarp();
+        // zeros in the rows of others, while the loads are on their way (the two warps that see to those come later)
+        each([&](int r, int, int, uint32_t* to) {
+            if (s_ids[row0 + r] == a) return;
+            for (int t = 0; t < p.terms; ++t) to[t * term] = 0;
+        });
+        if (any) {
+            const bool done = bar_wait_warp(acc_full, (uint32_t)turn & 1u, p.err, 4);   // every warp: nobody is ahead by an adapter
+            if (!done) stop = 1;
+            if (j + p.slots >= count) grid_release();
+            fence_after_sync();
+            ++turn;
+            // every CTA's sums of a row go to the CTA that has it
+            if (warp >= ROWS_EPI && warp < ROWS_EPI + 4 && 32 * q < cols)
+                for (int g = 0, owner = 0, l = 0; g < groups && 8 * g < rows; ++g) {
+                    uint32_t v[8];
+                    tmem_load8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(8 * g), v);
+                    tmem_load_wait();
+                    const uint32_t to = smem_addr(red + ((slice * own_groups + l) * 8) * p.block_cols + col);
+                    if (col < cols) {
+                        if (p.slices == 1) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] += from[i * p.block_cols];
+                            for (int i = 0; i < 8; ++i) st_shared1(to + i * p.block_cols * 4, v[i]);
+                        } else {
+                            const uint32_t there = cluster_addr(to, owner);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) st_cluster(there + i * p.block_cols * 4, __uint_as_float(v[i]));
+                        }
+                    }
+                    if (++owner == p.slices) {
+                        owner = 0;
+                        ++l;
                     }
                 }
-                // the rows of this round
-                uint32_t which = __ballot_sync(0xffffffffu, lane < 8 && s_ids[row0 + 8 * g + (lane & 7)] == a);
-                if (round == 0) which ^= 0xffu;
-                if (col >= cols) continue;
-                __nv_bfloat16* to = h + 8 * g * p.cw;
+            fence_before_sync();
+            __syncwarp();
+            if (p.slices > 1) cluster_barrier_smem();
+            else __syncthreads();
+            each([&](int r, int l, int c, uint32_t* to) {
+                if (s_ids[row0 + r] != a) return;
+                float2 v = make_float2(0.f, 0.f);
+                const float* from = red + l * p.block_cols + c;
+                for (int o = 0; o < p.slices; ++o, from += own_groups * 8 * p.block_cols) {
+                    const float2 x = *reinterpret_cast<const float2*>(from);
+                    v.x += x.x;
+                    v.y += x.y;
+                }
+                uint32_t hi = 0, lo = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i, to += p.cw) {
-                    const float w = round ? v[i] * scale : 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    const float w = (e ? v.y : v.x) * scale;
                     float t1 = __bfloat162float(__float2bfloat16_rn(w));
                     if (isinf(t1) && !isinf(w)) t1 = __bfloat162float(__float2bfloat16_rz(w));
-                    const __nv_bfloat16 t2 = __float2bfloat16_rn(isfinite(t1) ? w - t1 : 0.f);
-                    if (which >> i & 1) {
-                        to[0] = __float2bfloat16_rn(t1);
-                        to[term] = t2;
-                        if (p.terms == 3) to[2 * term] = __ushort_as_bfloat16(round ? 0x7fc0 : 0);
-                    }
+                    hi |= (__float_as_uint(t1) >> 16) << (16 * e);
+                    lo |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(isfinite(t1) ? w - t1 : 0.f)) << (16 * e);
                 }
-            }
+                to[0] = hi;
+                to[term] = lo;
+                if (p.terms == 3) to[2 * term] = 0x7fc07fc0u;  // NaN
+            });
         }
         fence_before_sync();
         __syncwarp();
@@ -844,7 +841,7 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     const int64_t runs = p.tiles * (p.tile_rows / p.run) * p.col_runs, room = 2 * gemm_num_sms() - (few ? 0 : LOOK_CTAS / 2);
     p.slots = few ? (int)std::min<int64_t>(p.cap, p.T) : std::min(p.cap, 2);
     p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (int64_t)p.k_stages * stage / 98304, room / (runs * p.slots)}));
-    const int groups = p.run / 8, red = (p.slices - 1) * ((groups + p.slices - 1) / p.slices) * 8 * p.block_cols * 4;
+    const int groups = p.run / 8, red = p.slices * ((groups + p.slices - 1) / p.slices) * 8 * p.block_cols * 4;
     const int smem = 1024 + p.stages * stage + std::max(red, 128 * 128);
     const int64_t rows = runs * p.slots * p.slices, most = std::max<int64_t>(LOOK_CTAS / 6, std::min<int64_t>(LOOK_CTAS, 2 * gemm_num_sms() - rows));
     const int64_t looks = few ? 0 : std::min<int64_t>((most + p.slices - 1) / p.slices, ((int64_t)p.n * p.check_parts + p.slices - 1) / p.slices) * p.slices;
