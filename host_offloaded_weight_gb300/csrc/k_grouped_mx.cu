@@ -10,6 +10,7 @@
 // CTA an SM: warp 0 loads by TMA, warp 1 copies the scales to TMEM and issues the products, four warps at a time take turns at
 // bringing the block scales, four write the results while the next tile is computed (two accumulators).
 #include <algorithm>
+#include <cstdlib>
 
 #include "kernels.h"
 #include "tc.cuh"
@@ -20,8 +21,11 @@ namespace {
 using namespace tc;
 
 constexpr int TILE_P = 128, P_BYTES = TILE_P * 128;
-constexpr int CHUNK = 16;                    // rows of a box: 32 columns with both terms
+constexpr int CHUNK = 16;                    // rows that a tile's columns are counted in: 32 columns with both terms
 constexpr int CHUNK_BYTES = 2 * CHUNK * 128;
+// A tile's chunks come in boxes of four, two and one, the larger ones first (a copy for each chunk kept the loading warp
+// 45 clocks each busy, 630 a stage); a box has the first terms of its rows, then the second ones.
+constexpr int BOXES = 3;
 constexpr int TEAM = 4, EPI_WARPS = 8;
 constexpr int PAIR = 16;                     // gate/up tiles: rows of one matrix side by side
 constexpr int MAX_G = GROUPED_MX_MAX_GROUPS;
@@ -34,8 +38,8 @@ struct Cfg {
     static constexpr int Q_BYTES = MAXC * CHUNK_BYTES;
     static constexpr int SCALE_BYTES = (1 + PARTS) * 512;
     static constexpr int STAGE = (P_BYTES + Q_BYTES + SCALE_BYTES + 1023) / 1024 * 1024;
-    static constexpr int BLOCKS = (MAXC * CHUNK + 31) / 32;    // of 32 rows
-    static constexpr int FIT = (232448 - 1024 - 1024 - 4 * (MAX_G + 1)) / STAGE;
+    static constexpr int OWN_ROWS = (MAXC + 1) / 2 * CHUNK;    // rows of an epilogue warp
+    static constexpr int FIT = (232448 - 1024 - 1024 - 20 * (MAX_G + 1) - 8 * EPI_WARPS * OWN_ROWS) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT / 2 * 2 : 8;
     static constexpr int TEAMS = 2, RUN = STAGES >= 5 ? 4 : 2; // scale warps: teams take turns of RUN stages
     static constexpr int SCALE_COLS = 4 * (1 + PARTS);
@@ -48,7 +52,9 @@ struct Cfg {
 };
 
 struct GroupedParams {
-    CUtensorMap map_p, map_p2, map_q;   // weights [groups][rows][K] (p2: the up matrices), terms [2][M][K]
+    // Weights [groups][rows][K] (p2: the up matrices; both: gate and up in one map, see map_both) and terms [2][M][K]
+    CUtensorMap map_p, map_p2, map_q[BOXES];
+    int both, up_first;
     const uint8_t* scale_p;
     const uint8_t* scale_p2;
     int64_t scale_stride;               // bytes between groups
@@ -62,31 +68,83 @@ struct GroupedParams {
     uint32_t* err;
 };
 
-struct Tile {
-    int g, p0, row, rows, chunks;   // group, first output column, first sorted row, rows, chunks of 16
+// Column of the first term of row i of a tile of `chunks`, and how many columns after it the second one's is.
+__device__ __forceinline__ int column(int chunks, int i, int& apart) {
+    int first = 0;
+#pragma unroll
+    for (int size = CHUNK << (BOXES - 1); size > CHUNK; size >>= 1)
+        if (chunks & (size / CHUNK)) {
+            if (i < first + size) {
+                apart = size;
+                return first + i;
+            }
+            first += size;
+        }
+    apart = CHUNK;
+    return first + i;
+}
+// The row of column c, and which term.
+__device__ __forceinline__ int row_of(int chunks, int c, int& term) {
+    int first = 0;
+#pragma unroll
+    for (int size = CHUNK << (BOXES - 1); size > CHUNK; size >>= 1)
+        if (chunks & (size / CHUNK)) {
+            if (c < 2 * (first + size)) {
+                term = c - 2 * first >= size;
+                return c - first - (term ? size : 0);
+            }
+            first += size;
+        }
+    term = c - 2 * first >= CHUNK;
+    return c - first - (term ? CHUNK : 0);
+}
+
+// What the CTAs keep of the groups in shared memory.
+struct Groups {
+    int first[MAX_G + 1];   // row tiles before each group
+    int row[MAX_G];         // its first row
+    int end[MAX_G];
+    int share[MAX_G];       // chunks of each of its row tiles, the first `more` of them have one more
+    int more[MAX_G];
 };
 
-// Tile t of the launch: weight tiles innermost, so that the CTAs at work share a group's rows.
-template <int MAXC>
-__device__ __forceinline__ Tile tile_at(const GroupedParams& p, const int* first, int t) {
-    const int n = t % p.tiles_p, mt = t / p.tiles_p;
-    int lo = 0, hi = p.n_groups - 1;  // the last group with first[g] <= mt
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] <= mt) lo = mid;
-        else hi = mid - 1;
+// A CTA's tiles, in order: weight tiles innermost, so that the CTAs at work share a group's rows. Steps by additions: a
+// division by a number that only the launch knows takes 150 clocks.
+struct Tiles {
+    const Groups& s;
+    int t, n, mt, g;                // tile, weight tile, row tile, group
+    int step_n, step_mt;
+    int p0, row, rows, chunks;      // first output column, first sorted row, rows, chunks of 16
+    __device__ __forceinline__ Tiles(const GroupedParams& p, const Groups& groups) : s(groups), t((int)blockIdx.x), g(0) {
+        step_mt = (int)gridDim.x / p.tiles_p;
+        step_n = (int)gridDim.x - step_mt * p.tiles_p;
+        mt = t / p.tiles_p;
+        n = t - mt * p.tiles_p;
     }
-    Tile r;
-    r.g = lo;
-    r.p0 = n * (p.dual ? TILE_P / 2 : TILE_P);
-    const int r0 = max(p.bounds[lo], 0), r1 = min(p.bounds[lo + 1], p.M), c = (r1 - r0 + CHUNK - 1) / CHUNK;
-    const int tiles = (c + MAXC - 1) / MAXC, q = mt - first[lo];
-    const int c0 = (int)((int64_t)c * q / tiles), c1 = (int)((int64_t)c * (q + 1) / tiles);  // even shares
-    r.row = r0 + c0 * CHUNK;
-    r.chunks = c1 - c0;
-    r.rows = min(r1 - r.row, r.chunks * CHUNK);
-    return r;
-}
+    __device__ __forceinline__ void next(const GroupedParams& p) {
+        t += gridDim.x;
+        mt += step_mt;
+        n += step_n;
+        if (n >= p.tiles_p) {
+            n -= p.tiles_p;
+            ++mt;
+        }
+    }
+    // the tile's place, for t below the number of tiles
+    __device__ __forceinline__ void find(const GroupedParams& p) {
+        int hi = p.n_groups - 1;  // the last group with first[g] <= mt, from the one before on
+        while (g < hi) {
+            const int mid = (g + hi + 1) >> 1;
+            if (s.first[mid] <= mt) g = mid;
+            else hi = mid - 1;
+        }
+        const int q = mt - s.first[g], more = s.more[g];
+        p0 = n * (p.dual ? TILE_P / 2 : TILE_P);
+        chunks = s.share[g] + (q < more ? 1 : 0);
+        row = s.row[g] + (q * s.share[g] + min(q, more)) * CHUNK;
+        rows = min(s.end[g] - row, chunks * CHUNK);
+    }
+};
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
@@ -114,7 +172,9 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
     const uint32_t done = bars + 8u * (2 * S + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (2 * S + 5));
     __shared__ volatile int stop;
-    __shared__ int first[MAX_G + 1];   // row tiles before each group
+    __shared__ Groups groups;
+    __shared__ __align__(16) int s_to[EPI_WARPS][C::OWN_ROWS];
+    __shared__ __align__(16) float s_weight[EPI_WARPS][C::OWN_ROWS];
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -130,8 +190,8 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         bar_init(done, 1);
         bar_init_fence();
         tma_desc_prefetch(&p.map_p);
-        tma_desc_prefetch(&p.map_q);
-        if (p.dual) tma_desc_prefetch(&p.map_p2);
+        for (int i = 0; i < BOXES; ++i) tma_desc_prefetch(&p.map_q[i]);
+        if (p.dual && !p.both) tma_desc_prefetch(&p.map_p2);
     }
     if (warp == 1) tmem_get(smem_addr(tmem_slot), C::TMEM_COLS);
     // The kernel before this one, which splits the rows, began after everything earlier was complete: only the split rows have
@@ -142,8 +202,12 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             const int g = g0 + lane;
             int t = 0;
             if (g < p.n_groups) {
-                const int n = min(p.bounds[g + 1], p.M) - max(p.bounds[g], 0);
-                t = n > 0 ? ((n + CHUNK - 1) / CHUNK + MAXC - 1) / MAXC : 0;
+                const int r0 = max(p.bounds[g], 0), r1 = min(p.bounds[g + 1], p.M), c = max(r1 - r0 + CHUNK - 1, 0) / CHUNK;
+                t = (c + MAXC - 1) / MAXC;
+                groups.row[g] = r0;
+                groups.end[g] = r1;
+                groups.share[g] = t ? c / t : 0;
+                groups.more[g] = t ? c % t : 0;
             }
             int before = t;
 #pragma unroll
@@ -151,16 +215,16 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
                 const int o = __shfl_up_sync(0xffffffffu, before, i);
                 if (lane >= i) before += o;
             }
-            if (g < p.n_groups) first[g] = sum + before - t;
+            if (g < p.n_groups) groups.first[g] = sum + before - t;
             sum += __shfl_sync(0xffffffffu, before, 31);
         }
-        if (lane == 0) first[p.n_groups] = sum;
+        if (lane == 0) groups.first[p.n_groups] = sum;
     }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const int stages = p.k_stages, tiles = first[p.n_groups] * p.tiles_p;
+    const int stages = p.k_stages, tiles = groups.first[p.n_groups] * p.tiles_p;
 
     if (warp == 0) {
         // ------------------------------------------------------------ operand tiles
@@ -168,14 +232,16 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         int s = 0, it = 0;
         uint32_t phase = 1;  // a new barrier's preceding phase counts as complete
         bool ok = true, waited = false;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const Tile tl = tile_at<MAXC>(p, first, t);
+        for (Tiles tl(p, groups); ok && tl.t < tiles; tl.next(p)) {
+            tl.find(p);
             // an unpacking copy counts the packed bytes (it leaves every second 8 bytes alone)
             const uint32_t bytes = P_BYTES / 2 + tl.chunks * CHUNK_BYTES;
             auto weights = [&](int st, int k) {
                 const uint32_t at = base + st * C::STAGE;
                 bar_expect(full(st), bytes);
-                if (p.dual) {
+                if (p.both) {
+                    tma_5d(at, &p.map_p, full(st), k * 128, 0, 0, tl.p0 / PAIR, tl.g);
+                } else if (p.dual) {
                     for (int i = 0; i < TILE_P / 2; i += PAIR) {
                         tma_3d(at + 2 * i * 128, &p.map_p, full(st), k * 128, tl.p0 + i, tl.g);
                         tma_3d(at + (2 * i + PAIR) * 128, &p.map_p2, full(st), k * 128, tl.p0 + i, tl.g);
@@ -186,7 +252,13 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             };
             auto rows = [&](int st, int k) {
                 const uint32_t at = base + st * C::STAGE + P_BYTES;
-                for (int c = 0; c < tl.chunks; ++c) tma_3d(at + c * CHUNK_BYTES, &p.map_q, full(st), k * 128, tl.row + c * CHUNK, 0);
+                int c = 0;
+#pragma unroll
+                for (int i = BOXES - 1; i >= 0; --i)
+                    if (tl.chunks >> i & 1) {
+                        tma_3d(at + c * CHUNK_BYTES, &p.map_q[i], full(st), k * 128, tl.row + c * CHUNK, 0);
+                        c += 1 << i;
+                    }
             };
             int k = 0;
             if (!waited) {  // the first stages' weights need not wait for the split rows
@@ -232,8 +304,8 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         const bool one = elect_one();
         int n = 0, it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
-            const Tile tl = tile_at<MAXC>(p, first, t);
+        for (Tiles tl(p, groups); ok && tl.t < tiles; tl.next(p), ++n) {
+            tl.find(p);
             const uint32_t idesc = mx_idesc(5, 0, TILE_P, 32 * tl.chunks);
             const int b = n & 1, parts = (32 * tl.chunks + 127) / 128;
             if (!bar_wait_warp(acc_empty(b), (uint32_t)((n >> 1) + 1) & 1u, p.err, 2) || stop) {
@@ -277,45 +349,44 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         constexpr int RUN = C::RUN, NR = 1 + C::PARTS;
         typedef typename Words<RUN>::type V;
         const int team = (warp - 2) / TEAM, w = (warp - 2) % TEAM, runs = (stages + RUN - 1) / RUN;
-        struct Turn {
-            int t, run, at;  // tile, turn of it, the tile's first stage in the ring's line
+        Tiles tl(p, groups);   // of the turn to request next
+        int run = 0, at_stage = 0;                    // that turn of its tile, the tile's first stage in the ring's line
+        int now_run, now_at;                          // the turn at hand
+        bool now_on;
+        auto skip = [&](int by) {
+            for (run += by; run >= runs; run -= runs, at_stage += stages) tl.next(p);
         };
-        auto after = [&](Turn u, int by) {
-            for (u.run += by; u.run >= runs; u.run -= runs, u.t += gridDim.x, u.at += stages) {}
-            return u;
-        };
-        Tile tl;
-        int tl_of = -1;
         V v[2][NR];
-        auto fetch = [&](V (&to)[NR], const Turn& u) {
-            if (u.t >= tiles) return;
-            if (tl_of != u.t) {
-                tl = tile_at<MAXC>(p, first, u.t);
-                tl_of = u.t;
-            }
-            const int64_t at = 4ll * RUN * u.run;
+        auto fetch = [&](V (&to)[NR]) {
+            if (tl.t >= tiles) return;
+            tl.find(p);
+            const int64_t at = 4ll * RUN * run;
             const int r = 32 * w + lane;
-            const bool second = p.dual && (r & PAIR);
+            const bool second = p.dual && ((r & PAIR) != 0) != (p.up_first != 0);
             const int row = tl.p0 + (p.dual ? r / (2 * PAIR) * PAIR + (r & (PAIR - 1)) : r);
             words((second ? p.scale_p2 : p.scale_p) + tl.g * p.scale_stride + (int64_t)row * p.scale_pitch + at, row < p.N, to[0]);
 #pragma unroll
             for (int j = 0; j < C::PARTS; ++j) {
-                const int q = 128 * j + r, i = q / 32 * CHUNK + (q & 15);  // column q: chunk, term, row of the chunk
-                const int64_t src = (int64_t)((q >> 4) & 1) * p.M + tl.row + i;
-                words_now(p.scale_q + src * p.scale_pitch + at, i < tl.rows, to[1 + j]);
+                int term;
+                const int i = row_of(tl.chunks, 128 * j + r, term);
+                const int64_t src = (int64_t)term * p.M + tl.row + i;
+                words_now(p.scale_q + src * p.scale_pitch + at, 128 * j + r < 32 * tl.chunks && i < tl.rows, to[1 + j]);
             }
         };
-        Turn u = after(Turn{(int)blockIdx.x, 0, 0}, team);
         bool ok = true;
         grid_wait();
-        fetch(v[0], u);
-        while (ok && u.t < tiles) {
-            const Turn next = after(u, C::TEAMS);
-            fetch(v[1], next);
+        skip(team);
+        fetch(v[0]);
+        now_on = tl.t < tiles;
+        while (ok && now_on) {
+            now_run = run;
+            now_at = at_stage;
+            skip(C::TEAMS);
+            fetch(v[1]);
 #pragma unroll
             for (int i = 0; i < RUN; ++i) {
-                if (!ok || u.run * RUN + i >= stages) continue;
-                const int it = u.at + u.run * RUN + i, s = it % S;
+                if (!ok || now_run * RUN + i >= stages) continue;
+                const int it = now_at + now_run * RUN + i, s = it % S;
                 if (!bar_wait_warp(empty(s), (uint32_t)(it / S + 1) & 1u, p.err, 7)) {
                     ok = false;
                     stop = 1;
@@ -330,29 +401,31 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             }
 #pragma unroll
             for (int j = 0; j < NR; ++j) v[0][j] = v[1][j];
-            u = next;
+            now_on = tl.t < tiles;
         }
     } else {
         // ------------------------------------------------------------ results
-        // Two warps a TMEM lane quarter, each with every second group of eight rows. A lane has a weight row, an output column.
+        // Two warps a TMEM lane quarter, each with every second chunk of 16 rows. A lane has a weight row, an output column.
         // Gate/up tiles alternate: 16 gate rows, the 16 up rows of the same columns, so that a lane's partner is 16 lanes away;
         // each of the two finishes half of the group's rows.
         const int q = warp & 3, half = (warp - C::FIRST_EPI) >> 2, row = 32 * q + lane;  // q: the lane quarter that this warp can read
         const bool upper = lane & 16;
+        int* const to = s_to[warp - C::FIRST_EPI];        // places and weights of this warp's rows
+        float* const w = s_weight[warp - C::FIRST_EPI];
         int n = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
-            const Tile tl = tile_at<MAXC>(p, first, t);
+        for (Tiles tl(p, groups); tl.t < tiles; tl.next(p), ++n) {
+            tl.find(p);
             const int b = n & 1;
-            // places and weights of the rows, read while the products run: lane l has rows l, 32 + l, ...
-            int to[C::BLOCKS];
-            float w[C::BLOCKS];
-            if (p.epi == EPI_SCALE_F32) {
-#pragma unroll
-                for (int c = 0; c < C::BLOCKS; ++c) {
-                    to[c] = 32 * c + lane < tl.rows ? __ldg(p.row_table + tl.row + 32 * c + lane) : -1;
-                    if (to[c] >= p.M) to[c] = -1;
-                    w[c] = to[c] >= 0 ? __ldg(p.row_weight + to[c]) : 0.f;
+            if (p.epi == EPI_SCALE_F32) {  // read while the products run; the warp's chunks are every second one
+                __syncwarp();
+                for (int l = lane; l < C::OWN_ROWS; l += 32) {
+                    const int i = ((l >> 4) * 2 + half) * CHUNK + (l & 15);
+                    int r = i < tl.rows ? __ldg(p.row_table + tl.row + i) : -1;
+                    if (r >= p.M) r = -1;
+                    to[l] = r;
+                    w[l] = r >= 0 ? __ldg(p.row_weight + r) : 0.f;
                 }
+                __syncwarp();
             }
             if (!bar_wait_warp(acc_full(b), (uint32_t)(n >> 1) & 1u, p.err, 4) || stop) {
                 stop = 1;
@@ -361,43 +434,46 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             fence_after_sync();
             const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::BQ);
             const int col = tl.p0 + (p.dual ? 16 * q + (lane & 15) : row);
-#pragma unroll
-            for (int c = 0; c < C::BLOCKS; ++c) {
+            const bool in = col < p.N;
 #pragma unroll 1
-                for (int g = half; g < 4; g += 2) {
-                    const int i0 = 32 * c + 8 * g;
-                    if (i0 >= tl.rows) break;
-                    uint32_t x[8], y[8];
-                    const uint32_t a = at + (uint32_t)(i0 / CHUNK * 32 + i0 % CHUNK);
-                    tmem_load8(a, x);
-                    tmem_load8(a + CHUNK, y);
-                    tmem_load_wait();
-                    float v[8];
+            for (int i0 = half * CHUNK, l0 = 0; i0 < tl.rows; i0 += 2 * CHUNK, l0 += CHUNK) {
+                uint32_t x[CHUNK], y[CHUNK];
+                int apart;
+                const uint32_t c = at + (uint32_t)column(tl.chunks, i0, apart);
+                tmem_load16(c, x);
+                tmem_load16(c + apart, y);
+                tmem_load_wait();
+                float v[CHUNK];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(y[j]) + __uint_as_float(x[j]);  // the smaller term first
-                    if (p.epi == EPI_SCALE_F32) {
+                for (int j = 0; j < CHUNK; ++j) v[j] = __uint_as_float(y[j]) + __uint_as_float(x[j]);  // the smaller term first
+                if (p.epi == EPI_SCALE_F32) {
+                    float* const out = static_cast<float*>(p.C) + col;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int r = __shfl_sync(0xffffffffu, to[c], 8 * g + j);
-                            const float wr = __shfl_sync(0xffffffffu, w[c], 8 * g + j);
-                            if (r >= 0 && col < p.N) static_cast<float*>(p.C)[(int64_t)r * p.N + col] = wr * v[j];
+                    for (int j = 0; j < CHUNK; j += 4) {
+                        const int4 r = *reinterpret_cast<const int4*>(to + l0 + j);
+                        const float4 f = *reinterpret_cast<const float4*>(w + l0 + j);
+                        if (in && r.x >= 0) out[(uint64_t)(uint32_t)r.x * (uint32_t)p.N] = f.x * v[j];
+                        if (in && r.y >= 0) out[(uint64_t)(uint32_t)r.y * (uint32_t)p.N] = f.y * v[j + 1];
+                        if (in && r.z >= 0) out[(uint64_t)(uint32_t)r.z * (uint32_t)p.N] = f.z * v[j + 2];
+                        if (in && r.w >= 0) out[(uint64_t)(uint32_t)r.w * (uint32_t)p.N] = f.w * v[j + 3];
+                    }
+                } else {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + (int64_t)(tl.row + i0) * p.N + col;
+                    const int rows = in ? tl.rows - i0 : 0;
+                    if (p.dual) {
+                        if (upper) out += (int64_t)(CHUNK / 2) * p.N;
+#pragma unroll
+                        for (int j = 0; j < CHUNK / 2; ++j, out += p.N) {
+                            const float mine = upper ? v[j + CHUNK / 2] : v[j];
+                            const float other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + CHUNK / 2], 16);
+                            const bool swap = upper != (p.up_first != 0);
+                            const float gate = swap ? other : mine, up = swap ? mine : other;
+                            if (j + (upper ? CHUNK / 2 : 0) < rows) *out = __float2bfloat16_rn(__fdividef(gate, 1.f + __expf(-gate)) * up);
                         }
                     } else {
-                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.C) + (int64_t)(tl.row + i0) * p.N + col;
-                        const int rows = col < p.N ? tl.rows - i0 : 0;
-                        if (p.dual) {
-                            if (upper) out += 4ll * p.N;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float other = __shfl_xor_sync(0xffffffffu, upper ? v[j] : v[j + 4], 16);
-                                const float gate = upper ? other : v[j], up = upper ? v[j + 4] : other;
-                                if (j + (upper ? 4 : 0) < rows) out[(int64_t)j * p.N] = __float2bfloat16_rn(gate / (1.f + __expf(-gate)) * up);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (j < rows) out[(int64_t)j * p.N] = __float2bfloat16_rn(v[j]);
-                        }
+                        for (int j = 0; j < CHUNK; ++j, out += p.N)
+                            if (j < rows) *out = __float2bfloat16_rn(v[j]);
                     }
                 }
             }
@@ -414,38 +490,74 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
     }
 }
 
+// split8 of tc.cuh, with the scaled values and what the first term leaves as f16 pairs: both are exact there, down to 2^-24 of
+// values below 2^8, far under what the second term can hold. (All in fp32: half as many instructions again.)
+__device__ __forceinline__ void split8_half(uint4 raw, uint2& o1, uint2& o2, uint32_t& b1, uint32_t& b2) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m & 0xffffu, m >> 16);
+    const uint32_t e = m >> 7;
+    // blocks next to either end of the range: the general form (all lanes of the warp work together in it)
+    if (__any_sync(0xffffffffu, e >= TOP_FIELD || (e < 32 && e > 0))) {
+        split8(raw, o1, o2, b1, b2);
+        return;
+    }
+    b1 = e == 0 ? 0 : e - 7;
+    b2 = e == 0 ? 0 : e - 12;
+    const float f1 = __uint_as_float((254 - min(b1, 253u)) << 23);
+    const __half2 up = __float2half2_rn(32.f);
+    uint32_t t1[4], t2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * f1, __uint_as_float(w[j] & 0xffff0000u) * f1);
+        uint16_t q;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(q) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
+        uint32_t d;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(q));
+        const __half2 rest = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&d)), up);
+        t1[j] = q;
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(q) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+        t2[j] = q;
+    }
+    o1 = make_uint2(__byte_perm(t1[0], t1[1], 0x5410), __byte_perm(t1[2], t1[3], 0x5410));
+    o2 = make_uint2(__byte_perm(t2[0], t2[1], 0x5410), __byte_perm(t2[2], t2[3], 0x5410));
+}
+
 // The two terms of the rows in sorted order, [2][M][pitch] bytes and their scales likewise; with k > 0 row i is row table[i] / k
-// of a, rows outside a are zero. A thread takes 8 values, four lanes a block; a CTA a run of the array's units.
-__global__ void __launch_bounds__(256)
-split_sorted_kernel(const __nv_bfloat16* __restrict__ a, const int* __restrict__ table, int k, int64_t a_rows, int M, int K, uint32_t per_row,
-                    uint32_t rows_a_cta, uint8_t* __restrict__ terms, uint8_t* __restrict__ scales, int scale_pitch) {
+// of a, rows outside a are zero. A warp takes a row at a time, a lane 8 values of it, four lanes a block.
+constexpr int SPLIT_WARPS = 8;
+__global__ void __launch_bounds__(32 * SPLIT_WARPS)
+split_sorted_kernel(const __nv_bfloat16* __restrict__ a, const int* __restrict__ table, int k, int64_t a_rows, int M, int K, int per_row,
+                    uint8_t* __restrict__ terms, uint8_t* __restrict__ scales, int scale_pitch) {
     grid_wait();
     grid_release();  // everything earlier is complete: the product may start on the weights
-    const int row0 = (int)(blockIdx.x * rows_a_cta);
-    const uint32_t units = min((int)rows_a_cta, M - row0) * per_row, most = (units + 31) & ~31u;
-    const int64_t total = (int64_t)M * per_row, at = (int64_t)row0 * per_row;
-    for (uint32_t i = threadIdx.x; i < most; i += 256) {  // whole warps: a block's lanes work together
-        const uint32_t r = i / per_row, g = i - r * per_row;
-        const int row = row0 + (int)r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < units) {
-            const int64_t from = k > 0 ? __ldg(table + row) / k : row;
-            if (from >= 0 && from < a_rows) v = row8(a + from * K, (int)g * 8, K, 1);
+    const int lane = threadIdx.x & 31;
+    for (int row = (int)blockIdx.x * SPLIT_WARPS + (threadIdx.x >> 5); row < M; row += gridDim.x * SPLIT_WARPS) {
+        int64_t from = row;
+        if (k > 0) from = __ldg(table + row) / k;
+        const bool in = from >= 0 && from < a_rows;
+        const __nv_bfloat16* x = a + (in ? from : 0) * K;
+        uint2* t1 = reinterpret_cast<uint2*>(terms) + (int64_t)row * per_row;
+        uint2* t2 = t1 + (int64_t)M * per_row;
+        uint8_t* s1 = scales + (int64_t)row * scale_pitch;
+        uint8_t* s2 = s1 + (int64_t)M * scale_pitch;
+#pragma unroll 2
+        for (int g0 = 0; g0 < per_row; g0 += 32) {
+            const int g = g0 + lane;
+            uint2 o1, o2;
+            uint32_t b1, b2;
+            split8_half(in && g * 8 < K ? __ldg(reinterpret_cast<const uint4*>(x) + g) : make_uint4(0, 0, 0, 0), o1, o2, b1, b2);  // K is a multiple of 8
+            if (g >= per_row) continue;
+            t1[g] = o1;
+            t2[g] = o2;
+            if ((g & 3) == 0) {
+                s1[g >> 2] = (uint8_t)b1;
+                s2[g >> 2] = (uint8_t)b2;
+            }
         }
-        uint2 o1, o2;
-        uint32_t b1, b2;
-        split8(v, o1, o2, b1, b2);
-        if (i >= units) continue;
-        reinterpret_cast<uint2*>(terms)[at + i] = o1;
-        reinterpret_cast<uint2*>(terms)[at + i + total] = o2;
-        if ((g & 3) == 0) {
-            uint8_t* s1 = scales + (int64_t)row * scale_pitch;
-            uint8_t* s2 = s1 + (int64_t)M * scale_pitch;
-            s1[g >> 2] = (uint8_t)b1;
-            s2[g >> 2] = (uint8_t)b2;
-            if (g + 4 == per_row)
-                for (int j = (int)(per_row >> 2); j < scale_pitch; ++j) s1[j] = s2[j] = 0;
-        }
+        for (int j = per_row / 4 + lane; j < scale_pitch; j += 32) s1[j] = s2[j] = 0;
     }
 }
 
@@ -463,13 +575,25 @@ bool map_weights(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, i
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// The terms [2][rows][pitch] in boxes of 128 bytes x 16 rows of both.
-bool map_terms(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch) {
+// Gate and up matrices of n experts as one tensor [n][rows / 16][2][16][K], the first of the two at `ptr` and the other `apart` bytes
+// on, in boxes of a tile: 16 rows of one, the 16 of the other, and so on. One copy a stage in place of eight; rows a multiple of 16.
+bool map_both(CUtensorMap* m, const void* ptr, int64_t apart, int64_t rows, int64_t pitch, int64_t n, int64_t stride) {
+    const MxEncodeFn fn = mx_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[5] = {(cuuint64_t)(2 * pitch), (cuuint64_t)PAIR, 2, (cuuint64_t)(rows / PAIR), (cuuint64_t)n};
+    cuuint64_t strides[4] = {(cuuint64_t)pitch, (cuuint64_t)apart, (cuuint64_t)(PAIR * pitch), (cuuint64_t)stride};
+    cuuint32_t box[5] = {128, PAIR, 2, TILE_P / 2 / PAIR, 1};
+    cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The terms [2][rows][pitch] in boxes of 128 bytes x box_rows of both.
+bool map_terms(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows) {
     const MxEncodeFn fn = mx_encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)rows, 2};
     cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(rows * pitch)};
-    cuuint32_t box[3] = {128, CHUNK, 2};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 2};
     cuuint32_t one[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -507,10 +631,19 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     uint8_t* scales = terms + 2 * M * kp;
     p.dual = d.epi == EPI_SWIGLU;
     p.epi = d.epi;
-    const int box = p.dual ? PAIR : TILE_P;
-    if (!map_weights(&p.map_p, d.b_codes, d.N, mx_code_pitch(d.K), d.n_groups, d.code_stride, box) ||
-        (p.dual && !map_weights(&p.map_p2, d.b2_codes, d.N, mx_code_pitch(d.K), d.n_groups, d.code_stride, box)) ||
-        !map_terms(&p.map_q, terms, M, kp))
+    const int64_t pitch = mx_code_pitch(d.K);
+    const int64_t apart = static_cast<const uint8_t*>(d.b2_codes) - static_cast<const uint8_t*>(d.b_codes);
+    p.both = p.dual && d.N % PAIR == 0 && apart != 0 && std::abs(apart) < (1ll << 40);
+    p.up_first = p.both && apart < 0;
+    bool ok = true;
+    if (p.both) {
+        ok = map_both(&p.map_p, p.up_first ? d.b2_codes : d.b_codes, std::abs(apart), d.N, pitch, d.n_groups, d.code_stride);
+    } else {
+        ok = map_weights(&p.map_p, d.b_codes, d.N, pitch, d.n_groups, d.code_stride, p.dual ? PAIR : TILE_P) &&
+             (!p.dual || map_weights(&p.map_p2, d.b2_codes, d.N, pitch, d.n_groups, d.code_stride, PAIR));
+    }
+    for (int i = 0; i < BOXES; ++i) ok = ok && map_terms(&p.map_q[i], terms, M, kp, CHUNK << i);
+    if (!ok)
         return cudaErrorInvalidValue;
     p.scale_p = static_cast<const uint8_t*>(d.b_scales);
     p.scale_p2 = static_cast<const uint8_t*>(d.b2_scales);
@@ -528,12 +661,11 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     p.row_weight = d.row_weight;
     p.C = d.C;
     p.err = err;
-    const uint32_t per_row = (uint32_t)(kp / 8);
-    const uint32_t rows_a_cta = std::max<uint32_t>(1, 1024 / per_row);  // about 1024 units
-    const int64_t blocks = (M + rows_a_cta - 1) / rows_a_cta;
+    const int per_row = (int)(kp / 8);
+    const int64_t blocks = std::min<int64_t>((M + SPLIT_WARPS - 1) / SPLIT_WARPS, 8ll * gemm_num_sms());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(32 * SPLIT_WARPS);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -541,7 +673,7 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, split_sorted_kernel, static_cast<const __nv_bfloat16*>(d.A), d.gather_k > 0 ? d.row_table : nullptr,
-                                             d.gather_k, d.a_rows, d.M, d.K, per_row, rows_a_cta, terms, scales, p.scale_pitch);
+                                             d.gather_k, d.a_rows, d.M, d.K, per_row, terms, scales, p.scale_pitch);
     if (e != cudaSuccess) return e;
     // rows of a tile at most: groups of 32 rows and fewer are bound by the weights' bytes and want more stages of them in flight
     const bool small = M <= 32ll * d.n_groups;
