@@ -6,6 +6,10 @@
 // are as many as its group needs (multiples of 32: 16 rows, two terms), so a group of three rows costs 32 columns and one of 300 three
 // tiles of 112 and less. A gate/up tile takes 64 gate rows and their 64 up rows.
 //
+// Large groups are bound by an SM's shared memory, about 133 bytes a clock of loads coming in and operands going out: a stage of 192
+// columns is 41 KB in and 40 KB out, 609 clocks for 384 of products. There a pair of CTAs shares a tile of 256 weight rows
+// (cta_group::2): each SM loads 128 rows of weights and one of the terms, 28 KB in and 28 KB out.
+//
 // split_sorted_kernel writes the terms in sorted order (gathering the rows by the routing's table where asked). Then one persistent
 // CTA an SM: warp 0 loads by TMA, warp 1 copies the scales to TMEM and issues the products, four warps at a time take turns at
 // bringing the block scales, four write the results while the next tile is computed (two accumulators).
@@ -30,19 +34,21 @@ constexpr int TEAM = 4, EPI_WARPS = 8;
 constexpr int PAIR = 16;                     // gate/up tiles: rows of one matrix side by side
 constexpr int MAX_G = GROUPED_MX_MAX_GROUPS;
 
-// MAXC: chunks of a tile at most.
-template <int MAXC>
+// MAXC: chunks of a tile at most. TWO: tiles of a pair of CTAs, the first of which holds the first terms and the second the second
+// ones, and issues the products.
+template <int MAXC, bool TWO>
 struct Cfg {
     static constexpr int BQ = 32 * MAXC;                       // columns
     static constexpr int PARTS = (BQ + 127) / 128;             // 128-row parts of the right operand's scales
-    static constexpr int Q_BYTES = MAXC * CHUNK_BYTES;
+    static constexpr int Q_BYTES = MAXC * CHUNK_BYTES / (TWO ? 2 : 1);
     static constexpr int SCALE_BYTES = (1 + PARTS) * 512;
     static constexpr int STAGE = (P_BYTES + Q_BYTES + SCALE_BYTES + 1023) / 1024 * 1024;
     static constexpr int OWN_ROWS = (MAXC + 1) / 2 * CHUNK;    // rows of an epilogue warp
     static constexpr int FIT = (232448 - 1024 - 1024 - 20 * (MAX_G + 1) - 8 * EPI_WARPS * OWN_ROWS) / STAGE;
-    static constexpr int STAGES = FIT < 8 ? FIT / 2 * 2 : 8;
-    static constexpr int TEAMS = 2, RUN = STAGES >= 5 ? 4 : 2; // scale warps: teams take turns of RUN stages
     static constexpr int SCALE_COLS = 4 * (1 + PARTS);
+    static constexpr int FIT2 = (512 - 2 * BQ) / SCALE_COLS < FIT ? (512 - 2 * BQ) / SCALE_COLS : FIT;
+    static constexpr int STAGES = FIT2 < 8 ? FIT2 : 8;
+    static constexpr int TEAMS = 2, RUN = 4;                   // scale warps: teams take turns of RUN stages
     static constexpr int SMEM = STAGES * STAGE + 1024 + 512;
     static constexpr int FIRST_EPI = 2 + TEAM * TEAMS, THREADS = 32 * (FIRST_EPI + EPI_WARPS);
     static constexpr int TMEM_COLS = 512;
@@ -99,6 +105,32 @@ __device__ __forceinline__ int row_of(int chunks, int c, int& term) {
     return c - first - (term ? CHUNK : 0);
 }
 
+template <bool TWO>
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+    if (TWO) tc::tma_3d_pair(dst, m, bar, x, y, z);
+    else tc::tma_3d(dst, m, bar, x, y, z);
+}
+template <bool TWO>
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w, int v) {
+    if (TWO) tc::tma_5d_pair(dst, m, bar, x, y, z, w, v);
+    else tc::tma_5d(dst, m, bar, x, y, z, w, v);
+}
+template <bool TWO>
+__device__ __forceinline__ void scales_to_tmem(uint32_t t, uint64_t desc) {
+    if (TWO) scale_copy_pair(t, desc);
+    else scale_copy(t, desc);
+}
+template <bool TWO>
+__device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add) {
+    if (TWO) mma_mxf8_pair(d, a, b, idesc, sa, sb, add);
+    else mma_mxf8(d, a, b, idesc, sa, sb, add);
+}
+template <bool TWO>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (TWO) mma_commit_pair(bar);
+    else mma_commit(bar);
+}
+
 // What the CTAs keep of the groups in shared memory.
 struct Groups {
     int first[MAX_G + 1];   // row tiles before each group
@@ -114,15 +146,24 @@ struct Tiles {
     const Groups& s;
     int t, n, mt, g;                // tile, weight tile, row tile, group
     int step_n, step_mt;
-    int p0, row, rows, chunks;      // first output column, first sorted row, rows, chunks of 16
-    __device__ __forceinline__ Tiles(const GroupedParams& p, const Groups& groups) : s(groups), t((int)blockIdx.x), g(0) {
-        step_mt = (int)gridDim.x / p.tiles_p;
-        step_n = (int)gridDim.x - step_mt * p.tiles_p;
+    int p0, row, rows, chunks;      // this CTA's first output column, first sorted row, rows, chunks of 16
+    int step, columns, own;         // output columns of a tile, and where in it this CTA's begin
+    __device__ __forceinline__ Tiles(const GroupedParams& p, const Groups& groups, bool two) : s(groups), t((int)blockIdx.x), g(0), step((int)gridDim.x) {
+        columns = p.dual ? TILE_P / 2 : TILE_P;
+        own = 0;
+        if (two) {
+            t >>= 1;
+            step >>= 1;
+            own = (int)cluster_rank() * columns;
+            columns *= 2;
+        }
+        step_mt = step / p.tiles_p;
+        step_n = step - step_mt * p.tiles_p;
         mt = t / p.tiles_p;
         n = t - mt * p.tiles_p;
     }
     __device__ __forceinline__ void next(const GroupedParams& p) {
-        t += gridDim.x;
+        t += step;
         mt += step_mt;
         n += step_n;
         if (n >= p.tiles_p) {
@@ -139,7 +180,7 @@ struct Tiles {
             else hi = mid - 1;
         }
         const int q = mt - s.first[g], more = s.more[g];
-        p0 = n * (p.dual ? TILE_P / 2 : TILE_P);
+        p0 = n * columns + own;
         chunks = s.share[g] + (q < more ? 1 : 0);
         row = s.row[g] + (q * s.share[g] + min(q, more)) * CHUNK;
         rows = min(s.end[g] - row, chunks * CHUNK);
@@ -147,18 +188,12 @@ struct Tiles {
 };
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ uint32_t word_of(const uint2& v, int i) { return i == 0 ? v.x : v.y; }
 __device__ __forceinline__ void words(const uint8_t* p, bool in, uint4& v) { v = in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void words(const uint8_t* p, bool in, uint2& v) { v = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0); }
 __device__ __forceinline__ void words_now(const uint8_t* p, bool in, uint4& v) { v = in ? __ldcg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void words_now(const uint8_t* p, bool in, uint2& v) { v = in ? __ldcg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0); }
-template <int RUN> struct Words;
-template <> struct Words<4> { typedef uint4 type; };
-template <> struct Words<2> { typedef uint2 type; };
 
-template <int MAXC>
-__global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(const __grid_constant__ GroupedParams p) {
-    using C = Cfg<MAXC>;
+template <int MAXC, bool TWO>
+__global__ void __launch_bounds__(Cfg<MAXC, TWO>::THREADS, 1) gemm_grouped_mx_kernel(const __grid_constant__ GroupedParams p) {
+    using C = Cfg<MAXC, TWO>;
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -180,12 +215,12 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
     if (threadIdx.x == 0) {
         stop = 0;
         for (int s = 0; s < S; ++s) {
-            bar_init(full(s), 1 + TEAM);  // the TMA thread and a team of scale warps
+            bar_init(full(s), 1 + (TWO ? 2 : 1) * TEAM);  // the (first CTA's) TMA thread and a team of scale warps (of each CTA)
             bar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(acc_full(b), 1);
-            bar_init(acc_empty(b), EPI_WARPS);
+            bar_init(acc_empty(b), (TWO ? 2 : 1) * EPI_WARPS);
         }
         bar_init(done, 1);
         bar_init_fence();
@@ -193,7 +228,10 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         for (int i = 0; i < BOXES; ++i) tma_desc_prefetch(&p.map_q[i]);
         if (p.dual && !p.both) tma_desc_prefetch(&p.map_p2);
     }
-    if (warp == 1) tmem_get(smem_addr(tmem_slot), C::TMEM_COLS);
+    if (warp == 1) {
+        if (TWO) tmem_get_pair(smem_addr(tmem_slot), C::TMEM_COLS);
+        else tmem_get(smem_addr(tmem_slot), C::TMEM_COLS);
+    }
     // The kernel before this one, which splits the rows, began after everything earlier was complete: only the split rows have
     // to be waited for.
     if (warp == 2) {
@@ -222,8 +260,11 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
     }
     fence_before_sync();
     __syncthreads();
+    if (TWO) cluster_barrier();  // both CTAs' barriers are set up, both have their TMEM
     fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    const int rank = TWO ? (int)cluster_rank() : 0;
+    const uint32_t full_at = TWO ? cluster_addr(full(0), 0) : full(0);  // the first CTA's
     const int stages = p.k_stages, tiles = groups.first[p.n_groups] * p.tiles_p;
 
     if (warp == 0) {
@@ -232,22 +273,22 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         int s = 0, it = 0;
         uint32_t phase = 1;  // a new barrier's preceding phase counts as complete
         bool ok = true, waited = false;
-        for (Tiles tl(p, groups); ok && tl.t < tiles; tl.next(p)) {
+        for (Tiles tl(p, groups, TWO); ok && tl.t < tiles; tl.next(p)) {
             tl.find(p);
             // an unpacking copy counts the packed bytes (it leaves every second 8 bytes alone)
-            const uint32_t bytes = P_BYTES / 2 + tl.chunks * CHUNK_BYTES;
+            const uint32_t bytes = TWO ? 2 * (P_BYTES / 2 + tl.chunks * (CHUNK_BYTES / 2)) : P_BYTES / 2 + tl.chunks * CHUNK_BYTES;
             auto weights = [&](int st, int k) {
-                const uint32_t at = base + st * C::STAGE;
-                bar_expect(full(st), bytes);
+                const uint32_t at = base + st * C::STAGE, bar = full_at + 8 * st;
+                if (rank == 0) bar_expect(full(st), bytes);
                 if (p.both) {
-                    tma_5d(at, &p.map_p, full(st), k * 128, 0, 0, tl.p0 / PAIR, tl.g);
+                    tma_5d<TWO>(at, &p.map_p, bar, k * 128, 0, 0, tl.p0 / PAIR, tl.g);
                 } else if (p.dual) {
                     for (int i = 0; i < TILE_P / 2; i += PAIR) {
-                        tma_3d(at + 2 * i * 128, &p.map_p, full(st), k * 128, tl.p0 + i, tl.g);
-                        tma_3d(at + (2 * i + PAIR) * 128, &p.map_p2, full(st), k * 128, tl.p0 + i, tl.g);
+                        tma_3d<TWO>(at + 2 * i * 128, &p.map_p, bar, k * 128, tl.p0 + i, tl.g);
+                        tma_3d<TWO>(at + (2 * i + PAIR) * 128, &p.map_p2, bar, k * 128, tl.p0 + i, tl.g);
                     }
                 } else {
-                    tma_3d(at, &p.map_p, full(st), k * 128, tl.p0, tl.g);
+                    tma_3d<TWO>(at, &p.map_p, bar, k * 128, tl.p0, tl.g);
                 }
             };
             auto rows = [&](int st, int k) {
@@ -256,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
 #pragma unroll
                 for (int i = BOXES - 1; i >= 0; --i)
                     if (tl.chunks >> i & 1) {
-                        tma_3d(at + c * CHUNK_BYTES, &p.map_q[i], full(st), k * 128, tl.row + c * CHUNK, 0);
+                        tma_3d<TWO>(at + c * (TWO ? CHUNK_BYTES / 2 : CHUNK_BYTES), &p.map_q[i], full_at + 8 * st, k * 128, tl.row + c * CHUNK, rank);
                         c += 1 << i;
                     }
             };
@@ -293,8 +334,8 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         }
         if (!waited) grid_wait();
         grid_release();
-        // an aborted CTA waits for its own copies before it exits
-        if (stop)
+        // an aborted CTA (of a pair the first, at whose barriers both CTAs' copies count) waits for its copies before it exits
+        if (stop && rank == 0)
             for (int i = 0; i < S && i < it; ++i) {
                 const int last = it - 1 - (it - 1 - i) % S;
                 bar_wait(full(i), (uint32_t)(last / S) & 1u, p.err, 5);
@@ -303,10 +344,10 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         // ------------------------------------------------------------ products
         const bool one = elect_one();
         int n = 0, it = 0;
-        bool ok = true;
-        for (Tiles tl(p, groups); ok && tl.t < tiles; tl.next(p), ++n) {
+        bool ok = rank == 0;
+        for (Tiles tl(p, groups, TWO); ok && tl.t < tiles; tl.next(p), ++n) {
             tl.find(p);
-            const uint32_t idesc = mx_idesc(5, 0, TILE_P, 32 * tl.chunks);
+            const uint32_t idesc = mx_idesc(5, 0, TWO ? 2 * TILE_P : TILE_P, 32 * tl.chunks);
             const int b = n & 1, parts = (32 * tl.chunks + 127) / 128;
             if (!bar_wait_warp(acc_empty(b), (uint32_t)((n >> 1) + 1) & 1u, p.err, 2) || stop) {
                 stop = 1;
@@ -316,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             const uint32_t d = tmem + (uint32_t)(b * C::BQ);
             for (int k = 0; k < stages; ++k, ++it) {
                 const int s = it % S;
-                if (!bar_wait_warp(full(s), (uint32_t)(it / S) & 1u, p.err, 3)) {
+                if (!(TWO ? bar_wait_cluster(full(s), (uint32_t)(it / S) & 1u, p.err, 3) : bar_wait_warp(full(s), (uint32_t)(it / S) & 1u, p.err, 3))) {
                     ok = false;
                     stop = 1;
                     break;
@@ -325,31 +366,33 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
                 const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
                 const uint32_t tp = tmem + (uint32_t)(2 * C::BQ + s * C::SCALE_COLS), tq = tp + 4;
                 if (one) {
-                    scale_copy(tp, scale_desc(sc));
+                    scales_to_tmem<TWO>(tp, scale_desc(sc));
 #pragma unroll
                     for (int j = 0; j < C::PARTS; ++j)
-                        if (j < parts) scale_copy(tq + 4 * j, scale_desc(sc + 512 * (1 + j)));
+                        if (j < parts) scales_to_tmem<TWO>(tq + 4 * j, scale_desc(sc + 512 * (1 + j)));
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // 32 bytes of each row
-                        mma_mxf8(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc_at(idesc, j), tp, tq, (k | j) ? 1u : 0u);
-                    mma_commit(empty(s));
+                        product<TWO>(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc_at(idesc, j), tp, tq, (k | j) ? 1u : 0u);
+                    commit<TWO>(empty(s));
                 }
                 __syncwarp();
             }
-            if (ok && one) mma_commit(acc_full(b));
+            if (ok && one) commit<TWO>(acc_full(b));
             __syncwarp();
         }
-        if (one) mma_commit(done);
-        __syncwarp();
-        bar_wait(done, 0, p.err, 6);
+        if (rank == 0) {
+            if (one) commit<TWO>(done);
+            __syncwarp();
+            bar_wait(done, 0, p.err, 6);
+        }
     } else if (warp < C::FIRST_EPI) {
         // ------------------------------------------------------------ scales
         // Warp w of a team has rows 32 w + lane of each 128; the words of four such rows lie side by side at 16 lane in the order
         // that the tensor core reads. A row's words for RUN stages are loaded together, while the stages before are at hand.
         constexpr int RUN = C::RUN, NR = 1 + C::PARTS;
-        typedef typename Words<RUN>::type V;
+        typedef uint4 V;
         const int team = (warp - 2) / TEAM, w = (warp - 2) % TEAM, runs = (stages + RUN - 1) / RUN;
-        Tiles tl(p, groups);   // of the turn to request next
+        Tiles tl(p, groups, TWO);   // of the turn to request next
         int run = 0, at_stage = 0;                    // that turn of its tile, the tile's first stage in the ring's line
         int now_run, now_at;                          // the turn at hand
         bool now_on;
@@ -367,8 +410,8 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             words((second ? p.scale_p2 : p.scale_p) + tl.g * p.scale_stride + (int64_t)row * p.scale_pitch + at, row < p.N, to[0]);
 #pragma unroll
             for (int j = 0; j < C::PARTS; ++j) {
-                int term;
-                const int i = row_of(tl.chunks, 128 * j + r, term);
+                int term = 128 * j + r >= CHUNK * tl.chunks;
+                const int i = TWO ? 128 * j + r - (term ? CHUNK * tl.chunks : 0) : row_of(tl.chunks, 128 * j + r, term);
                 const int64_t src = (int64_t)term * p.M + tl.row + i;
                 words_now(p.scale_q + src * p.scale_pitch + at, 128 * j + r < 32 * tl.chunks && i < tl.rows, to[1 + j]);
             }
@@ -397,7 +440,10 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
                 for (int j = 0; j < NR; ++j) st_shared1(to + 512 * j, word_of(v[0][j], i));
                 fence_smem_async();
                 __syncwarp();
-                if (lane == 0) bar_arrive(full(s));
+                if (lane == 0) {
+                    if (rank == 0) bar_arrive(full(s));
+                    else bar_arrive_cluster(full_at + 8 * s);
+                }
             }
 #pragma unroll
             for (int j = 0; j < NR; ++j) v[0][j] = v[1][j];
@@ -413,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
         int* const to = s_to[warp - C::FIRST_EPI];        // places and weights of this warp's rows
         float* const w = s_weight[warp - C::FIRST_EPI];
         int n = 0;
-        for (Tiles tl(p, groups); tl.t < tiles; tl.next(p), ++n) {
+        for (Tiles tl(p, groups, TWO); tl.t < tiles; tl.next(p), ++n) {
             tl.find(p);
             const int b = n & 1;
             if (p.epi == EPI_SCALE_F32) {  // read while the products run; the warp's chunks are every second one
@@ -438,8 +484,8 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
 #pragma unroll 1
             for (int i0 = half * CHUNK, l0 = 0; i0 < tl.rows; i0 += 2 * CHUNK, l0 += CHUNK) {
                 uint32_t x[CHUNK], y[CHUNK];
-                int apart;
-                const uint32_t c = at + (uint32_t)column(tl.chunks, i0, apart);
+                int apart = CHUNK * tl.chunks;
+                const uint32_t c = at + (uint32_t)(TWO ? i0 : column(tl.chunks, i0, apart));
                 tmem_load16(c, x);
                 tmem_load16(c + apart, y);
                 tmem_load_wait();
@@ -479,14 +525,20 @@ __global__ void __launch_bounds__(Cfg<MAXC>::THREADS, 1) gemm_grouped_mx_kernel(
             }
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) bar_arrive(acc_empty(b));
+            if (lane == 0) {
+                if (TWO) bar_arrive_cluster(cluster_addr(acc_empty(b), 0));
+                else bar_arrive(acc_empty(b));
+            }
         }
     }
     fence_before_sync();
-    __syncthreads();
+    __syncwarp();
+    if (TWO) cluster_barrier();  // neither CTA's memory goes while the other's copies, products or arrivals may reach it
+    else __syncthreads();
     if (warp == 1) {
         fence_after_sync();
-        tmem_free(tmem, C::TMEM_COLS);
+        if (TWO) tmem_free_pair(tmem, C::TMEM_COLS);
+        else tmem_free(tmem, C::TMEM_COLS);
     }
 }
 
@@ -587,35 +639,39 @@ bool map_both(CUtensorMap* m, const void* ptr, int64_t apart, int64_t rows, int6
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// The terms [2][rows][pitch] in boxes of 128 bytes x box_rows of both.
-bool map_terms(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows) {
+// The terms [2][rows][pitch] in boxes of 128 bytes x box_rows, of both or of one.
+bool map_terms(CUtensorMap* m, const void* ptr, int64_t rows, int64_t pitch, int box_rows, int box_terms) {
     const MxEncodeFn fn = mx_encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)rows, 2};
     cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(rows * pitch)};
-    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 2};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, (cuuint32_t)box_terms};
     cuuint32_t one[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MAXC>
+template <int MAXC, bool TWO>
 cudaError_t launch(const GroupedParams& p, int64_t most_tiles, cudaStream_t s) {
-    auto kern = gemm_grouped_mx_kernel<MAXC>;
-    using C = Cfg<MAXC>;
+    auto kern = gemm_grouped_mx_kernel<MAXC, TWO>;
+    using C = Cfg<MAXC, TWO>;
     static SmemAllowance allowed;
     const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(most_tiles, gemm_num_sms()));
+    cfg.gridDim = dim3(TWO ? 2 * (unsigned)std::min<int64_t>(most_tiles, std::max(1, gemm_num_sms() / 2)) : (unsigned)std::min<int64_t>(most_tiles, gemm_num_sms()));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = TWO ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -633,6 +689,8 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     p.epi = d.epi;
     const int64_t pitch = mx_code_pitch(d.K);
     const int64_t apart = static_cast<const uint8_t*>(d.b2_codes) - static_cast<const uint8_t*>(d.b_codes);
+    // rows of a tile at most: groups of 32 rows and fewer are bound by the weights' bytes and want more stages of them in flight
+    const bool two = M > 32ll * d.n_groups;
     p.both = p.dual && d.N % PAIR == 0 && apart != 0 && std::abs(apart) < (1ll << 40);
     p.up_first = p.both && apart < 0;
     bool ok = true;
@@ -642,7 +700,7 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
         ok = map_weights(&p.map_p, d.b_codes, d.N, pitch, d.n_groups, d.code_stride, p.dual ? PAIR : TILE_P) &&
              (!p.dual || map_weights(&p.map_p2, d.b2_codes, d.N, pitch, d.n_groups, d.code_stride, PAIR));
     }
-    for (int i = 0; i < BOXES; ++i) ok = ok && map_terms(&p.map_q[i], terms, M, kp, CHUNK << i);
+    for (int i = 0; i < BOXES; ++i) ok = ok && map_terms(&p.map_q[i], terms, M, kp, CHUNK << i, two ? 1 : 2);
     if (!ok)
         return cudaErrorInvalidValue;
     p.scale_p = static_cast<const uint8_t*>(d.b_scales);
@@ -655,7 +713,7 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     p.M = d.M;
     p.N = d.N;
     p.k_stages = (int)(kp / 128);
-    const int rows = p.dual ? TILE_P / 2 : TILE_P;
+    const int rows = (p.dual ? TILE_P / 2 : TILE_P) * (two ? 2 : 1);
     p.tiles_p = (d.N + rows - 1) / rows;
     p.row_table = d.row_table;
     p.row_weight = d.row_weight;
@@ -675,12 +733,10 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     const cudaError_t e = cudaLaunchKernelEx(&cfg, split_sorted_kernel, static_cast<const __nv_bfloat16*>(d.A), d.gather_k > 0 ? d.row_table : nullptr,
                                              d.gather_k, d.a_rows, d.M, d.K, per_row, terms, scales, p.scale_pitch);
     if (e != cudaSuccess) return e;
-    // rows of a tile at most: groups of 32 rows and fewer are bound by the weights' bytes and want more stages of them in flight
-    const bool small = M <= 32ll * d.n_groups;
-    const int most = CHUNK * (small ? 2 : 7);
+    const int most = CHUNK * (two ? 7 : 2);
     const int64_t tiles = (M / most + std::min<int64_t>(d.n_groups, M)) * p.tiles_p;  // a group has at most one tile that is not full
     if (tiles > 0x3fffffffll) return cudaErrorInvalidValue;
-    return small ? launch<2>(p, tiles, s) : launch<7>(p, tiles, s);
+    return two ? launch<7, true>(p, tiles, s) : launch<2, false>(p, tiles, s);
 }
 
 }  // namespace ls
