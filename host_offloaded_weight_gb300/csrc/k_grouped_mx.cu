@@ -542,6 +542,12 @@ __global__ void __launch_bounds__(Cfg<MAXC, TWO>::THREADS, 1) gemm_grouped_mx_ke
     }
 }
 
+// The row of A that an entry of the table stands for; -1: none.
+__device__ __forceinline__ int64_t source_row(int entry, int k, int64_t rows) {
+    const int r = entry < 0 ? -1 : entry / k;
+    return r < rows ? r : -1;
+}
+
 // split8 of tc.cuh, with the scaled values and what the first term leaves as f16 pairs: both are exact there, down to 2^-24 of
 // values below 2^8, far under what the second term can hold. (All in fp32: half as many instructions again.)
 __device__ __forceinline__ void split8_half(uint4 raw, uint2& o1, uint2& o2, uint32_t& b1, uint32_t& b2) {
@@ -587,9 +593,8 @@ split_sorted_kernel(const __nv_bfloat16* __restrict__ a, const int* __restrict__
     grid_release();  // everything earlier is complete: the product may start on the weights
     const int lane = threadIdx.x & 31;
     for (int row = (int)blockIdx.x * SPLIT_WARPS + (threadIdx.x >> 5); row < M; row += gridDim.x * SPLIT_WARPS) {
-        int64_t from = row;
-        if (k > 0) from = __ldg(table + row) / k;
-        const bool in = from >= 0 && from < a_rows;
+        const int64_t from = k > 0 ? source_row(__ldg(table + row), k, a_rows) : row < a_rows ? row : -1;
+        const bool in = from >= 0;
         const __nv_bfloat16* x = a + (in ? from : 0) * K;
         uint2* t1 = reinterpret_cast<uint2*>(terms) + (int64_t)row * per_row;
         uint2* t2 = t1 + (int64_t)M * per_row;
@@ -689,8 +694,9 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     p.epi = d.epi;
     const int64_t pitch = mx_code_pitch(d.K);
     const int64_t apart = static_cast<const uint8_t*>(d.b2_codes) - static_cast<const uint8_t*>(d.b_codes);
-    // rows of a tile at most: groups of 32 rows and fewer are bound by the weights' bytes and want more stages of them in flight
-    const bool two = M > 32ll * d.n_groups;
+    // Groups of a few rows are bound by the weights' bytes and want single CTAs with more stages in flight: 6 rows a group take
+    // 49 us that way and 52 in pairs (up, 128 experts of 2048 x 768), 16 rows 61 and 59, 32 rows 78 and 65.
+    const bool two = M > 12ll * d.n_groups;
     p.both = p.dual && d.N % PAIR == 0 && apart != 0 && std::abs(apart) < (1ll << 40);
     p.up_first = p.both && apart < 0;
     bool ok = true;
