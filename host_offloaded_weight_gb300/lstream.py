@@ -647,14 +647,14 @@ def _expert_rows(t, what: str):
 
 # The usual arguments (torch tensors of the right types, dense) are recognised in few steps, since a check of each by the
 # functions above would cost a one-token layer 2 us of its call; all others take those functions.
-_BF16 = _F32 = _U8 = None
+_BF16 = _F32 = _U8 = _INT32 = None
 
 
 def _bind_types():
-    global _BF16, _F32, _U8
+    global _BF16, _F32, _U8, _INT32
     torch = sys.modules.get("torch")
     if torch is not None:
-        _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+        _BF16, _F32, _U8, _INT32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
 def _conversion(values, ld, codes, scales, what: str):
@@ -810,7 +810,7 @@ def lsk_lora_adapters(down, up, up2=None, scale=None) -> LoraAdapters:
 def _ids(t, what: str, need: int):
     """Address of a dense int32 tensor of at least `need` values; raw addresses and None pass."""
     if getattr(t, "dtype", None) is not None:
-        if "int32" not in str(t.dtype) or "uint" in str(t.dtype):
+        if t.dtype is not _INT32 and ("int32" not in str(t.dtype) or "uint" in str(t.dtype)):
             raise TypeError(f"{what} has to be int32, not {t.dtype}")
         _dense(t, what)
         if t.numel() < need:
@@ -823,16 +823,29 @@ def lsk_gemm_lora_bf16(epilogue: int, A, B, adapters: LoraAdapters, ids, C_out, 
     """lsk_gemm_bf16 with the adapter ids[t] (int32 [M], none where it is not one of the adapters') beside row t's product."""
     if adapters.N != N or adapters.K != K or adapters.two != (epilogue == LSK_EPI_SWIGLU):
         raise ValueError("these adapters are for another projection")
+    try:
+        usual = (A.dtype is _BF16 and B.dtype is _BF16 and C_out.dtype is _BF16 and ids.dtype is _INT32 and A.is_contiguous()
+                 and B.is_contiguous() and C_out.is_contiguous() and ids.is_contiguous() and ids.numel() >= M)
+    except AttributeError:
+        usual = False
+    if usual:
+        a, b, i, c = A.data_ptr(), B.data_ptr(), ids.data_ptr(), C_out.data_ptr()
+    else:
+        _bind_types()
+        a, b, i, c = _values(A, 0, "A"), _values(B, 0, "B"), _ids(ids, "ids", M), _values(C_out, 0, "C_out")
     rows = b_rows if b_rows is not None else B.shape[0]
     rf32 = 0 if resid is None else _is_f32(resid)
     return _check(_lib.lsk_gemm_lora_bf16(
-        epilogue, _values(A, 0, "A"), _values(B, 0, "B"), rows, b2_row_off, adapters.ref, _ids(ids, "ids", M),
-        0 if bias is None else _values(bias, 0, "bias"), 0 if resid is None else _values(resid, rf32, "resid"), rf32,
-        _values(C_out, 0, "C_out"), 0 if C32 is None else _values(C32, 1, "C32"), M, N, K, _stream(stream)))
+        epilogue, a, b, rows, b2_row_off, adapters.ref, i, 0 if bias is None else _values(bias, 0, "bias"),
+        0 if resid is None else _values(resid, rf32, "resid"), rf32, c, 0 if C32 is None else _values(C32, 1, "C32"), M, N, K,
+        _stream(stream)))
 
 
 def _packed(codes, scales, what: str):
     """Stacked MXFP4 matrices' addresses and the bytes between them."""
+    if codes.dtype is _U8 and scales.dtype is _U8 and codes.is_contiguous() and scales.is_contiguous():
+        return codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0)
+    _bind_types()
     for t, name in ((codes, what + "_codes"), (scales, what + "_scales")):
         if t.itemsize != 1:
             raise TypeError(f"{name} has to be bytes, not {t.dtype}")
@@ -846,13 +859,25 @@ def lsk_gemm_grouped_bf16_mxfp4(epilogue: int, A, B_codes, B_scales, group_bound
     """Rows sorted by group through the groups' MXFP4 matrices: B_codes [n_groups, N, code pitch] and B_scales [n_groups, N, scale pitch]
     (LSK_EPI_SWIGLU: B2 likewise), A [rows, K] bf16, group_bounds [n_groups + 1] and row_table [M] int32, row_weight [M] float32,
     C_out [M, N] bf16, float32 for LSK_EPI_SCALE_F32; all but the groups dense. gather_k > 0: row i is A's row row_table[i] // gather_k."""
+    if B_codes.shape[0] < n_groups or (B2_codes is not None and B2_codes.shape[0] < n_groups):
+        raise ValueError(f"fewer matrices than {n_groups} groups")
     bc, bs, cs, ss = _packed(B_codes, B_scales, "B")
     b2c = b2s = 0
     if B2_codes is not None:
         b2c, b2s, c2, s2 = _packed(B2_codes, B2_scales, "B2")
         if (c2 != cs or s2 != ss) and n_groups > 1:
             raise ValueError("B and B2 need the same distance between groups")
+    f32 = epilogue == LSK_EPI_SCALE_F32
+    try:
+        usual = (A.dtype is _BF16 and C_out.dtype is (_F32 if f32 else _BF16) and group_bounds.dtype is _INT32 and A.is_contiguous()
+                 and C_out.is_contiguous() and group_bounds.is_contiguous() and group_bounds.numel() > n_groups)
+    except AttributeError:
+        usual = False
+    if usual:
+        a, g, c = A.data_ptr(), group_bounds.data_ptr(), C_out.data_ptr()
+    else:
+        _bind_types()
+        a, g, c = _values(A, 0, "A"), _ids(group_bounds, "group_bounds", n_groups + 1), _values(C_out, int(f32), "C_out")
     return _check(_lib.lsk_gemm_grouped_bf16_mxfp4(
-        epilogue, _values(A, 0, "A"), A.shape[0], bc, bs, b2c, b2s, cs, ss, _ids(group_bounds, "group_bounds", n_groups + 1), n_groups,
-        0 if row_table is None else _ids(row_table, "row_table", M), 0 if row_weight is None else _values(row_weight, 1, "row_weight"),
-        gather_k, _values(C_out, int(epilogue == LSK_EPI_SCALE_F32), "C_out"), M, N, K, _stream(stream)))
+        epilogue, a, A.shape[0], bc, bs, b2c, b2s, cs, ss, g, n_groups, 0 if row_table is None else _ids(row_table, "row_table", M),
+        0 if row_weight is None else _values(row_weight, 1, "row_weight"), gather_k, c, M, N, K, _stream(stream)))

@@ -255,3 +255,73 @@ def test_no_rows_and_refusals():
         with pytest.raises(L.LsError):
             L.lsk_gemm_grouped_bf16_mxfp4(a["epi"], c.A, c.codes[0], c.scales[0], c.bounds, 1, c.out, 4, a["N"], a["K"], row_table=c.table,
                                           gather_k=a["gather_k"])
+
+
+@pytest.mark.parametrize("sizes", [[3, 2], [90, 7]])
+def test_entries_of_the_table_that_are_no_row_count_as_zero(sizes):
+    c = Case(sizes, 72, 128, "store", gather_k=4)
+    c.table[1], c.table[4] = -1, 4 * c.A.shape[0]
+    c.run()
+    torch.cuda.synchronize()
+    zero = (c.out[:-1] == 0).all(1)
+    assert zero[1] and zero[4] and int(zero.sum()) == 2
+
+
+@pytest.mark.parametrize("sizes", [[3, 0, 9], [130, 0, 250]])
+@pytest.mark.parametrize("first", ["gate", "up"])
+def test_gate_and_up_in_one_buffer_in_either_order(sizes, first):
+    """Gate and up rows are read through one map where they can be: whichever lies first, and as one expert-major blob."""
+    c = Case(sizes, 128, 256, "swiglu")
+    c.run()
+    torch.cuda.synchronize()
+    want = c.out.clone()
+    E, order = len(sizes), (0, 1) if first == "gate" else (1, 0)
+    for kind in ("codes", "scales"):
+        t = getattr(c, kind)
+        blob = torch.stack([t[i] for i in order], 1).contiguous()          # [E, 2, N, pitch]
+        setattr(c, kind, [blob[:, order.index(i)] for i in (0, 1)])
+    c.out.fill_(77.0)
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, want)
+
+
+def test_calls_in_a_chain_overlap_without_harm():
+    """Up, down and the next layer's up in a row, each started while the one before runs."""
+    sizes, H, F = [40, 0, 9, 200, 64], 256, 384
+    M = sum(sizes)
+    up, down = Case(sizes, F, H, "swiglu", gather_k=1), Case(sizes, H, F, "scale")
+    down.table, down.A = up.table, up.out[:M]
+    want = []
+    for times in (1, 25):
+        for _ in range(times):
+            up.run()
+            if times == 1:
+                torch.cuda.synchronize()
+            down.run()
+            if times == 1:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        want.append((up.out.clone(), down.out.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*want))
+
+
+def test_captured_twice_and_replayed_in_turn():
+    c = Case([5, 70, 0, 12], 264, 520, "scale")
+    c.run()
+    torch.cuda.synchronize()
+    want = c.out.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c.run(stream=s)
+            c.run(stream=s)
+        graphs.append(g)
+    for i in range(6):
+        c.out.fill_(77.0)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, want)

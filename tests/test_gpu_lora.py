@@ -211,3 +211,61 @@ def test_calls_in_flight_on_streams_and_again_the_same_bits(T):
 def test_no_rows():
     c = Case(4, 64, 64, 8, 2)
     assert L.lsk_gemm_lora_bf16(L.LSK_EPI_STORE, c.x, c.w, L.lsk_lora_adapters(c.down, c.up), c.ids, c.out, 0, 64, 64) == L.LS_OK
+
+
+@pytest.mark.parametrize("T,K,r", [(3, 6400, 16), (5, 8000, 16), (2, 11000, 16), (20, 13824, 32), (70, 8192, 64), (100, 4104, 256), (150, 13824, 16), (260, 9000, 128)])
+def test_long_rows_shared_by_clusters_of_every_size(T, K, r):
+    Case(T, 256, K, r, 3, "swiglu", seed=3).run().check()
+
+
+@pytest.mark.parametrize("T", [30, 200])
+def test_many_adapters(T):
+    """More than the numbers that the notes on adapters tell apart; two in use share one, and one of them is not finite."""
+    n, ids = 5000, [[7, 7 + 4096, 4999, 0, 2500][i % 5] for i in range(T)]
+    c = Case(T, 64, 64, 8, n, "store", ids=ids).run()
+    c.check()
+    before = c.out.clone()
+    c.up[7 + 4096, 3, 2] = float("inf")
+    c.run()
+    torch.cuda.synchronize()
+    own = torch.zeros(T + 1, dtype=torch.bool, device="cuda")
+    own[:T] = c.ids == 7 + 4096
+    assert torch.equal(c.out[~own], before[~own]) and not bool(torch.isfinite(c.out[own]).all(1).any())
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_the_residual_stream_in_place(T):
+    """C32 over the residual that it takes: every element is read before it is written."""
+    c = Case(T, 512, 256, 16, 4, "resid")
+    c.run()
+    torch.cuda.synchronize()
+    first = c.out.clone(), c.out32.clone()
+    both = torch.empty((T + 1, 512), device="cuda")
+    both[:T], both[T] = c.resid, 77.0
+    c.resid, c.out32 = both[:T], both
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, first[0]) and torch.equal(c.out32, first[1])
+
+
+def test_behind_and_before_other_products_of_the_library():
+    """The product starts while the kernel before it runs: calls in a chain, each on what the one before wrote."""
+    T, H, F = 48, 512, 1024
+    up, down = Case(T, F, H, 16, 4, "gelu"), Case(T, H, F, 16, 4, "resid", resid_f32=False)
+    down.ids, down.x, down.resid = up.ids, up.out[:T], up.x
+    want = []
+    for overlapped in (False, True):
+        up.out.fill_(0)
+        for _ in range(1 if not overlapped else 30):
+            up.run()
+            if not overlapped:
+                torch.cuda.synchronize()
+            down.run()
+            if not overlapped:
+                torch.cuda.synchronize()
+            L.lsk_gemm_bf16(L.LSK_EPI_BIAS_GELU, up.x, up.w, up.out, T, F, H, bias=up.bias)   # over the rows that were just read
+            if not overlapped:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        want.append((down.out.clone(), down.out32.clone(), up.out.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*want))
