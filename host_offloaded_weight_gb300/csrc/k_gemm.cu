@@ -90,13 +90,13 @@ struct GemmParams {
 };
 
 // A product with low-rank adapters beside it (see k_gemm_lora.cu): after its k-blocks a tile takes, for each adapter with
-// a row in it, blocks of h [256 rows, cw] (two terms, one after the other) with the cw columns of the adapter's `up`.
+// a row in it, blocks of h [256 rows, cw] (its terms, one after the other) with the cw columns of the adapter's `up`.
 struct LoraGemmParams : GemmParams {
     CUtensorMap tmH, tmUp, tmUp2;
     const int* lora_count;   // [row tile] adapters
     const int* lora_list;    // [row tile][lora_cap] which
-    const uint8_t* lora_notes;  // [adapter][16] not all zero: not finite, read as zeros (its third term of h is NaN)
-    int lora_cap, lora_cw, lora_chunks, lora_parts, lora_rank;
+    const uint8_t* lora_notes;  // [adapter][16] not all zero: not finite, read as zeros (its last term of h is NaN)
+    int lora_cap, lora_cw, lora_chunks, lora_parts, lora_rank, lora_terms;
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -938,7 +938,8 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                             const uint4 v = *reinterpret_cast<const uint4*>(p.lora_notes + 16ll * next[i]);
                             if (v.x | v.y | v.z | v.w) next[i] = -1 - next[i];
                         }
-                        const int end = min(8, count - j0) * p.lora_parts * 2;
+                        const int end = min(8, count - j0) * p.lora_parts * p.lora_terms;
+                        int term = 0, part = 0, i = 0;
                         for (int e = 0; e < end; ++e, ++it) {
                             const int s = it % S2_STAGES;
                             if (!mbar_wait(empty_bar(s), ((uint32_t)(it / S2_STAGES) & 1u) ^ 1u, p.err, 1, p.mbar_limit_ns)) {
@@ -946,7 +947,7 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                                 s_abort = 1;
                                 break;
                             }
-                            const int part = (e >> 1) % p.lora_parts, i = (e >> 1) / p.lora_parts, half = part / p.lora_chunks;
+                            const int half = part >= p.lora_chunks;
                             int a = next[0];
 #pragma unroll
                             for (int o = 1; o < 8; ++o) a = o == i ? next[o] : a;
@@ -954,12 +955,19 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                             if (leader) mbar_expect_tx(full_bar(s), 2 * (128 + BN / 2) * cw * 2);
                             const int64_t block = ((int64_t)m2 * p.lora_cap + j0 + i) * p.lora_parts + part;
                             tma_load_2d_2sm(sa, &p.tmH, leader_full, 0,
-                                            (int)((block * 3 + (a < 0 ? 2 : e & 1)) * 256) + (int)rank * 128);
+                                            (int)((block * (p.lora_terms + 1) + (a < 0 ? p.lora_terms : term)) * 256) + (int)rank * 128);
                             // out of bounds: zeros, for an adapter that is not finite and for the other half of a gate/up tile
                             const bool none = a < 0 || (DUAL && half != (int)rank);
-                            tma_load_3d_2sm(sa + S2_A, half ? &p.tmUp2 : &p.tmUp, leader_full, part % p.lora_chunks * cw,
+                            tma_load_3d_2sm(sa + S2_A, half ? &p.tmUp2 : &p.tmUp, leader_full, (part - half * p.lora_chunks) * cw,
                                             none ? p.N : DUAL ? n * 128 : b_row, max(a, 0));
                             issued_mask |= 1u << s;
+                            if (++term == p.lora_terms) {
+                                term = 0;
+                                if (++part == p.lora_parts) {
+                                    part = 0;
+                                    ++i;
+                                }
+                            }
                         }
                     }
                 }
@@ -1009,7 +1017,8 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                 if constexpr (LORA) {
                     if (!waited) grid_dep_wait();
                     waited = true;
-                    const int more = ok ? p.lora_count[t % num_m2] * p.lora_parts * 2 : 0, cw = p.lora_cw;
+                    const int more = ok ? p.lora_count[t % num_m2] * p.lora_parts * p.lora_terms : 0, cw = p.lora_cw;
+                    int term = 0, chunk = 0;
                     for (int e = 0; e < more; ++e, ++it) {
                         const int s = it % S2_STAGES;
                         if (!mbar_wait(full_bar(s), (uint32_t)(it / S2_STAGES) & 1u, p.err, 3, p.mbar_limit_ns)) {
@@ -1019,7 +1028,11 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                         }
                         tc_fence_after();
                         const uint32_t sa = base + s * S2_STAGE;
-                        const int left = min(cw, p.lora_rank - (e >> 1) % p.lora_parts % p.lora_chunks * cw);
+                        const int left = min(cw, p.lora_rank - chunk * cw);
+                        if (++term == p.lora_terms) {
+                            term = 0;
+                            if (++chunk == p.lora_chunks) chunk = 0;
+                        }
                         for (int kk = 0; kk < (left + 15) / 16; ++kk)
                             umma2_bf16(d, make_sdesc_narrow(sa + kk * 32, cw), make_sdesc_narrow(sa + S2_A + kk * 32, cw), IDESC, 1u);
                         umma2_commit_both(empty_bar(s));
@@ -1651,6 +1664,7 @@ cudaError_t launch_gemm_bf16_lora(const GemmDesc& d, const LoraArgs& l, int64_t 
     p.lora_chunks = l.chunks;
     p.lora_parts = l.parts;
     p.lora_rank = l.rank;
+    p.lora_terms = l.terms;
     const int64_t tiles = (d.M + 255ll) / 256 * p.num_n_tiles;
     if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
     const int clusters = (int)std::min<int64_t>(std::max(1, gemm_num_sms() / 2), tiles);

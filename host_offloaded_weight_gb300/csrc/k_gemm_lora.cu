@@ -4,7 +4,8 @@
 // Two launches. lora_rows_kernel writes h_t = s_a down_a x_t as blocks: one for each tile of rows and each adapter with a row in
 // it, zero in the rows of others. The shared product then takes a block with its adapter's `up` as some more columns of K. It
 // starts as soon as the first kernel's CTAs run: its loads of the shared weights need nothing of it, only these last columns do.
-// h is kept as two bf16 terms (16 bits: the first term alone would be off by 2^-9, more than the fp32 sums lose).
+// h is kept as two bf16 terms, 16 bits (the first term alone would be off by 2^-9, as much as the result's own rounding), and as
+// three, 24 bits, where the result is asked for in fp32 too.
 //
 // 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests.
 //
@@ -12,7 +13,7 @@
 // right one, 16 to 128 columns. Each part of `up` is looked over in shared memory before its product.
 // More rows: the pair kernel of k_gemm.cu, whose operands lie in two SMs. Other CTAs of the first kernel look over the `up`
 // matrices of the adapters in use (bytes that the product then finds in L2). One that is not finite is read out of bounds, which
-// gives zeros, against a third term that is NaN in its own rows: they come out NaN, no others do.
+// gives zeros, against one more term that is NaN in its own rows: they come out NaN, no others do.
 #include <algorithm>
 
 #include "kernels.h"
@@ -94,6 +95,11 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 // memory, each CTA finishing its share of the groups of eight rows, in the order of the CTAs. Bound by the latencies of its steps:
 // ids, first loads, sums.
 // (Register products, m16n8k16, from plain loads of a row's 64 bytes by four lanes took 55 to 110 us for 2048 rows of 5120.)
+// The nearest bf16 that is finite where v is.
+__device__ __forceinline__ float near_bf16(float v) {
+    const float h = __bfloat162float(__float2bfloat16_rn(v));
+    return isinf(h) && !isinf(v) ? __bfloat162float(__float2bfloat16_rz(v)) : h;
+}
 constexpr int ROWS_PROD = 0, ROWS_MMA = 1, ROWS_EPI = 2;   // warps; four of the epilogue
 
 __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_constant__ LoraArgs p) {
@@ -250,14 +256,14 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             for (int u = tid; u < own << log_units; u += ROWS_THREADS) {
                 const int l = u >> log_units, c = (u - (l << log_units)) * 2, r = (slice + (l >> 3) * p.slices) * 8 + (l & 7);
                 const int64_t block = ((int64_t)tile * p.cap + j) * p.parts + part0 + (c >> log_cw);
-                f(r, l, c, reinterpret_cast<uint32_t*>(p.h + (block * p.terms * p.tile_rows + row0 + r) * p.cw + (c & (p.cw - 1))));
+                f(r, l, c, reinterpret_cast<uint32_t*>(p.h + (block * p.blocks_terms * p.tile_rows + row0 + r) * p.cw + (c & (p.cw - 1))));
             }
         };
         __syncwarp();
         // zeros in the rows of others, while the loads are on their way (the two warps that see to those come later)
         each([&](int r, int, int, uint32_t* to) {
             if (s_ids[row0 + r] == a) return;
-            for (int t = 0; t < p.terms; ++t) to[t * term] = 0;
+            for (int t = 0; t < p.blocks_terms; ++t) to[t * term] = 0;
         });
         if (any) {
             const bool done = bar_wait_warp(acc_full, (uint32_t)turn & 1u, p.err, 4);   // every warp: nobody is ahead by an adapter
@@ -300,18 +306,16 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
                     v.x += x.x;
                     v.y += x.y;
                 }
-                uint32_t hi = 0, lo = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float w = (e ? v.y : v.x) * scale;
-                    float t1 = __bfloat162float(__float2bfloat16_rn(w));
-                    if (isinf(t1) && !isinf(w)) t1 = __bfloat162float(__float2bfloat16_rz(w));
-                    hi |= (__float_as_uint(t1) >> 16) << (16 * e);
-                    lo |= (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(isfinite(t1) ? w - t1 : 0.f)) << (16 * e);
+                // each term is what the ones before it leave, to the nearest bf16
+                v.x *= scale;
+                v.y *= scale;
+                for (int t = 0; t < p.terms; ++t) {
+                    const float2 h = make_float2(near_bf16(v.x), near_bf16(v.y));
+                    to[t * term] = __float_as_uint(h.x) >> 16 | (__float_as_uint(h.y) & 0xffff0000u);
+                    v.x = isfinite(h.x) ? v.x - h.x : 0.f;
+                    v.y = isfinite(h.y) ? v.y - h.y : 0.f;
                 }
-                to[0] = hi;
-                to[term] = lo;
-                if (p.terms == 3) to[2 * term] = 0x7fc07fc0u;  // NaN
+                if (p.blocks_terms > p.terms) to[p.terms * term] = 0x7fc07fc0u;  // NaN
             });
         }
         fence_before_sync();
@@ -369,7 +373,7 @@ struct FewLora {
     int k_stages, tiles, splits;
     int dual, b2_row_off, epi;
     int cw, chunks, parts, rank;   // columns of a part of h; parts of a rank, of an adapter
-    int pack, halves;              // blocks of a stage; 2: a stage has one term of one block
+    int terms, fit, pack, split;   // terms of h, of a stage; blocks of a stage, or stages of a block
     const int* count;
     const int* list;
     const int* ids;
@@ -396,16 +400,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 // A CTA's adapter stages: every so many stages of the tile's; first: the stage's first block, part `part` of adapter j of the
-// tile. p.pack blocks and both their terms, or (halves = 2) one term of one block.
+// tile. p.pack blocks and all their terms, or (p.split > 1 stages a block) p.fit terms of one block, `term` and up.
 struct Blocks {
     const FewLora& p;
     int all, first, term, j, part;
     __device__ __forceinline__ Blocks(const FewLora& q, int slice, int count) : p(q), all(count), first(0), term(0), j(0), part(0) { step(slice); }
     __device__ __forceinline__ void step(int stages) {
-        if (p.halves == 2) {
-            term += stages;
-            stages = term >> 1;
-            term &= 1;
+        if (p.split > 1) {
+            int blocks = 0;
+            for (term += stages * p.fit; term >= p.split * p.fit; term -= p.split * p.fit) ++blocks;
+            stages = blocks;
         } else {
             stages *= p.pack;
         }
@@ -415,6 +419,7 @@ struct Blocks {
     __device__ __forceinline__ void next() { step(p.splits); }
     __device__ __forceinline__ bool left() const { return first < all; }
     __device__ __forceinline__ int blocks() const { return min(p.pack, all - first); }
+    __device__ __forceinline__ int terms() const { return min(p.fit, p.terms - term); }  // (a copy brings p.fit)
 };
 
 // GELU(v) = v Phi(v), SiLU(v) = v / (1 + e^-v)
@@ -518,8 +523,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
             for (; at_block.left() && turn(); at_block.next(), next()) {
                 if (!one) continue;
                 const uint32_t at = base + s * F::STAGE;
-                const int blocks = at_block.blocks(), terms = 3 - p.halves;
-                bar_expect(full(s), blocks * (up_bytes + terms * h_bytes));
+                const int blocks = at_block.blocks();
+                bar_expect(full(s), blocks * (up_bytes + p.fit * h_bytes));
                 int j = at_block.j, part = at_block.part;
                 for (int i = 0; i < blocks; ++i) {
                     const int half = part >= p.chunks, col = (part - (half ? p.chunks : 0)) * p.cw, a = s_list[j];
@@ -528,8 +533,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                     const uint32_t to = at + i * up_bytes;
                     tma_3d(to, up, full(s), col, half ? p.N : n0, a);
                     if (p.dual) tma_3d(to + up_bytes / 2, up, full(s), col, half ? n0 : p.N, a);
-                    // both terms side by side, or the one
-                    tma_2d(at + P_BYTES + i * terms * h_bytes, &p.map_h, full(s), 0, ((at_block.first + i) * 2 + at_block.term) * NQ);
+                    tma_2d(at + P_BYTES + i * p.fit * h_bytes, &p.map_h, full(s), 0, ((at_block.first + i) * p.terms + at_block.term) * NQ);
                     if (++part == p.parts) {
                         part = 0;
                         ++j;
@@ -596,14 +600,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 uses ^= 1u << s;
                 fence_after_sync();
                 const uint32_t sp = base + s * F::STAGE, sq = sp + P_BYTES;
-                const int blocks = at_block.blocks(), terms = 3 - p.halves;
+                const int blocks = at_block.blocks(), terms = at_block.terms();
                 if (one) {
                     int part = at_block.part;
                     for (int i = 0; i < blocks; ++i) {
                         const int chunk = part >= p.chunks ? part - p.chunks : part, steps = (min(p.cw, p.rank - chunk * p.cw) + 15) / 16;
                         for (int k = 0; k < steps; ++k)
                             for (int t = 0; t < terms; ++t) {
-                                mma_bf16(d, narrow_desc(sp + i * up_bytes + 32 * k, p.cw), narrow_desc(sq + (i * terms + t) * h_bytes + 32 * k, p.cw),
+                                mma_bf16(d, narrow_desc(sp + i * up_bytes + 32 * k, p.cw), narrow_desc(sq + (i * p.fit + t) * h_bytes + 32 * k, p.cw),
                                          IDESC, add);
                                 add = 1;
                             }
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 grid_wait();
                 more = *p.count * p.parts;
             }
-            const int up_bytes = TILE_P * p.cw * 2, h_bytes = NQ * p.cw * 2, terms = 3 - p.halves;
+            const int up_bytes = TILE_P * p.cw * 2, h_bytes = NQ * p.cw * 2;
             Blocks at_block(p, slice, more);
             for (; at_block.left(); at_block.next(), ++it) {
                 const int s = it % S;
@@ -713,7 +717,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                             if ((*w & 0x7f80) == 0x7f80) *w = 0;
                         }
                         const int a = p.list[j];
-                        uint8_t* h = gbase + s * F::STAGE + P_BYTES + i * terms * h_bytes;  // its rows, whatever the order within one
+                        uint8_t* h = gbase + s * F::STAGE + P_BYTES + i * p.fit * h_bytes;  // its rows, whatever the order within one
                         for (int t = 0; t < p.M; ++t)
                             if (p.ids[t] == a && lane < p.cw / 2) *reinterpret_cast<uint32_t*>(h + (t * p.cw + lane * 2) * 2) = 0x7fc07fc0u;
                     }
@@ -862,15 +866,19 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
 }
 
 template <int NQ>
-cudaError_t launch_few(FewLora& p, int rows, cudaStream_t s) {
+cudaError_t launch_few(FewLora& p, int rows, const void* h, int64_t h_rows, cudaStream_t s) {
     auto kern = gemm_lora_few_kernel<NQ>;
     using F = Few<NQ>;
     static SmemAllowance allowed;
     const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), F::SMEM);
     if (e != cudaSuccess) return e;
     p.tiles = (p.N + rows - 1) / rows;
-    p.pack = std::max(1, F::PACK * 32 / p.cw);
-    p.halves = F::PACK * 32 / p.cw ? 1 : 2;  // 2 where rows of 64 columns meet more than 32 tokens
+    // what a stage has room for beside 128 rows of `up`, of term rows as long as those of x; a copy has up to 256 rows
+    const int room = F::Q_BYTES / (NQ * p.cw * 2);
+    p.fit = std::min({p.terms, room, 256 / NQ});
+    p.split = (p.terms + p.fit - 1) / p.fit;
+    p.pack = p.split > 1 ? 1 : std::min(room / p.fit, 64 / p.cw);
+    if (!lora_map(&p.map_h, h, h_rows, p.cw, p.cw, p.fit * NQ, 0, 0)) return cudaErrorInvalidValue;
     p.splits = few_splits(p.tiles, p.k_stages, F::MAX_SPLIT);
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = config(dim3(p.splits > 1 ? p.tiles * p.splits : std::min(p.tiles, gemm_num_sms())), FEW_THREADS, F::SMEM, s, at, true);
@@ -894,7 +902,7 @@ Layout layout(const LoraArgs& p) {
     l.list = up256(4 * p.tiles);
     l.notes = l.list + up256(4 * p.tiles * p.cap);
     l.h = l.notes + up256(16ll * p.n);
-    l.bytes = l.h + p.tiles * p.cap * p.parts * 2ll * p.terms * p.tile_rows * p.cw;
+    l.bytes = l.h + p.tiles * p.cap * p.parts * 2ll * p.blocks_terms * p.tile_rows * p.cw;
     return l;
 }
 
@@ -912,7 +920,7 @@ bool lora_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int b
               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool lora_plan(LoraArgs& p, bool dual) {
+bool lora_plan(LoraArgs& p, bool dual, bool fp32) {
     p.cw = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : 64;
     p.chunks = (p.rank + p.cw - 1) / p.cw;
     p.parts = p.chunks * (dual ? 2 : 1);
@@ -923,8 +931,9 @@ bool lora_plan(LoraArgs& p, bool dual) {
     p.check_parts = 1;
     while (p.check_parts < 16 && (int64_t)p.N * p.rank * 2 / p.check_parts > 24576) p.check_parts *= 2;
     // blocks are rows of one tensor map, counted in 32 bits
-    p.terms = p.tile_rows == 256 ? 3 : 2;
-    return p.tiles * p.cap * p.parts * p.terms * p.tile_rows <= 0x7fffffffll && (int64_t)p.n * p.check_parts <= 0x3fffffffll;
+    p.terms = fp32 ? 3 : 2;
+    p.blocks_terms = p.terms + (p.tile_rows == 256 ? 1 : 0);
+    return p.tiles * p.cap * p.parts * p.blocks_terms * p.tile_rows <= 0x7fffffffll && (int64_t)p.n * p.check_parts <= 0x3fffffffll;
 }
 
 int64_t lora_ws_bytes(const LoraArgs& p) { return layout(p).bytes; }
@@ -940,13 +949,12 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     const bool few = p.tile_rows != 256;
     const cudaError_t e = launch_rows(p, dual, s);
     if (e != cudaSuccess) return e;
-    const int64_t h_rows = p.tiles * p.cap * p.parts * p.terms * p.tile_rows;
+    const int64_t h_rows = p.tiles * p.cap * p.parts * p.blocks_terms * p.tile_rows;
     if (!few) return launch_gemm_bf16_lora(d, p, h_rows, s);
     const int rows = dual ? TILE_P / 2 : TILE_P;
     FewLora f;
     memset(&f, 0, sizeof(f));
     if (!lora_map(&f.map_w, d.B, d.b_rows, d.K, 64, rows, 0, 0) || !lora_map(&f.map_x, d.A, d.M, d.K, 64, p.tile_rows, 0, 0) ||
-        !lora_map(&f.map_h, p.h, h_rows, p.cw, p.cw, (p.cw == 64 && p.tile_rows > 32 ? 1 : 2) * p.tile_rows, 0, 0) ||
         !lora_map(&f.map_up, p.up, d.N, p.rank, p.cw, rows, p.n, p.up_stride) ||
         (dual && !lora_map(&f.map_up2, p.up2, d.N, p.rank, p.cw, rows, p.n, p.up_stride)))
         return cudaErrorInvalidValue;
@@ -961,6 +969,7 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     f.chunks = p.chunks;
     f.parts = p.parts;
     f.rank = p.rank;
+    f.terms = p.terms;
     f.count = p.count;
     f.list = p.list;
     f.ids = p.ids;
@@ -971,10 +980,10 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     f.C32 = static_cast<float*>(d.C32);
     f.err = d.err_word;
     switch (p.tile_rows) {
-        case 16: return launch_few<16>(f, rows, s);
-        case 32: return launch_few<32>(f, rows, s);
-        case 64: return launch_few<64>(f, rows, s);
-        default: return launch_few<128>(f, rows, s);
+        case 16: return launch_few<16>(f, rows, p.h, h_rows, s);
+        case 32: return launch_few<32>(f, rows, p.h, h_rows, s);
+        case 64: return launch_few<64>(f, rows, p.h, h_rows, s);
+        default: return launch_few<128>(f, rows, p.h, h_rows, s);
     }
 }
 

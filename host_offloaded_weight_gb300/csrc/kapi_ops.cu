@@ -183,7 +183,7 @@ ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A, const void* B, int
     p.n = l->n;
     p.rank = l->rank;
     p.err = entry_error_word();
-    if (!lora_plan(p, dual)) return LS_ERR_UNSUPPORTED;
+    if (!lora_plan(p, dual, C32 != nullptr)) return LS_ERR_UNSUPPORTED;
     GemmDesc d;
     d.epi = epilogue;
     d.A = A; d.lda = K; d.a_rows = M;

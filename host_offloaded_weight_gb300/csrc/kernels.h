@@ -139,8 +139,8 @@ struct LoraArgs {
     int T, N, K, n, rank;
     // by lora_plan. h as blocks [tile][adapter of the tile][part][term] of tile_rows x cw values; a part is cw of
     // the rank's columns, the gate's `chunks` parts first
-    // Terms: two that add up to h, and for the pair kernel a third, NaN in the adapter's rows.
-    int cw, chunks, parts, tile_rows, cap, check_parts, terms;
+    // Terms: two or three that add up to h; blocks of the pair kernel have one more, NaN in the adapter's rows.
+    int cw, chunks, parts, tile_rows, cap, check_parts, terms, blocks_terms;
     int64_t tiles;
     // the first kernel's grid
     CUtensorMap map_x, map_down;
@@ -152,7 +152,7 @@ struct LoraArgs {
     uint8_t* notes;           // [n][16] of the adapters in use: not all zero for one that is not finite
     __nv_bfloat16* h;
 };
-bool lora_plan(LoraArgs& p, bool dual);  // false: more blocks than can be counted
+bool lora_plan(LoraArgs& p, bool dual, bool fp32);  // fp32: results in 32 bits too; false: more blocks than can be counted
 int64_t lora_ws_bytes(const LoraArgs& p);
 // d: the shared product (dense, as for launch_gemm_bf16; b_rows given); ws: lora_ws_bytes, 256-byte aligned.
 cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStream_t s);

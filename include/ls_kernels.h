@@ -285,10 +285,11 @@ typedef struct lsk_lora {
  *   C[t] = epilogue(A[t] B^T + scale_a (A[t] down_a^T) up_a^T),  a = ids_dev[t]
  * and nothing added where ids_dev[t] is not one of 0 .. n-1 (say, -1). All epilogues, arguments and alignments of
  * lsk_gemm_bf16; with LSK_EPI_SWIGLU the gate's and the other projection's parts are added before the SiLU and the product.
- * Sums are fp32 in a fixed order; A[t] down_a^T, scaled, enters the second product as two bf16 terms (16 bits). Rows of
+ * Sums are fp32 in a fixed order; A[t] down_a^T, scaled, enters the second product as two bf16 terms (16 bits), with C32
+ * as three (24). Rows of
  * one adapter cost least side by side (a tile takes up to 256 rows and pays for each adapter among them). An adapter with a
  * NaN or an infinity in `up` or up2 makes its own rows NaN; rows of others are as if it were not there. Takes scratch on
- * `stream` from the library's pool (LS_ERR_OOM if refused): 4 rank bytes, rounded up, for each row of a tile and each
+ * `stream` from the library's pool (LS_ERR_OOM if refused): 4 to 8 rank bytes, rounded up, for each row of a tile and each
  * adapter that it could hold, min(n, 256) of them. K up to 2^24. LS_ERR_UNSUPPORTED for ranks above 256 or more scratch rows
  * than 2^31. */
 ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A_dev, const void* B_dev, int64_t b_rows, int32_t b2_row_off,

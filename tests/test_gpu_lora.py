@@ -1,7 +1,7 @@
 """The shared projection with low-rank adapters beside it, against a 64-bit form.
 
 Tolerances. The fp32 sum of n products of bf16 values, in whatever order, is within n 2^-23 sum|products| of the exact one; the
-two terms of h are within 2^-16 |h|, and h itself within K 2^-23 of its own sum of magnitudes. So a result before the epilogue
+two terms of h are within 2^-16 |h| (the three of a call with fp32 results within 2^-23), and h itself within K 2^-23 of its own sum of magnitudes. So a result before the epilogue
 is within  (K + r + 4) 2^-23 S + 2^-16 S_h,  where S is the sum of all magnitudes |x w| and |s||x d||u|, and S_h that of the
 adapter's part; far less in fact. A bf16 result is then rounded once: half a step, 2^-8 of its magnitude at most. GELU and SiLU
 have slopes of at most 1.13 and 1.1; GELU's own form is within 2e-6 of the exact one, SiLU's by __expf within 2^-20 relative."""
@@ -64,7 +64,7 @@ class Case:
                 z[rows] += s * (x[rows] @ d.T) @ u.T
                 Sh[rows] = abs(s) * (x[rows].abs() @ d.abs().T) @ u.abs().T
             parts.append(z)
-            tols.append((self.K + r + 4) * 2.0 ** -23 * (S + Sh) + 2.0 ** -16 * Sh)
+            tols.append((self.K + r + 4) * 2.0 ** -23 * (S + Sh) + (2.0 ** -16 if self.out32 is None else 2.0 ** -23) * Sh)
         z, tol = parts[0], tols[0]
         if self.epi == "swiglu":
             g, u = parts
