@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     __shared__ uint32_t s_tmem;
     __shared__ __align__(8) uint64_t s_bars[2 * ROWS_MAX_STAGES + 1];
     __shared__ volatile int stop;
-    if (p.tile_rows != 256) grid_release();
     if ((int)blockIdx.x >= p.rows_ctas) {
         look_over(p, (int)blockIdx.x - p.rows_ctas, (int)gridDim.x - p.rows_ctas);
         return;
@@ -181,10 +180,14 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
         if (tid < count) p.list[(int64_t)tile * p.cap + tid] = s_list[tid];
         if (tid == 0) p.count[tile] = count;
     }
+    // A product of few rows may start beside this kernel from here on (one of many waits for its memory traffic to pass: loads
+    // took 15 us behind the pair kernel's first ones). Not before tensor memory is taken: the product might take all that is left.
+    if (p.tile_rows != 256) grid_release();
     const uint32_t tmem = s_tmem;
     const int k0 = (int)((int64_t)slice * p.k_stages / p.slices), k1 = (int)((int64_t)(slice + 1) * p.k_stages / p.slices);
     // (divisions by numbers that only the launch knows take 150 clocks each: counters and shifts below)
     const int log_cw = p.cw == 16 ? 4 : p.cw == 32 ? 5 : 6;
+    const int chains = min(k1 - k0, p.chains);
     const int cols = min(128, p.parts * p.cw - col0), part0 = col0 >> log_cw, parts = cols >> log_cw;
     const int groups = p.run / 8, own_groups = (groups + p.slices - 1) / p.slices;
     const int q = warp & 3, col = 32 * q + lane;   // the epilogue: q the TMEM lane quarter that a warp can read, col the lane's column
@@ -238,7 +241,8 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
                         const uint32_t sp = base + s * stage;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16(tmem, operand_desc(sp + 32 * i), operand_desc(sp + down_bytes + 32 * i), idesc, k > k0 || i ? 1u : 0u);
+                            mma_bf16(tmem + (uint32_t)(((k - k0) & (p.chains - 1)) * p.run), operand_desc(sp + 32 * i), operand_desc(sp + down_bytes + 32 * i), idesc,
+                                     k - k0 >= p.chains || i ? 1u : 0u);
                         mma_commit(empty(s));
                     }
                     __syncwarp();
@@ -274,18 +278,23 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             // every CTA's sums of a row go to the CTA that has it
             if (warp >= ROWS_EPI && warp < ROWS_EPI + 4 && 32 * q < cols)
                 for (int g = 0, owner = 0, l = 0; g < groups && 8 * g < rows; ++g) {
-                    uint32_t v[8];
-                    tmem_load8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(8 * g), v);
-                    tmem_load_wait();
+                    float v[8];
+                    for (int c = 0; c < chains; ++c) {
+                        uint32_t x[8];
+                        tmem_load8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c * p.run + 8 * g), x);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = c ? v[i] + __uint_as_float(x[i]) : __uint_as_float(x[i]);
+                    }
                     const uint32_t to = smem_addr(red + ((slice * own_groups + l) * 8) * p.block_cols + col);
                     if (col < cols) {
                         if (p.slices == 1) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) st_shared1(to + i * p.block_cols * 4, v[i]);
+                            for (int i = 0; i < 8; ++i) st_shared1(to + i * p.block_cols * 4, __float_as_uint(v[i]));
                         } else {
                             const uint32_t there = cluster_addr(to, owner);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) st_cluster(there + i * p.block_cols * 4, __uint_as_float(v[i]));
+                            for (int i = 0; i < 8; ++i) st_cluster(there + i * p.block_cols * 4, v[i]);
                         }
                     }
                     if (++owner == p.slices) {
@@ -337,16 +346,20 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ the shared product, few rows
+// The tensor core cuts its fp32 sums off, so a long chain of products loses 2^-25 and more of the sum with each: an accumulator takes
+// CHAIN stages at a time, and the epilogue's warps add it up in registers (64 x 5120 x 13824: off by 3.1e-6 in one chain, now 2e-7).
+//
 // One CTA an SM, persistent over tiles of 128 weight rows (SwiGLU: 64 gate rows and their 64 up rows). Warp 0 loads by TMA,
 // warp 1 issues the products (kind::f16, 128 x NQ x 16), warps 2 to 5 write the results. Few tiles are shared along K by a
 // cluster, whose CTAs add the sums of every so many groups of eight tokens out of their shared memory, in a fixed order.
 // After its stages of the shared weights a CTA takes its share of the tile's adapter stages: 128 rows of `up` (rows of
 // 32, 64 or 128 bytes: 16, 32 or 64 columns, whatever holds the rank) and both terms of the block of h.
+constexpr int CHAIN = 4;  // stages
 constexpr int TILE_P = 128, P_BYTES = TILE_P * 128, FEW_EPI = 4, FEW_THREADS = 32 * (2 + FEW_EPI);
 
-template <int NQ>
+// PACK: the right operand's room in a stage, in rows of x.
+template <int NQ, int PACK>
 struct Few {
-    static constexpr int PACK = NQ <= 32 ? 2 : 1;                 // an adapter stage's blocks: PACK 64 / cw term rows of x's size
     static constexpr int Q_BYTES = PACK * NQ * 128;
     static constexpr int STAGE = P_BYTES + Q_BYTES;
     static constexpr int MAX_SPLIT = NQ <= 16 ? 8 : 4;
@@ -363,7 +376,7 @@ struct Few {
     static constexpr int FIT = (200 * 1024 - RED_BYTES - X_BYTES - 1024 - 512) / STAGE;
     static constexpr int STAGES = FIT < 9 ? FIT : 9;
     static constexpr int SMEM = STAGES * STAGE + RED_BYTES + X_BYTES + 1024 + 512;
-    static constexpr int COLS = 2 * NQ < 32 ? 32 : 2 * NQ;        // of tensor memory: two accumulators
+    static constexpr int COLS = 4 * NQ;                           // of tensor memory: two accumulators, a tile's sums (and a quarter not used)
     static_assert(STAGES >= 4 && SMEM <= 232448, "shared memory");
 };
 
@@ -426,9 +439,9 @@ struct Blocks {
 __device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.f + erff(v * 0.70710678118654752f)); }
 __device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
 
-template <int NQ>
+template <int NQ, int PACK>
 __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __grid_constant__ FewLora p) {
-    using F = Few<NQ>;
+    using F = Few<NQ, PACK>;
     constexpr int S = F::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -441,8 +454,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
     auto acc_empty = [&](int b) { return bars + 8u * (2 * S + 2 + b); };
     const uint32_t done = bars + 8u * (2 * S + 4);
     auto checked = [&](int s) { return bars + 8u * (2 * S + 5 + s); };  // an adapter stage's values are finite
-    const uint32_t based = bars + 8u * (3 * S + 5);                     // a tile's stages of the shared weights have all arrived
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (3 * S + 6));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (3 * S + 5));
     __shared__ volatile int stop;
     __shared__ int s_list[LORA_FEW_ROWS];  // the loading warp's copy of the adapters
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -459,7 +471,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
             bar_init(acc_empty(b), FEW_EPI);
         }
         bar_init(done, 1);
-        bar_init(based, 1);
         bar_init_fence();
         tma_desc_prefetch(&p.map_w);
         tma_desc_prefetch(&p.map_x);
@@ -556,41 +567,55 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
         int n = 0, it = 0, more = -1;
         uint32_t uses = 0;
         bool ok = true;
-        for (int tile = tile0; ok && tile < p.tiles; tile += step, ++n) {
+        uint32_t d = 0, add = 0;
+        int left = 0;                   // stages that this chain still takes
+        auto chain = [&]() {            // the accumulator for the next stage
+            if (left > 0) return true;
             const int b = n & 1;
             if (!bar_wait_warp(acc_empty(b), (uint32_t)((n >> 1) + 1) & 1u, p.err, 2) || stop) {
+                ok = false;
                 stop = 1;
-                break;
+                return false;
             }
             fence_after_sync();
-            const uint32_t d = tmem + (uint32_t)(b * NQ);
-            uint32_t add = 0;
-            auto ready = [&]() {
-                if (!bar_wait_warp(full(it % S), (uint32_t)(it / S) & 1u, p.err, 3)) {
+            d = tmem + (uint32_t)(b * NQ);
+            add = 0;
+            left = CHAIN;
+            return true;
+        };
+        auto close = [&](bool last) {   // after a stage's products
+            __syncwarp();
+            add = 1;
+            if (--left > 0 && !last) return;
+            if (one) mma_commit(acc_full(n & 1));
+            __syncwarp();
+            left = 0;
+            ++n;
+        };
+        for (int tile = tile0; ok && tile < p.tiles; tile += step) {
+            for (int k = k0; k < k1 && chain(); ++k, ++it) {
+                const int s = it % S;
+                if (!bar_wait_warp(full(s), (uint32_t)(it / S) & 1u, p.err, 3)) {
                     ok = false;
                     stop = 1;
+                    break;
                 }
                 fence_after_sync();
-                return ok;
-            };
-            for (int k = k0; k < k1 && ready(); ++k, ++it) {
-                const uint32_t sp = base + it % S * F::STAGE, sq = sp + P_BYTES;
+                const uint32_t sp = base + s * F::STAGE, sq = sp + P_BYTES;
                 if (one) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mma_bf16(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), IDESC, i ? 1u : add);
-                    mma_commit(empty(it % S));
+                    mma_commit(empty(s));
                 }
-                __syncwarp();
-                add = 1;
+                close(k + 1 == k1);
             }
-            if (one && ok) bar_arrive(based);
             if (ok && more < 0) {
                 grid_wait();
                 more = *p.count * p.parts;
             }
             const int up_bytes = TILE_P * p.cw * 2, h_bytes = NQ * p.cw * 2;
             Blocks at_block(p, slice, more);
-            for (; ok && at_block.left(); at_block.next(), ++it) {
+            while (ok && at_block.left() && chain()) {
                 const int s = it % S;
                 if (!bar_wait_warp(checked(s), uses >> s & 1u, p.err, 9)) {  // the stage's uses for adapters have a count of their own
                     ok = false;
@@ -613,13 +638,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                             }
                         if (++part == p.parts) part = 0;
                     }
-                    mma_commit(empty(it % S));
+                    mma_commit(empty(s));
                 }
-                __syncwarp();
-                add = 1;
+                at_block.next();
+                ++it;
+                close(!at_block.left());
             }
-            if (ok && one) mma_commit(acc_full(b));
-            __syncwarp();
         }
         if (one) mma_commit(done);
         __syncwarp();
@@ -670,40 +694,58 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 p.C[at + (int64_t)j * p.N] = __float2bfloat16_rn(y);
             }
         };
-        auto sums = [&](int b, int g, float (&v)[8]) {
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16), whole = lanes + 2 * NQ;  // whole: this warp's place for a tile's sums
+        auto sums = [&](int g, float (&v)[8]) {
             uint32_t x[8];
-            tmem_load8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NQ + 8 * g), x);
+            tmem_load8(whole + 8 * g, x);
             tmem_load_wait();
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(x[j]);
         };
-        int n = 0, it = 0, more = -1;
-        for (int tile = tile0; tile < p.tiles; tile += step, ++n) {
+        float sum[NQ];
+        int n = 0, it = 0, more = -1;   // chains, stages, adapter blocks of a tile
+        auto collect = [&](bool first) {
             const int b = n & 1;
-            // Adapter stages first pass by these warps, a quarter each. 0 times infinity is NaN: a value that is not finite would
-            // reach rows of other adapters. It becomes zero, and the adapter's own rows of h NaN.
-            // (A wait by parity cannot tell a use of a stage from the one two before it: these warps have not seen the uses for the
-            // shared weights, so they first hear that all of those are over.)
-            it += k1 - k0;
-            if (!dead && !bar_wait_warp(based, (uint32_t)n & 1u, p.err, 10)) {
+            if (!dead && (!bar_wait_warp(acc_full(b), (uint32_t)(n >> 1) & 1u, p.err, 4) || stop)) {
                 stop = 1;
                 dead = true;
             }
+            fence_after_sync();
+#pragma unroll
+            for (int g = 0; g < NQ / 8; ++g) {
+                if (g >= groups) break;
+                uint32_t x[8];
+                tmem_load8(lanes + (uint32_t)(b * NQ + 8 * g), x);
+                tmem_load_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[8 * g + j] = first ? __uint_as_float(x[j]) : sum[8 * g + j] + __uint_as_float(x[j]);
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) bar_arrive(acc_empty(b));
+            ++n;
+        };
+        for (int tile = tile0; tile < p.tiles; tile += step) {
+            for (int k = k0; k < k1; k += CHAIN) collect(k == k0);
+            // Adapter stages first pass by these warps, a quarter each. 0 times infinity is NaN: a value that is not finite would
+            // reach rows of other adapters. It becomes zero, and the adapter's own rows of h NaN.
+            // (A wait by parity cannot tell a use of a stage from the one two before it. The last chain above is complete, so every use
+            // before these is over.)
+            it += k1 - k0;
             if (more < 0) {
                 grid_wait();
                 more = *p.count * p.parts;
             }
             const int up_bytes = TILE_P * p.cw * 2, h_bytes = NQ * p.cw * 2;
             Blocks at_block(p, slice, more);
-            for (; at_block.left(); at_block.next(), ++it) {
+            for (int in_chain = 0; at_block.left(); ++it) {
                 const int s = it % S;
-                if (dead || !bar_wait_warp(full(s), (uint32_t)(it / S) & 1u, p.err, 8)) {
+                if (!dead && !bar_wait_warp(full(s), (uint32_t)(it / S) & 1u, p.err, 8)) {
                     stop = 1;
                     dead = true;
-                    continue;
                 }
                 int j = at_block.j, part = at_block.part;
-                for (int i = 0; i < at_block.blocks(); ++i) {
+                for (int i = 0; !dead && i < at_block.blocks(); ++i) {
                     uint8_t* v = gbase + s * F::STAGE + i * up_bytes + q * (up_bytes / 4);
                     uint32_t bad = 0;
 #pragma unroll 4
@@ -729,12 +771,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 fence_smem_async();
                 __syncwarp();
                 if (lane == 0) bar_arrive(checked(s));
+                at_block.next();
+                if (++in_chain == CHAIN || !at_block.left()) {
+                    collect(false);
+                    in_chain = 0;
+                }
             }
-            if (!dead && (!bar_wait_warp(acc_full(b), (uint32_t)(n >> 1) & 1u, p.err, 4) || stop)) {
-                stop = 1;
-                dead = true;
+#pragma unroll
+            for (int g = 0; g < NQ / 8; ++g) {
+                if (g >= groups) break;
+                tmem_store8(whole + 8 * g, sum + 8 * g);
             }
-            fence_after_sync();
+            tmem_store_wait();
 #pragma unroll 1
             for (int g = 0, owner = -1, l = 0; g < groups; ++g) {  // l: the owner's groups before this one
                 if (++owner == p.splits) {
@@ -743,7 +791,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                 }
                 if (p.splits > 1 && owner == slice) continue;
                 float v[8];
-                sums(b, g, v);
+                sums(g, v);
                 if (p.splits == 1) {
                     finish(tile * rows, g, v);
                 } else {
@@ -753,19 +801,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                     for (int j = 0; j < 8; ++j) st_cluster(to + (j * TILE_P + row) * 4, v[j]);
                 }
             }
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) bar_arrive(acc_empty(b));
         }
         if (p.splits > 1) {
             // a cluster has one tile; its sums are added in the order of the CTAs, this one's own first
             __syncwarp();
             cluster_barrier();
-            fence_after_sync();
 #pragma unroll 1
             for (int g = slice, l = 0; g < groups; g += p.splits, ++l) {
                 float v[8];
-                sums(0, g, v);
+                sums(g, v);
 #pragma unroll 1
                 for (int o = 0; o < p.splits - 1; ++o)
 #pragma unroll
@@ -835,7 +879,10 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     p.block_cols = std::min(cols, 128);
     p.col_runs = (cols + 127) / 128;
     p.k_stages = (p.K + 63) / 64;
-    p.tmem_cols = std::max(32, p.run);
+    // Accumulators that the stages take in turn (the tensor core cuts its sums off, see CHAIN below). Two CTAs of an SM get by with
+    // its tensor memory: one that waited for another's could hold up its cluster, and that the other.
+    p.chains = std::min(4, 256 / p.run);
+    p.tmem_cols = p.chains * p.run;
     // 64 KB and more of loads in flight; the products read 128 rows of the last stage's left operand, whatever lies behind it
     const int stage = (p.block_cols + p.run) * 128;
     p.stages = std::max(3, std::min(ROWS_MAX_STAGES, 65536 / stage));
@@ -845,6 +892,7 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     const int64_t runs = p.tiles * (p.tile_rows / p.run) * p.col_runs, room = 2 * gemm_num_sms() - (few ? 0 : LOOK_CTAS / 2);
     p.slots = few ? (int)std::min<int64_t>(p.cap, p.T) : std::min(p.cap, 2);
     p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (int64_t)p.k_stages * stage / 98304, room / (runs * p.slots)}));
+    while (!few && 2 * p.slots <= p.cap && runs * p.slices * 2 * p.slots <= room) p.slots *= 2;
     const int groups = p.run / 8, red = p.slices * ((groups + p.slices - 1) / p.slices) * 8 * p.block_cols * 4;
     const int smem = 1024 + p.stages * stage + std::max(red, 128 * 128);
     const int64_t rows = runs * p.slots * p.slices, most = std::max<int64_t>(LOOK_CTAS / 6, std::min<int64_t>(LOOK_CTAS, 2 * gemm_num_sms() - rows));
@@ -865,10 +913,10 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, lora_rows_kernel, p);
 }
 
-template <int NQ>
+template <int NQ, int PACK>
 cudaError_t launch_few(FewLora& p, int rows, const void* h, int64_t h_rows, cudaStream_t s) {
-    auto kern = gemm_lora_few_kernel<NQ>;
-    using F = Few<NQ>;
+    auto kern = gemm_lora_few_kernel<NQ, PACK>;
+    using F = Few<NQ, PACK>;
     static SmemAllowance allowed;
     const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), F::SMEM);
     if (e != cudaSuccess) return e;
@@ -979,11 +1027,14 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     f.C = static_cast<__nv_bfloat16*>(d.C);
     f.C32 = static_cast<float*>(d.C32);
     f.err = d.err_word;
+    // Room for two terms of a block beside its `up`, where it costs few stages: with room for one, 64 rows' blocks of 64 columns are
+    // two stages that both read `up` (64 adapters of rank 64 beside 13824 x 5120: 108 us). With it where it is not needed, five
+    // stages in place of seven: 37.5 us for 36.6 (64 x 5120 x 13824).
     switch (p.tile_rows) {
-        case 16: return launch_few<16>(f, rows, p.h, h_rows, s);
-        case 32: return launch_few<32>(f, rows, p.h, h_rows, s);
-        case 64: return launch_few<64>(f, rows, p.h, h_rows, s);
-        default: return launch_few<128>(f, rows, p.h, h_rows, s);
+        case 16: return launch_few<16, 2>(f, rows, p.h, h_rows, s);
+        case 32: return launch_few<32, 2>(f, rows, p.h, h_rows, s);
+        case 64: return p.cw == 64 ? launch_few<64, 2>(f, rows, p.h, h_rows, s) : launch_few<64, 1>(f, rows, p.h, h_rows, s);
+        default: return launch_few<128, 1>(f, rows, p.h, h_rows, s);
     }
 }
 
