@@ -1027,13 +1027,13 @@ cudaError_t launch_gemm_lora(const GemmDesc& d, LoraArgs& p, void* ws, cudaStrea
     f.C = static_cast<__nv_bfloat16*>(d.C);
     f.C32 = static_cast<float*>(d.C32);
     f.err = d.err_word;
-    // Room for two terms of a block beside its `up`, where it costs few stages: with room for one, 64 rows' blocks of 64 columns are
-    // two stages that both read `up` (64 adapters of rank 64 beside 13824 x 5120: 108 us). With it where it is not needed, five
-    // stages in place of seven: 37.5 us for 36.6 (64 x 5120 x 13824).
+    // 64 rows: room for all terms of a block beside its `up`, where the smaller stage has it not and the block would be two stages
+    // that both read `up` (64 adapters of rank 64 beside 13824 x 5120: 108 us, now 79). Elsewhere the smaller stage, of which there
+    // are seven in place of five: 36.6 us for 37.5 without adapters (64 x 5120 x 13824).
     switch (p.tile_rows) {
         case 16: return launch_few<16, 2>(f, rows, p.h, h_rows, s);
         case 32: return launch_few<32, 2>(f, rows, p.h, h_rows, s);
-        case 64: return p.cw == 64 ? launch_few<64, 2>(f, rows, p.h, h_rows, s) : launch_few<64, 1>(f, rows, p.h, h_rows, s);
+        case 64: return p.terms * p.cw > 64 ? launch_few<64, 2>(f, rows, p.h, h_rows, s) : launch_few<64, 1>(f, rows, p.h, h_rows, s);
         default: return launch_few<128, 1>(f, rows, p.h, h_rows, s);
     }
 }

@@ -288,7 +288,7 @@ typedef struct lsk_lora {
  * Sums are fp32 in a fixed order; A[t] down_a^T, scaled, enters the second product as two bf16 terms (16 bits), with C32
  * as three (24). Rows of
  * one adapter cost least side by side (a tile takes up to 256 rows and pays for each adapter among them). An adapter with a
- * NaN or an infinity in `up` or up2 makes its own rows NaN; rows of others are as if it were not there. Takes scratch on
+ * NaN or an infinity makes NaN or infinities of its own rows, wholly or in part; rows of others are as if it were not there. Takes scratch on
  * `stream` from the library's pool (LS_ERR_OOM if refused): 4 to 8 rank bytes, rounded up, for each row of a tile and each
  * adapter that it could hold, min(n, 256) of them. K up to 2^24. LS_ERR_UNSUPPORTED for ranks above 256 or more scratch rows
  * than 2^31. */
