@@ -9,6 +9,14 @@
 //
 // 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests.
 //
+// What bounds it. 16 rows with 14 adapters of rank 16 beside 13824 x 5120: 36 us, the weights alone (ids of no adapter) 31, the floor
+// 22; 64 rows and 24 adapters of rank 32 beside 5120 x 13824, fp32 results too: 52 us, alone 36. What the adapters add is the
+// time of the first kernel, whose loads queue behind the stream of weights (7 us by itself, 14 beside it), and the stages of `up`
+// at the end (2 to 5 us). Early requests of the product for all its stages made the first kernel's loads wait 15 us and more where
+// they went through the pair kernel, so there it starts when h is computed. One row beside 4096 x 1024 takes 14 us, a chain of
+// latencies: ids 1, first load 2.5, sums 1.5, the next kernel's look at them 1.5, `up` 2, results 1.5, and two launches.
+// 2048 rows gate/up beside 13824 x 5120 take 377 us, without adapters 324 (lsk_gemm_bf16); 4096 rows of 4096 x 1024 with rank 64 46 and 29.
+//
 // Up to 128 rows (gemm_lora_few_kernel, below): the weights are the left operand (128 rows a tile) and the tokens the
 // right one, 16 to 128 columns. Each part of `up` is looked over in shared memory before its product.
 // More rows: the pair kernel of k_gemm.cu, whose operands lie in two SMs. Other CTAs of the first kernel look over the `up`

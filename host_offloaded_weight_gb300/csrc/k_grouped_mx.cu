@@ -6,13 +6,21 @@
 // are as many as its group needs (multiples of 32: 16 rows, two terms), so a group of three rows costs 32 columns and one of 300 three
 // tiles of 112 and less. A gate/up tile takes 64 gate rows and their 64 up rows.
 //
-// Large groups are bound by an SM's shared memory, about 133 bytes a clock of loads coming in and operands going out: a stage of 192
-// columns is 41 KB in and 40 KB out, 609 clocks for 384 of products. There a pair of CTAs shares a tile of 256 weight rows
-// (cta_group::2): each SM loads 128 rows of weights and one of the terms, 28 KB in and 28 KB out.
+// split_sorted_kernel writes the terms in sorted order (gathering the rows by the routing's table where asked). Then persistent CTAs,
+// one an SM: warp 0 loads by TMA, warp 1 copies the scales to TMEM and issues the products, eight warps in two teams bring the
+// block scales, eight write the results while the next tile is computed (two accumulators).
 //
-// split_sorted_kernel writes the terms in sorted order (gathering the rows by the routing's table where asked). Then one persistent
-// CTA an SM: warp 0 loads by TMA, warp 1 copies the scales to TMEM and issues the products, four warps at a time take turns at
-// bringing the block scales, four write the results while the next tile is computed (two accumulators).
+// What bounds it. Groups of a few rows: 96 tokens through gate and up of 128 experts (2048 x 768, k = 8) take 49 us, 4.4 TB/s of
+// the weights where the memory could bring 6.7. A stage of 16 KB of unpacked weights takes its issuing warp 406 clocks, the tensor
+// pipe is active in 60 of them, and neither a second issuing warp (50 us), nor one product in place of four (43 us), nor no weights
+// at all (46 us) changed that much; scales written to TMEM by their warps in place of copies of the tensor core: 47.6 us, but 215
+// for 195 at 4096 tokens.
+// Large groups: an SM's shared memory, about 133 bytes a clock of loads coming in and operands going out. From single CTAs a stage of 192
+// columns is 41 KB in and 40 KB out, 609 clocks for 384 of products; so a pair of CTAs shares a tile of 256 weight rows
+// (cta_group::2): each SM loads 128 rows of weights and one of the terms, 28 KB in and 28 KB out. 4096 tokens: up 227 -> 201 us,
+// the tensor pipe active 66 % of the product's 145; the split before it takes 50. Rows fetched by the table in the product itself
+// (16-byte asynchronous copies, terms written once for a token): 241 us, 288 with fewer waits. Terms of a token split once and copied
+// to its experts' rows: 199 us for 201.
 #include <algorithm>
 #include <cstdlib>
 
