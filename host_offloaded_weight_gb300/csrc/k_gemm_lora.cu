@@ -41,8 +41,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {  // two bf16
     return (uint32_t)((w & 0x7f80u) == 0x7f80u) | (uint32_t)((w & 0x7f800000u) == 0x7f800000u);
 }
 
-// 16 bytes, or zeros. Volatile, so that the loads of a step are all issued before its first product: left to the compiler they
-// waited for one another.
+// 16 bytes, or zeros. Volatile, so that the eight of a step are all requested before the first is looked at.
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* at, bool on) {
     uint4 v;
     asm volatile(
@@ -575,6 +574,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
         int n = 0, it = 0, more = -1;
         uint32_t uses = 0;
         bool ok = true;
+        const uint32_t low_p = operand_low(base), low_q = operand_low(base + P_BYTES);
         uint32_t d = 0, add = 0;
         int left = 0;                   // stages that this chain still takes
         auto chain = [&]() {            // the accumulator for the next stage
@@ -609,10 +609,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) gemm_lora_few_kernel(const __g
                     break;
                 }
                 fence_after_sync();
-                const uint32_t sp = base + s * F::STAGE, sq = sp + P_BYTES;
+                const uint32_t off = (uint32_t)s * (F::STAGE >> 4);
                 if (one) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_bf16(d, operand_desc(sp + 32 * i), operand_desc(sq + 32 * i), IDESC, i ? 1u : add);
+                    for (int i = 0; i < 4; ++i) mma_bf16(d, operand_from(low_p + off + 2 * i), operand_from(low_q + off + 2 * i), IDESC, i ? 1u : add);
                     mma_commit(empty(s));
                 }
                 close(k + 1 == k1);
@@ -902,7 +902,8 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (int64_t)p.k_stages * stage / 98304, room / (runs * p.slots)}));
     while (!few && 2 * p.slots <= p.cap && runs * p.slices * 2 * p.slots <= room) p.slots *= 2;
     const int groups = p.run / 8, red = p.slices * ((groups + p.slices - 1) / p.slices) * 8 * p.block_cols * 4;
-    const int smem = 1024 + p.stages * stage + std::max(red, 128 * 128);
+    // not less than 80 KB: a third CTA of an SM would wait for tensor memory
+    const int smem = std::max(80 * 1024, 1024 + p.stages * stage + std::max(red, 128 * 128));
     const int64_t rows = runs * p.slots * p.slices, most = std::max<int64_t>(LOOK_CTAS / 6, std::min<int64_t>(LOOK_CTAS, 2 * gemm_num_sms() - rows));
     const int64_t looks = few ? 0 : std::min<int64_t>((most + p.slices - 1) / p.slices, ((int64_t)p.n * p.check_parts + p.slices - 1) / p.slices) * p.slices;
     if (rows + looks > 0x7fffffffll) return cudaErrorInvalidValue;

@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(Cfg<MAXC, TWO>::THREADS, 1) gemm_grouped_mx_ke
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         const bool one = elect_one();
+        const uint32_t low_p = operand_low(base), low_q = operand_low(base + P_BYTES), low_s = scale_low(base + P_BYTES + C::Q_BYTES);
         int n = 0, it = 0;
         bool ok = rank == 0;
         for (Tiles tl(p, groups, TWO); ok && tl.t < tiles; tl.next(p), ++n) {
@@ -371,16 +372,16 @@ __global__ void __launch_bounds__(Cfg<MAXC, TWO>::THREADS, 1) gemm_grouped_mx_ke
                     break;
                 }
                 fence_after_sync();
-                const uint32_t sp = base + s * C::STAGE, sq = sp + P_BYTES, sc = sq + C::Q_BYTES;
+                const uint32_t off = (uint32_t)s * (C::STAGE >> 4);
                 const uint32_t tp = tmem + (uint32_t)(2 * C::BQ + s * C::SCALE_COLS), tq = tp + 4;
                 if (one) {
-                    scales_to_tmem<TWO>(tp, scale_desc(sc));
+                    scales_to_tmem<TWO>(tp, scale_from(low_s + off));
 #pragma unroll
                     for (int j = 0; j < C::PARTS; ++j)
-                        if (j < parts) scales_to_tmem<TWO>(tq + 4 * j, scale_desc(sc + 512 * (1 + j)));
+                        if (j < parts) scales_to_tmem<TWO>(tq + 4 * j, scale_from(low_s + off + (512 >> 4) * (1 + j)));
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // 32 bytes of each row
-                        product<TWO>(d, operand_desc(sp + 32 * j), operand_desc(sq + 32 * j), idesc_at(idesc, j), tp, tq, (k | j) ? 1u : 0u);
+                        product<TWO>(d, operand_from(low_p + off + 2 * j), operand_from(low_q + off + 2 * j), idesc_at(idesc, j), tp, tq, (k | j) ? 1u : 0u);
                     commit<TWO>(empty(s));
                 }
                 __syncwarp();

@@ -218,6 +218,13 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+// The same from its low half: addresses enter in units of 16 bytes, so that a step of n bytes is an addition of n / 16.
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t operand_from(uint32_t low) {
+    return (uint64_t)low | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint32_t scale_low(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t scale_from(uint32_t low) { return (uint64_t)low | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46); }
 // 512 bytes of scales: 32 rows of 16 bytes, no swizzle, groups of 8 rows 128 bytes apart.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
     return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
