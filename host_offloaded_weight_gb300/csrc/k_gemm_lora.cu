@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     __shared__ int s_list[MAX_TILE];
     __shared__ int s_warp[ROWS_THREADS / 32];
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(8) uint64_t s_bars[2 * ROWS_MAX_STAGES + 1];
+    __shared__ __align__(8) uint64_t s_bars[2 * ROWS_MAX_STAGES + 2];
     __shared__ volatile int stop;
     if ((int)blockIdx.x >= p.rows_ctas) {
         look_over(p, (int)blockIdx.x - p.rows_ctas, (int)gridDim.x - p.rows_ctas);
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     const uint32_t bars = smem_addr(s_bars);
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (ROWS_MAX_STAGES + s); };
-    const uint32_t acc_full = bars + 8u * 2 * ROWS_MAX_STAGES;
+    const uint32_t acc_full = bars + 8u * 2 * ROWS_MAX_STAGES, red_full = acc_full + 8u;
     // slices (a cluster) innermost, then runs of columns, slots, runs of rows
     int at = (int)blockIdx.x;
     const int slice = at % p.slices;
@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             bar_init(empty(s), 1);
         }
         bar_init(acc_full, 1);
+        bar_init(red_full, 1);
         bar_init_fence();
         tma_desc_prefetch(&p.map_x);
         tma_desc_prefetch(&p.map_down);
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     const int q = warp & 3, col = 32 * q + lane;   // the epilogue: q the TMEM lane quarter that a warp can read, col the lane's column
     const int rows = min(p.run, p.T - t0 - row0);  // rows that exist (zero and less: none)
     int it = 0, turn = 0;                          // stages and adapters so far
+    bool left = false, came = true;                // everything is sent; everything is here
     int ring = 0;                                  // the place of the next stage, and the parity of its use
     uint32_t parity = 0;
     if (p.slices > 1) cluster_barrier_smem();           // the others' shared memory is there
@@ -279,6 +281,12 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
         if (any) {
             const bool done = bar_wait_warp(acc_full, (uint32_t)turn & 1u, p.err, 4);   // every warp: nobody is ahead by an adapter
             if (!done) stop = 1;
+            if (p.slices > 1 && tid == 0) {   // what comes to this CTA: its groups with rows, from each
+                int due = 0;
+                for (int g = slice; g < groups && 8 * g < rows; g += p.slices) ++due;
+                bar_expect(red_full, due * p.slices * 8 * cols * 4);
+            }
+            __syncwarp();
             if (j + p.slots >= count) grid_release();
             fence_after_sync();
             ++turn;
@@ -299,9 +307,9 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
 #pragma unroll
                             for (int i = 0; i < 8; ++i) st_shared1(to + i * p.block_cols * 4, __float_as_uint(v[i]));
                         } else {
-                            const uint32_t there = cluster_addr(to, owner);
+                            const uint32_t there = cluster_addr(to, owner), counted = cluster_addr(red_full, owner);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) st_cluster(there + i * p.block_cols * 4, v[i]);
+                            for (int i = 0; i < 8; ++i) st_async(there + i * p.block_cols * 4, v[i], counted);
                         }
                     }
                     if (++owner == p.slices) {
@@ -311,8 +319,14 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
                 }
             fence_before_sync();
             __syncwarp();
-            if (p.slices > 1) cluster_barrier_smem();
-            else __syncthreads();
+            if (p.slices == 1) {
+                __syncthreads();
+            } else {
+                left = j + p.slots >= count;
+                if (left) cluster_arrive();
+                came = bar_wait_cluster(red_full, (uint32_t)(turn - 1) & 1u, p.err, 10);
+                if (!came) stop = 1;
+            }
             each([&](int r, int l, int c, uint32_t* to) {
                 if (s_ids[row0 + r] != a) return;
                 float2 v = make_float2(0.f, 0.f);
@@ -344,6 +358,11 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     }
     if (stop && warp == ROWS_PROD)  // an aborted CTA waits for its own copies before it exits
         for (int i = 0; i < S && i < it; ++i) bar_wait(full(i), (uint32_t)((it - 1 - (it - 1 - i) % S) / S) & 1u, p.err, 5);
+    __syncwarp();
+    if (left) {  // an aborted CTA's memory does not go while others' sums may reach it
+        cluster_wait();
+        if (!came) bar_wait_cluster(red_full, (uint32_t)(turn - 1) & 1u, p.err, 11);
+    }
     fence_before_sync();
     __syncthreads();
     if (warp == ROWS_MMA) {

@@ -90,8 +90,12 @@ __device__ __forceinline__ void fence_smem_async() { asm volatile("fence.proxy.a
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same for what was written to shared memory alone (of any CTA of the cluster): a release of everything waits for the global
-// stores before it, ten microseconds beside a kernel that streams weights.
+// Its halves, without an order of memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// The same for this CTA's own shared memory alone (what it set up there, or has read and others may overwrite; stores to
+// another's are not in order behind it: st_async): a release of everything waits for the global stores before it, ten
+// microseconds beside a kernel that streams weights.
 __device__ __forceinline__ void cluster_barrier_smem() {
     asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -105,6 +109,10 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, uint32_t rank) {
 }
 __device__ __forceinline__ void st_cluster(uint32_t a, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+// The same, counted by the barrier at `bar` of that CTA when it is there.
+__device__ __forceinline__ void st_async(uint32_t a, float v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(a), "f"(v), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -233,6 +233,19 @@ def test_many_adapters(T):
     assert torch.equal(c.out[~own], before[~own]) and not bool(torch.isfinite(c.out[own]).all(1).any())
 
 
+@pytest.mark.parametrize("T,K,r,n,used", [(90, 4096, 8, 77, 11), (96, 4096, 16, 96, 11), (64, 2048, 32, 64, 11), (300, 4096, 32, 3, 2)])
+def test_sums_of_a_cluster_are_whole_before_they_are_added(T, K, r, n, used):
+    """Many calls one behind the other, each with other rows of x: no row may have sums of the call before, or none."""
+    cases = [Case(T, 200, K, r, n, ids=[(7 * i) % used + (n - used) for i in range(T)], seed=s) for s in range(4)]
+    wants = [c.exact() for c in cases]
+    for _ in range(25):
+        for c in cases:
+            c.run()
+        torch.cuda.synchronize()
+        for c, (want, tol) in zip(cases, wants):
+            assert bool(((c.out[:T].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
+
+
 @pytest.mark.parametrize("T", [40, 300])
 def test_the_residual_stream_in_place(T):
     """C32 over the residual that it takes: every element is read before it is written."""
