@@ -97,10 +97,10 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 
 // ------------------------------------------------------------------ h
 // A cluster of CTAs, a slice of K each, has a run of a tile's rows (all of a few-row tile, half of a full one) and up to 128 columns
-// of h, for one adapter of the tile after the other: `down` is the left operand of the products (its rows, 128 with what lies
-// behind them, whose results nobody reads), the rows of x, all of them, the right one. The CTAs' sums are added through their shared
-// memory, each CTA finishing its share of the groups of eight rows, in the order of the CTAs. Bound by the latencies of its steps:
-// ids, first loads, sums.
+// of h, for one adapter of the tile after the other, or for a gang of several at a time whose columns lie side by side: `down` is
+// the left operand of the products (its rows, 128 with what lies behind them, whose results nobody reads), the rows of x, all of
+// them, the right one. The CTAs' sums are added through their shared memory, each CTA finishing its share of the groups of eight
+// rows, in the order of the CTAs. Bound by the latencies of its steps: ids, first loads, sums.
 // (Register products, m16n8k16, from plain loads of a row's 64 bytes by four lanes took 55 to 110 us for 2048 rows of 5120.)
 // The nearest bf16 that is finite where v is.
 __device__ __forceinline__ float near_bf16(float v) {
@@ -196,7 +196,10 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     // (divisions by numbers that only the launch knows take 150 clocks each: counters and shifts below)
     const int log_cw = p.cw == 16 ? 4 : p.cw == 32 ? 5 : 6;
     const int chains = min(k1 - k0, p.chains);
-    const int cols = min(128, p.parts * p.cw - col0), part0 = col0 >> log_cw, parts = cols >> log_cw;
+    const int own_cols = min(128, p.parts * p.cw - col0), part0 = col0 >> log_cw, parts = own_cols >> log_cw;   // of an adapter
+    // the finish: a thread has the same two columns of every row, of an adapter of the gang
+    const int log_units = 31 - __clz(own_cols * p.gang) - 1, log_own = 31 - __clz(own_cols), c = (tid & ((1 << log_units) - 1)) * 2;
+    const int member = c >> log_own, own_c = c & (own_cols - 1);
     const int groups = p.run / 8, own_groups = (groups + p.slices - 1) / p.slices;
     const int q = warp & 3, col = 32 * q + lane;   // the epilogue: q the TMEM lane quarter that a warp can read, col the lane's column
     const int rows = min(p.run, p.T - t0 - row0);  // rows that exist (zero and less: none)
@@ -205,11 +208,15 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     int ring = 0;                                  // the place of the next stage, and the parity of its use
     uint32_t parity = 0;
     if (p.slices > 1) cluster_barrier_smem();           // the others' shared memory is there
-    for (int j = slot; j < count; j += p.slots) {
-        const int a = s_list[j];
-        bool mine = false;
-        for (int r = tid; r < rows; r += ROWS_THREADS) mine = mine || s_ids[row0 + r] == a;
-        const bool any = __syncthreads_or(mine);   // the same in the cluster
+    for (int j = slot * p.gang; j < count; j += p.slots * p.gang) {
+        const int members = min(p.gang, count - j), cols = members * own_cols;
+        bool any = true;                               // few rows are one run, with a row of each adapter
+        if (p.gang == 1) {
+            bool mine = false;
+            for (int r = tid; r < rows; r += ROWS_THREADS) mine = mine || s_ids[row0 + r] == s_list[j];
+            any = __syncthreads_or(mine);              // the same in the cluster
+        }
+        const int a = member < members ? s_list[j + member] : -2;   // this thread's: no row has -2
         if (any) {
             auto step = [&]() {
                 if (++ring == S) {
@@ -228,9 +235,13 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
                     if (one) {
                         const uint32_t to = base + s * stage;
                         bar_expect(full(s), cols * 128 + p.run * 128);
-                        for (int i = 0; i < parts; ++i) {
-                            const int half = part0 + i >= p.chunks;
-                            tma_4d(to + i * p.cw * 128, &p.map_down, full(s), k * 64, (part0 + i - half * p.chunks) * p.cw, half, a);
+                        for (int i = 0, m = 0, part = part0; m < members; ++i) {
+                            const int half = part >= p.chunks;
+                            tma_4d(to + i * p.cw * 128, &p.map_down, full(s), k * 64, (part - half * p.chunks) * p.cw, half, s_list[j + m]);
+                            if (++part == part0 + parts) {
+                                part = part0;
+                                ++m;
+                            }
                         }
                         tma_2d(to + down_bytes, &p.map_x, full(s), k * 64, t0 + row0);
                     }
@@ -262,19 +273,20 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             it += k1 - k0;
         }
         // this CTA's rows and columns, two columns a thread: row r is row (r & 7) of its r / 8th group
-        const int own = groups > slice ? (groups - slice + p.slices - 1) / p.slices * 8 : 0, log_units = 31 - __clz(cols) - 1;
-        const float scale = any && p.scale ? __ldg(p.scale + a) : 1.f;
+        const int own = groups > slice ? (groups - slice + p.slices - 1) / p.slices * 8 : 0;
+        const float scale = any && p.scale && a >= 0 ? __ldg(p.scale + a) : 1.f;
         const int64_t term = (int64_t)p.tile_rows * p.cw / 2;
-        auto each = [&](auto f) {   // f(row of the run, local row, column, where its pair of h goes)
-            for (int u = tid; u < own << log_units; u += ROWS_THREADS) {
-                const int l = u >> log_units, c = (u - (l << log_units)) * 2, r = (slice + (l >> 3) * p.slices) * 8 + (l & 7);
-                const int64_t block = ((int64_t)tile * p.cap + j) * p.parts + part0 + (c >> log_cw);
-                f(r, l, c, reinterpret_cast<uint32_t*>(p.h + (block * p.blocks_terms * p.tile_rows + row0 + r) * p.cw + (c & (p.cw - 1))));
+        const int64_t block = ((int64_t)tile * p.cap + j + member) * p.parts + part0 + (own_c >> log_cw);
+        auto each = [&](auto f) {   // f(row of the run, local row, where its pair of h goes)
+            if (a == -2) return;
+            for (int l = tid >> log_units; l < own; l += ROWS_THREADS >> log_units) {
+                const int r = (slice + (l >> 3) * p.slices) * 8 + (l & 7);
+                f(r, l, reinterpret_cast<uint32_t*>(p.h + (block * p.blocks_terms * p.tile_rows + row0 + r) * p.cw + (own_c & (p.cw - 1))));
             }
         };
         __syncwarp();
         // zeros in the rows of others, while the loads are on their way (the two warps that see to those come later)
-        each([&](int r, int, int, uint32_t* to) {
+        each([&](int r, int, uint32_t* to) {
             if (s_ids[row0 + r] == a) return;
             for (int t = 0; t < p.blocks_terms; ++t) to[t * term] = 0;
         });
@@ -287,7 +299,8 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
                 bar_expect(red_full, due * p.slices * 8 * cols * 4);
             }
             __syncwarp();
-            if (j + p.slots >= count) grid_release();
+            const bool last = j + p.slots * p.gang >= count;
+            if (last) grid_release();
             fence_after_sync();
             ++turn;
             // every CTA's sums of a row go to the CTA that has it
@@ -322,12 +335,12 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             if (p.slices == 1) {
                 __syncthreads();
             } else {
-                left = j + p.slots >= count;
+                left = last;
                 if (left) cluster_arrive();
                 came = bar_wait_cluster(red_full, (uint32_t)(turn - 1) & 1u, p.err, 10);
                 if (!came) stop = 1;
             }
-            each([&](int r, int l, int c, uint32_t* to) {
+            each([&](int r, int l, uint32_t* to) {
                 if (s_ids[row0 + r] != a) return;
                 float2 v = make_float2(0.f, 0.f);
                 const float* from = red + l * p.block_cols + c;
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
         }
         fence_before_sync();
         __syncwarp();
-        if (j + p.slots >= count) break;
+        if (j + p.slots * p.gang >= count) break;
         // the next adapter's sums go where these were read
         if (p.slices > 1 && any) cluster_barrier_smem();
         else __syncthreads();
@@ -903,7 +916,14 @@ cudaLaunchConfig_t config(dim3 grid, int threads, int smem, cudaStream_t s, cuda
 cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     const int cols = p.parts * p.cw;
     p.run = std::min(p.tile_rows, 128);
-    p.block_cols = std::min(cols, 128);
+    // Adapters of few rows go together, as many as 128 columns hold: x is read once for them, and more SMs are left for the product
+    // to start on. 128 rows of as many adapters of rank 16, 4096 x 4096: 44 us one by one, now 36; 8 rows 21.7 and 17.4; 128 rows
+    // of 8 adapters of rank 32, 5120 x 13824: 53 and 42. (64 columns at most: 24 adapters of rank 32 49 us for 51, but the last 51.)
+    const bool few = p.tile_rows != 256;
+    const int most_adapters = (int)std::min<int64_t>(p.cap, p.T);
+    p.gang = 1;
+    while (few && 2 * p.gang * cols <= 128 && p.gang < most_adapters) p.gang *= 2;
+    p.block_cols = std::min(p.gang * cols, 128);
     p.col_runs = (cols + 127) / 128;
     p.k_stages = (p.K + 63) / 64;
     // Accumulators that the stages take in turn (the tensor core cuts its sums off, see CHAIN below). Two CTAs of an SM get by with
@@ -913,12 +933,12 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     // 64 KB and more of loads in flight; the products read 128 rows of the last stage's left operand, whatever lies behind it
     const int stage = (p.block_cols + p.run) * 128;
     p.stages = std::max(3, std::min(ROWS_MAX_STAGES, 65536 / stage));
-    // A cluster for each run of rows and columns and each adapter that there may be (few rows) or two (a full tile has few), over
+    // A cluster for each run of rows and columns and each gang that there may be (few rows) or two adapters (a full tile has few), over
     // slices of 96 KB and more; as many as are resident together, two an SM.
-    const bool few = p.tile_rows != 256;
     const int64_t runs = p.tiles * (p.tile_rows / p.run) * p.col_runs, room = 2 * gemm_num_sms() - (few ? 0 : LOOK_CTAS / 2);
-    p.slots = few ? (int)std::min<int64_t>(p.cap, p.T) : std::min(p.cap, 2);
+    p.slots = few ? (most_adapters + p.gang - 1) / p.gang : std::min(p.cap, 2);
     p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (int64_t)p.k_stages * stage / 98304, room / (runs * p.slots)}));
+    if (few && runs * p.slots * p.slices <= gemm_num_sms()) p.stages = std::min(ROWS_MAX_STAGES, 131072 / stage);  // an SM to itself
     while (!few && 2 * p.slots <= p.cap && runs * p.slices * 2 * p.slots <= room) p.slots *= 2;
     const int groups = p.run / 8, red = p.slices * ((groups + p.slices - 1) / p.slices) * 8 * p.block_cols * 4;
     // not less than 80 KB: a third CTA of an SM would wait for tensor memory

@@ -246,6 +246,15 @@ def test_sums_of_a_cluster_are_whole_before_they_are_added(T, K, r, n, used):
             assert bool(((c.out[:T].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
 
 
+@pytest.mark.parametrize("epi", ["store", "swiglu", "resid"])
+@pytest.mark.parametrize("T,K,r,n,used", [(128, 640, 16, 128, 128), (90, 4096, 8, 77, 77), (64, 2048, 32, 64, 11), (16, 1032, 24, 9, 3), (9, 512, 64, 9, 5),
+                                          (48, 1024, 40, 40, 7), (128, 8192, 32, 8, 8)])
+def test_gangs_of_few_rows_adapters(T, K, r, n, used, epi):
+    """Numbers of adapters that leave the last gang of a slot short, in use by rows apart."""
+    ids = [(7 * i) % used + (n - used) for i in range(T)]
+    Case(T, 200, K, r, n, epi, ids=ids, seed=5).run().check()
+
+
 @pytest.mark.parametrize("T", [40, 300])
 def test_the_residual_stream_in_place(T):
     """C32 over the residual that it takes: every element is read before it is written."""
