@@ -286,10 +286,9 @@ typedef struct lsk_lora {
  * and nothing added where ids_dev[t] is not one of 0 .. n-1 (say, -1). All epilogues, arguments and alignments of
  * lsk_gemm_bf16; with LSK_EPI_SWIGLU the gate's and the other projection's parts are added before the SiLU and the product.
  * Sums are fp32 in a fixed order; A[t] down_a^T, scaled, enters the second product as two bf16 terms (16 bits), with C32
- * as three (24). Rows of
- * one adapter cost least side by side (a tile takes up to 256 rows and pays for each adapter among them). An adapter with a
- * NaN or an infinity makes NaN or infinities of its own rows, wholly or in part; rows of others are as if it were not there. Takes scratch on
- * `stream` from the library's pool (LS_ERR_OOM if refused): 4 to 8 rank bytes, rounded up, for each row of a tile and each
+ * as three (24). Rows of one adapter cost least side by side (a tile takes up to 256 rows and pays for each adapter among
+ * them). An adapter with a NaN or an infinity makes NaN or infinities of its own rows, wholly or in part; rows of others are
+ * as if it were not there. Takes scratch on `stream` from the library's pool (LS_ERR_OOM if refused): 4 to 8 rank bytes, rounded up, for each row of a tile and each
  * adapter that it could hold, min(n, 256) of them. K up to 2^24. LS_ERR_UNSUPPORTED for ranks above 256 or more scratch rows
  * than 2^31. */
 ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A_dev, const void* B_dev, int64_t b_rows, int32_t b2_row_off,
@@ -307,7 +306,8 @@ ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A_dev, const void* B_
  * M: rows of the table and of C. Groups may be empty; rows of C that belong to no group are left as they were. A's values enter as
  * in lsk_gemm_bf16_mxfp4 (exact down to 2^-13 of the largest of their block of 32, within 2^-22 of that largest below); sums are
  * fp32 in a fixed order, SiLU takes __expf. Any K and N from 1 up where A's rows are 16-byte aligned (K a multiple of 8);
- * bounds outside 0 .. M are cut to it. Codes 32-byte aligned, strides of them multiples of 32 bytes; scales, A and strides of
+ * bounds outside 0 .. M are cut to it, and a row that bounds out of order give to two groups has the one's or the other's values.
+ * Codes 32-byte aligned, strides of them multiples of 32 bytes; scales, A and strides of
  * scales 16; with one group the strides are not read. n_groups <= 256, M up to 2^30 (LS_ERR_UNSUPPORTED above). Takes scratch on
  * `stream` from the library's pool, 2 M (K + K / 32) bytes and the padding (LS_ERR_OOM if refused). */
 ls_status lsk_gemm_grouped_bf16_mxfp4(int32_t epilogue, const void* A_dev, int64_t a_rows, const void* b_codes_dev,

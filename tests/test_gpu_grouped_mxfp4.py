@@ -246,6 +246,33 @@ def test_a_layer_from_its_parts(T, E, k, H, F):
         assert bool(((few - out32).abs().double() <= 2 * (2.0 ** -8 + 2.0 ** -12) * size).all())
 
 
+@pytest.mark.parametrize("bounds", [[0, 25, 10, 30], [0, 250, 20, 300], [5, 200, 0, 300, 100, 280]])
+def test_rows_that_bounds_out_of_order_give_to_two_groups_have_the_values_of_one(bounds):
+    n, M = len(bounds) - 1, max(bounds)
+    wants = []
+    for e in range(n):
+        c = Case([0] * e + [M] + [0] * (n - 1 - e), 130, 200)
+        if e:
+            c.codes, c.scales, c.values = first.codes, first.scales, first.values
+        else:
+            first = c
+        want, tol = c.exact()
+        wants.append((want, tol + 2.0 ** -8 * (want.abs() + tol)))
+    first.bounds = _dev(np.array(bounds, np.int32))
+    for _ in range(3):
+        first.run()
+    torch.cuda.synchronize()
+    assert L.lsk_device_error() == 0
+    rows, got = torch.arange(M, device="cuda")[:, None], first.out[:M].double()
+    right = torch.zeros_like(got, dtype=torch.bool)
+    owned = torch.zeros_like(rows, dtype=torch.bool)
+    for e, (want, tol) in enumerate(wants):
+        mine = (rows >= bounds[e]) & (rows < bounds[e + 1])
+        right |= mine & ((got - want).abs() <= tol)
+        owned |= mine
+    assert bool((right | ~owned).all()) and bool((got == 77.0)[~owned.expand_as(got)].all())
+
+
 def test_no_rows_and_refusals():
     c = Case([4], 64, 64)
     c.M = 0
