@@ -10,11 +10,12 @@
 // one an SM: warp 0 loads by TMA, warp 1 copies the scales to TMEM and issues the products, eight warps in two teams bring the
 // block scales, eight write the results while the next tile is computed (two accumulators).
 //
-// What bounds it. Groups of a few rows: 96 tokens through gate and up of 128 experts (2048 x 768, k = 8) take 49 us, 4.4 TB/s of
-// the weights where the memory could bring 6.7. A stage of 16 KB of unpacked weights takes its issuing warp 406 clocks, the tensor
-// pipe is active in 60 of them, and neither a second issuing warp (50 us), nor one product in place of four (43 us), nor no weights
-// at all (46 us) changed that much; scales written to TMEM by their warps in place of copies of the tensor core: 47.6 us, but 215
-// for 195 at 4096 tokens.
+// What bounds it. Groups of a few rows: 96 tokens through gate and up of 128 experts (2048 x 768, k = 8) take 46 us, 4.7 TB/s of
+// the weights where the memory could bring 6.7. At 49 us, before the descriptors of a stage came by additions, a stage of 16 KB of
+// unpacked weights took its issuing warp 406 clocks, the tensor pipe was active in 60 of them, and neither a second issuing warp
+// (50 us), nor one product in place of four (43 us), nor no weights at all (46 us) changed that much, nor do ten stages of 16 rows at
+// most in place of eight of 32 (46.5; five: 52); scales written to TMEM by their warps in place of copies of the tensor core: 47.6
+// us, but 215 for 195 at 4096 tokens.
 // Large groups: an SM's shared memory, about 133 bytes a clock of loads coming in and operands going out. From single CTAs a stage of 192
 // columns is 41 KB in and 40 KB out, 609 clocks for 384 of products; so a pair of CTAs shares a tile of 256 weight rows
 // (cta_group::2): each SM loads 128 rows of weights and one of the terms, 28 KB in and 28 KB out. 4096 tokens: up 227 -> 201 us,
@@ -703,9 +704,10 @@ cudaError_t launch_gemm_grouped_mx(const GroupedMxDesc& d, void* ws, uint32_t* e
     p.epi = d.epi;
     const int64_t pitch = mx_code_pitch(d.K);
     const int64_t apart = static_cast<const uint8_t*>(d.b2_codes) - static_cast<const uint8_t*>(d.b_codes);
-    // Groups of a few rows are bound by the weights' bytes and want single CTAs with more stages in flight: 6 rows a group take
-    // 49 us that way and 52 in pairs (up, 128 experts of 2048 x 768), 16 rows 61 and 59, 32 rows 78 and 65.
-    const bool two = M > 12ll * d.n_groups;
+    // Groups of a few rows are bound by the stages of weights that a CTA passes and want single CTAs. 128 experts of 2048 x 768, up and
+    // down: 6 rows a group take 46 and 29 us that way, 51 and 33 in pairs; 16 rows 55 and 36, 56 and 38; 24 rows down 42 and 41; 32
+    // rows up 69 and 63.
+    const bool two = M > 18ll * d.n_groups;
     p.both = p.dual && d.N % PAIR == 0 && apart != 0 && std::abs(apart) < (1ll << 40);
     p.up_first = p.both && apart < 0;
     bool ok = true;
