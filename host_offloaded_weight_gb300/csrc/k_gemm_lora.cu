@@ -9,13 +9,15 @@
 //
 // 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests.
 //
-// What bounds it. 16 rows with 14 adapters of rank 16 beside 13824 x 5120: 36 us, the weights alone (ids of no adapter) 31, the floor
-// 22; 64 rows and 24 adapters of rank 32 beside 5120 x 13824, fp32 results too: 52 us, alone 36. What the adapters add is the
-// time of the first kernel, whose loads queue behind the stream of weights (7 us by itself, 14 beside it), and the stages of `up`
-// at the end (2 to 5 us). Early requests of the product for all its stages made the first kernel's loads wait 15 us and more where
-// they went through the pair kernel, so there it starts when h is computed. One row beside 4096 x 1024 takes 14 us, a chain of
+// What bounds it. 16 rows with 14 adapters of rank 16 beside 13824 x 5120: 35 us, the weights alone (ids of no adapter) 31, the floor
+// 22; 64 rows and 24 adapters of rank 32 beside 5120 x 13824, fp32 results too: 51 us, alone 36. What the adapters add is the
+// time of the first kernel, whose loads queue behind the stream of weights (14 us for the 64 rows, 21 MB of `down`; the product
+// starts on the SMs that it leaves), and the stages of `up` at the end (5 us). One row beside 4096 x 1024 takes 14 us, a chain of
 // latencies: ids 1, first load 2.5, sums 1.5, the next kernel's look at them 1.5, `up` 2, results 1.5, and two launches.
-// 2048 rows gate/up beside 13824 x 5120 take 377 us, without adapters 324 (lsk_gemm_bf16); 4096 rows of 4096 x 1024 with rank 64 46 and 29.
+// Rows of full tiles: 2048 rows gate/up beside 13824 x 5120 take 372 us, lsk_gemm_bf16 in turn with it 341 (20 us the first kernel,
+// 8 the stages of `up`); 4096 rows of 4096 x 1024 with rank 64 45 and 30. The pair kernel starts when h is computed.
+// Tiles of fewer weight rows, so that all SMs have a share of the weights, changed nothing (13824 rows in 144 tiles of 96 in place
+// of 108 of 128: 30.8 us both, and 41 for 35 with adapters, whose kernel then finds no SM free).
 //
 // Up to 128 rows (gemm_lora_few_kernel, below): the weights are the left operand (128 rows a tile) and the tokens the
 // right one, 16 to 128 columns. Each part of `up` is looked over in shared memory before its product.
@@ -930,12 +932,13 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     // its tensor memory: one that waited for another's could hold up its cluster, and that the other.
     p.chains = std::min(4, 256 / p.run);
     p.tmem_cols = p.chains * p.run;
-    // 64 KB and more of loads in flight; the products read 128 rows of the last stage's left operand, whatever lies behind it
+    // 80 KB of loads in flight; the products read 128 rows of the last stage's left operand, whatever lies behind it
     const int stage = (p.block_cols + p.run) * 128;
-    p.stages = std::max(3, std::min(ROWS_MAX_STAGES, 65536 / stage));
+    p.stages = std::max(3, std::min(ROWS_MAX_STAGES, 81920 / stage));
     // A cluster for each run of rows and columns and each gang that there may be (few rows) or two adapters (a full tile has few), over
-    // slices of 96 KB and more; as many as are resident together, two an SM.
-    const int64_t runs = p.tiles * (p.tile_rows / p.run) * p.col_runs, room = 2 * gemm_num_sms() - (few ? 0 : LOOK_CTAS / 2);
+    // slices of 96 KB and more; as many as are resident together, two an SM, beside some that look adapters over (1024 rows of 16
+    // adapters, 5120 x 13824: 161 us; 174 with 48 more places left to those and 64 KB in flight).
+    const int64_t runs = p.tiles * (p.tile_rows / p.run) * p.col_runs, room = 2 * gemm_num_sms() - (few ? 0 : LOOK_CTAS / 4);
     p.slots = few ? (most_adapters + p.gang - 1) / p.gang : std::min(p.cap, 2);
     p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (int64_t)p.k_stages * stage / 98304, room / (runs * p.slots)}));
     if (few && runs * p.slots * p.slices <= gemm_num_sms()) p.stages = std::min(ROWS_MAX_STAGES, 131072 / stage);  // an SM to itself
