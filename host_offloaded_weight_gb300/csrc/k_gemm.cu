@@ -98,6 +98,11 @@ struct LoraGemmParams : GemmParams {
     const uint8_t* lora_notes;  // [adapter][16] not all zero: not finite, read as zeros (its last term of h is NaN)
     int lora_cap, lora_cw, lora_chunks, lora_parts, lora_rank, lora_terms;
 };
+// With fp32 results, which would show that the tensor core cuts its fp32 sums off: an accumulator takes `chain` stages at a time,
+// and the epilogue's warps add the chains up in registers.
+struct LoraChainGemmParams : LoraGemmParams {
+    int chain;
+};
 
 // ------------------------------------------------------------------ PTX helpers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -195,6 +200,12 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -837,9 +848,9 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
     return v;
 }
 
-template <int EPI, bool DUAL, int BN, bool ONE = false, bool LORA = false>
+template <int EPI, bool DUAL, int BN, bool ONE = false, bool LORA = false, bool CHAINS = false>
 __global__ void __launch_bounds__(s2_threads(EPI), 1)
-    gemm_bf16_tc2(const __grid_constant__ std::conditional_t<LORA, LoraGemmParams, GemmParams> p) {
+    gemm_bf16_tc2(const __grid_constant__ std::conditional_t<CHAINS, LoraChainGemmParams, std::conditional_t<LORA, LoraGemmParams, GemmParams>> p) {
     static_assert(BN % 32 == 0 && BN >= 64 && BN <= 256 && (!DUAL || BN == 256), "tile width");
     static_assert(!ONE || s2_out_f32(EPI), "one-tile layout: residual epilogues");
     extern __shared__ uint8_t smem_raw[];
@@ -850,6 +861,7 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
     constexpr int S2_STAGE = s2_stage_bytes(BN);
     constexpr int WSB = s2_warp_bytes(EPI, ONE);
     constexpr bool OUT32 = s2_out_f32(EPI);
+    static_assert(!CHAINS || (LORA && OUT32), "chains: products with adapters and fp32 results");
     constexpr int NBUF = s2_nbuf(EPI);
     const uint32_t stg0 = base + S2_STAGES * S2_STAGE;  // epilogue staging tiles, WSB bytes per warp
     constexpr int EW = s2_epi_warps(EPI);
@@ -988,31 +1000,52 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
             int it = 0, tcount = 0;
             bool ok = true;
             [[maybe_unused]] bool waited = false;
+            [[maybe_unused]] int chains = 0, left = 0;
             for (int t = cluster_id; t < num_tiles && ok; t += n_clusters, ++tcount) {
                 const int buf = tcount & 1;
                 const uint32_t tph = (uint32_t)(tcount >> 1) & 1u;
-                if (!mbar_wait(tempty_bar(buf), tph ^ 1u, p.err, 2, p.mbar_limit_ns) || s_abort) {
+                if (!CHAINS && (!mbar_wait(tempty_bar(buf), tph ^ 1u, p.err, 2, p.mbar_limit_ns) || s_abort)) {
                     s_abort = 1;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(buf * ACC_COLS);
-                for (int kb = 0; kb < kb_n; ++kb, ++it) {
-                    const int s = it % S2_STAGES;
-                    const uint32_t ph = (uint32_t)(it / S2_STAGES) & 1u;
-                    if (!mbar_wait(full_bar(s), ph, p.err, 3, p.mbar_limit_ns)) {
+                uint32_t d = tmem_base + (uint32_t)(buf * ACC_COLS);
+                [[maybe_unused]] auto begin = [&]() {  // the accumulator of a chain
+                    if (!mbar_wait(tempty_bar(chains & 1), ((uint32_t)(chains >> 1) & 1u) ^ 1u, p.err, 2, p.mbar_limit_ns) || s_abort) {
                         ok = false;
                         s_abort = 1;
-                        break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = base + s * S2_STAGE;
-                    const uint32_t sb = sa + S2_A;
+                    d = tmem_base + (uint32_t)((chains & 1) * ACC_COLS);
+                    return ok;
+                };
+                for (int kb = 0; kb < kb_n && ok;) {
+                    const int kb0 = kb;
+                    int kb1 = kb_n;
+                    if constexpr (CHAINS) {
+                        kb1 = min(kb_n - kb, p.chain) + kb;
+                        if (!begin()) break;
+                    }
+                    for (; kb < kb1; ++kb, ++it) {
+                        const int s = it % S2_STAGES;
+                        const uint32_t ph = (uint32_t)(it / S2_STAGES) & 1u;
+                        if (!mbar_wait(full_bar(s), ph, p.err, 3, p.mbar_limit_ns)) {
+                            ok = false;
+                            s_abort = 1;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = base + s * S2_STAGE;
+                        const uint32_t sb = sa + S2_A;
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        umma2_bf16(d, make_sdesc(sa + kk * 32), make_sdesc(sb + kk * 32), IDESC,
-                                   (kb > 0 || kk > 0) ? 1u : 0u);
-                    umma2_commit_both(empty_bar(s));
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            umma2_bf16(d, make_sdesc(sa + kk * 32), make_sdesc(sb + kk * 32), IDESC,
+                                       (kb > kb0 || kk > 0) ? 1u : 0u);
+                        umma2_commit_both(empty_bar(s));
+                    }
+                    if constexpr (CHAINS) {
+                        if (ok) umma2_commit_both(tfull_bar(chains++ & 1));
+                    }
                 }
                 if constexpr (LORA) {
                     if (!waited) grid_dep_wait();
@@ -1020,6 +1053,13 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                     const int more = ok ? p.lora_count[t % num_m2] * p.lora_parts * p.lora_terms : 0, cw = p.lora_cw;
                     int term = 0, chunk = 0;
                     for (int e = 0; e < more; ++e, ++it) {
+                        const bool starts = CHAINS && left == 0;
+                        if constexpr (CHAINS) {
+                            if (starts) {
+                                if (!begin()) break;
+                                left = p.chain;
+                            }
+                        }
                         const int s = it % S2_STAGES;
                         if (!mbar_wait(full_bar(s), (uint32_t)(it / S2_STAGES) & 1u, p.err, 3, p.mbar_limit_ns)) {
                             ok = false;
@@ -1028,17 +1068,22 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
                         }
                         tc_fence_after();
                         const uint32_t sa = base + s * S2_STAGE;
-                        const int left = min(cw, p.lora_rank - chunk * cw);
+                        const int cols = min(cw, p.lora_rank - chunk * cw);
                         if (++term == p.lora_terms) {
                             term = 0;
                             if (++chunk == p.lora_chunks) chunk = 0;
                         }
-                        for (int kk = 0; kk < (left + 15) / 16; ++kk)
-                            umma2_bf16(d, make_sdesc_narrow(sa + kk * 32, cw), make_sdesc_narrow(sa + S2_A + kk * 32, cw), IDESC, 1u);
+                        for (int kk = 0; kk < (cols + 15) / 16; ++kk)
+                            umma2_bf16(d, make_sdesc_narrow(sa + kk * 32, cw), make_sdesc_narrow(sa + S2_A + kk * 32, cw), IDESC,
+                                       starts && kk == 0 ? 0u : 1u);
                         umma2_commit_both(empty_bar(s));
+                        if (CHAINS && (--left == 0 || e + 1 == more)) {
+                            umma2_commit_both(tfull_bar(chains++ & 1));
+                            left = 0;
+                        }
                     }
                 }
-                if (ok) umma2_commit_both(tfull_bar(buf));
+                if (!CHAINS && ok) umma2_commit_both(tfull_bar(buf));
             }
             umma2_commit_both(done_bar);
             mbar_wait(done_bar, 0, p.err, 6, p.mbar_limit_ns);
@@ -1118,12 +1163,82 @@ __global__ void __launch_bounds__(s2_threads(EPI), 1)
             if (NBUF == 2) sb ^= 1;
         };
         int tcount = 0;
+        [[maybe_unused]] int chains = 0;
         for (int t = cluster_id; t < num_tiles; t += n_clusters, ++tcount) {
             const int buf = tcount & 1;
             const uint32_t tph = (uint32_t)(tcount >> 1) & 1u;
             const int m2 = t % num_m2, n = t / num_m2;
             const int row0 = m2 * 256 + (int)rank * 128 + q * 32;
             const int nbase = DUAL ? n * 128 : n * BN;
+            bool whole = false;
+            if constexpr (CHAINS) {
+                // the residual into L2 meanwhile: registers and tensor memory are full of sums
+                if (row0 + lane < p.M)
+                    for (int c = nbase + c_begin * 32; c < min(nbase + (c_begin + n_chunks) * 32, p.N); c += 8)
+                        if (const int64_t at = (int64_t)(row0 + lane) * p.ldr + c; p.resid_f32 || (c & 15) == 0)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p.resid) + at * (p.resid_f32 ? 4 : 2)));
+                float sum[PER_WARP][32];
+#pragma unroll
+                for (int i = 0; i < PER_WARP; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
+                auto collect = [&](int stages) {  // the chains of so many stages
+                    for (int k = 0; k < stages; k += min(p.chain, stages - k), ++chains) {
+                        const int b = chains & 1;
+                        if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(b), (uint32_t)(chains >> 1) & 1u, p.err, 4, p.mbar_limit_ns) && !s_abort)) {
+                            s_abort = 1;
+                            return false;
+                        }
+                        tc_fence_after();
+                        const uint32_t from = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * ACC_COLS + c_begin * 32);
+#pragma unroll
+                        for (int i = 0; i < PER_WARP; ++i) {
+                            if (i >= n_chunks) continue;
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t r[16];
+                                tmem_ld16(from + i * 32 + h, r);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) sum[i][h + j] += __uint_as_float(r[j]);
+                            }
+                        }
+                        release(b);
+                    }
+                    return true;
+                };
+                if (!collect(kb_n)) break;
+                if (tcount == 0) grid_dep_wait();
+                if (!collect(p.lora_count[m2] * p.lora_parts * p.lora_terms)) break;
+                float4 g[8];
+                issue(row0, nbase + c_begin * 32, g);
+#pragma unroll
+                for (int i = 0; i < PER_WARP; ++i) {
+                    const int n0 = nbase + (c_begin + i) * 32;
+                    if (i >= n_chunks) continue;
+                    const bool in = n0 < p.N && row0 < p.M;  // uniform across the warp
+                    const uint32_t s32 = stg + NBUF * S2_STG_BF + (uint32_t)sb * S2_STG_F32;
+                    if (in) {
+                        if (EPI == EPI_BIAS_RESID) add_bias_row(p, n0, sum[i]);
+                        if (lane == 0) bulk_wait_read<0>();  // the previous chunk's stores have left the staging tiles
+                        __syncwarp();
+#pragma unroll
+                        for (int it = 0; it < 8; ++it) st_shared_f4(s32 + 16u * sw4(it * 4 + rsub, c4), g[it]);
+                        __syncwarp();
+                    }
+                    if (i + 1 < n_chunks) issue(row0, n0 + 32, g);
+                    if (!in) continue;
+                    // each lane reads (and below overwrites) only its own row
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 t4 = ld_shared_f4(s32 + 16u * sw4(lane, j));
+                        sum[i][4 * j] += t4.x; sum[i][4 * j + 1] += t4.y; sum[i][4 * j + 2] += t4.z; sum[i][4 * j + 3] += t4.w;
+                    }
+                    store_chunk(sum[i], n0, row0, 0);
+                }
+                whole = true;
+            }
+            if (whole) continue;
             // GELU epilogue: the bias of this warp's first two chunks, one value per lane (more
             // chunks are rare: they read theirs after the wait)
             const bool has_bias = EPI == EPI_BIAS_GELU;
@@ -1393,7 +1508,7 @@ cudaError_t launch_t(const GemmParams& p, int grid, cudaStream_t s) {
 
 template <int EPI, bool DUAL, int BN, bool ONE = false, class P = GemmParams>
 cudaError_t launch_t2(const P& p, int clusters, cudaStream_t s) {
-    auto kern = gemm_bf16_tc2<EPI, DUAL, BN, ONE, std::is_same_v<P, LoraGemmParams>>;
+    auto kern = gemm_bf16_tc2<EPI, DUAL, BN, ONE, std::is_base_of_v<LoraGemmParams, P>, std::is_same_v<P, LoraChainGemmParams>>;
     static SmemAllowance allowed;
     const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(kern), s2_smem_bytes(EPI, BN, ONE));
     if (e != cudaSuccess) return e;
@@ -1630,7 +1745,7 @@ cudaError_t launch_gemm_bf16(const GemmDesc& d, int max_ctas, cudaStream_t s) {
 // The pair kernel with its adapters' columns. The maps of the blocks and of `up` are made for each call.
 cudaError_t launch_gemm_bf16_lora(const GemmDesc& d, const LoraArgs& l, int64_t h_rows, cudaStream_t s) {
     const bool dual = d.epi == EPI_SWIGLU;
-    LoraGemmParams p;
+    LoraChainGemmParams p;
     memset(&p, 0, sizeof(p));
     const int bn = dual ? 256 : gemm_pair_tile_n(d.M, d.N), b_box = dual ? 128 : bn / 2;
     if (!cached_tmap(&p.tmA, d.A, d.M, d.K, d.lda, 128) || !cached_tmap(&p.tmB, d.B, d.b_rows, d.K, d.ldb, b_box) ||
@@ -1665,15 +1780,20 @@ cudaError_t launch_gemm_bf16_lora(const GemmDesc& d, const LoraArgs& l, int64_t 
     p.lora_parts = l.parts;
     p.lora_rank = l.rank;
     p.lora_terms = l.terms;
+    // Off by (2048 x 1024, 5120 x 5120, 5120 x 13824) 3.1, 3.5 and 5.2 e-7 of their norm with chains of 8, 6.2, 6.1 and 7.2 with 16, 6.2, 32
+    // and 91 in one; a chain of fp32 additions is off by 2.5, 7 and 13. 1024 rows of 5120 x 13824: 190, 178 and 161 us.
+    p.chain = d.K <= 2048 ? 8 : 16;
+    const LoraGemmParams& plain = p;
     const int64_t tiles = (d.M + 255ll) / 256 * p.num_n_tiles;
     if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
     const int clusters = (int)std::min<int64_t>(std::max(1, gemm_num_sms() / 2), tiles);
     switch (d.epi) {
-        case EPI_STORE: return launch_t2_bn<EPI_STORE, false>(p, bn, clusters, s);
-        case EPI_BIAS_GELU: return launch_t2_bn<EPI_BIAS_GELU, false>(p, bn, clusters, s);
-        case EPI_BIAS_RESID: return launch_t2_bn<EPI_BIAS_RESID, false>(p, bn, clusters, s);
-        case EPI_RESID: return launch_t2_bn<EPI_RESID, false>(p, bn, clusters, s);
-        case EPI_SWIGLU: return launch_t2<EPI_SWIGLU, true, 256>(p, clusters, s);
+        case EPI_STORE: return launch_t2_bn<EPI_STORE, false>(plain, bn, clusters, s);
+        case EPI_BIAS_GELU: return launch_t2_bn<EPI_BIAS_GELU, false>(plain, bn, clusters, s);
+        case EPI_BIAS_RESID:
+            return d.C32 ? launch_t2_bn<EPI_BIAS_RESID, false>(p, bn, clusters, s) : launch_t2_bn<EPI_BIAS_RESID, false>(plain, bn, clusters, s);
+        case EPI_RESID: return d.C32 ? launch_t2_bn<EPI_RESID, false>(p, bn, clusters, s) : launch_t2_bn<EPI_RESID, false>(plain, bn, clusters, s);
+        case EPI_SWIGLU: return launch_t2<EPI_SWIGLU, true, 256>(plain, clusters, s);
     }
     return cudaErrorInvalidValue;
 }
