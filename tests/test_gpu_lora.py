@@ -255,6 +255,14 @@ def test_gangs_of_few_rows_adapters(T, K, r, n, used, epi):
     Case(T, 200, K, r, n, epi, ids=ids, seed=5).run().check()
 
 
+@pytest.mark.parametrize("epi", ["resid", "resid_only"])
+@pytest.mark.parametrize("T,N,K,r,n", [(700, 8008, 1096, 72, 9), (520, 7000, 2312, 256, 3), (1100, 4096, 2048, 8, 1100), (257, 200, 8, 16, 1)])
+def test_chains_of_fp32_results_over_several_tiles(T, N, K, r, n, epi):
+    """More tiles than pairs of SMs, chains cut short by the end of K and of the adapters, every id none's in some rows."""
+    Case(T, N, K, r, n, epi, seed=7).run().check()
+    Case(T, N, K, r, n, epi, ids=[-1] * T, seed=7).run().check()
+
+
 @pytest.mark.parametrize("T", [40, 300])
 def test_the_residual_stream_in_place(T):
     """C32 over the residual that it takes: every element is read before it is written."""
