@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(Cfg<MAXC, TWO>::THREADS, 1) gemm_grouped_mx_ke
             const int g = g0 + lane;
             int t = 0;
             if (g < p.n_groups) {
-                const int r0 = max(p.bounds[g], 0), r1 = min(p.bounds[g + 1], p.M), c = max(r1 - r0 + CHUNK - 1, 0) / CHUNK;
+                // cut at both ends: the difference of an entry of the largest magnitude and one of the other sign would wrap
+                const int r0 = min(max(p.bounds[g], 0), p.M), r1 = min(max(p.bounds[g + 1], 0), p.M), c = max(r1 - r0 + CHUNK - 1, 0) / CHUNK;
                 t = (c + MAXC - 1) / MAXC;
                 groups.row[g] = r0;
                 groups.end[g] = r1;
