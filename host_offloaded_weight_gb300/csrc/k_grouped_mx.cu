@@ -568,8 +568,9 @@ __device__ __forceinline__ void split8_half(uint4 raw, uint2& o1, uint2& o2, uin
     m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
     m = max(m & 0xffffu, m >> 16);
     const uint32_t e = m >> 7;
-    // blocks next to either end of the range: the general form (all lanes of the warp work together in it)
-    if (__any_sync(0xffffffffu, e >= TOP_FIELD || (e < 32 && e > 0))) {
+    // blocks next to either end of the range, subnormal ones among them, whose terms' scales are not 2^5 apart: the general form
+    // (all lanes of the warp work together in it). Zeros, as of padding, are right in either.
+    if (__any_sync(0xffffffffu, e >= TOP_FIELD || (e < 32 && m > 0))) {
         split8(raw, o1, o2, b1, b2);
         return;
     }

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from host_offloaded_weight_gb300 import lstream as L
+from oracle import mxfp4 as mx
 from test_gpu_grouped_mxfp4 import Case as Grouped
 from test_gpu_grouped_mxfp4 import _dev
 
@@ -42,3 +43,30 @@ def test_bounds_of_any_value_are_cut_to_the_rows(bounds, M, epi):
     for g in range(n):
         none &= ~((rows >= bounds[g]) & (rows < bounds[g + 1]))
     assert bool((got[place[none]] == 77.0).all())
+
+
+# exponent fields of blocks of 32: subnormal, next to either border of the split's quick form and of the range, ordinary; -1: zeros
+FIELDS = [0, 127, -1, 1, 31, 0, 32, 33, 253, 254, 0, 0, 127, 12]
+
+
+@pytest.mark.parametrize("epi", ["store", "scale"])
+@pytest.mark.parametrize("sizes", [[9, 20], [150, 200]])
+@pytest.mark.parametrize("fields", [FIELDS, [0] * 8, [0, -1, 127, 200] * 4, [31, 0] * 5], ids=lambda f: "_".join(map(str, f)))
+def test_blocks_of_every_magnitude_count_alike(fields, sizes, epi):
+    """Weights whose blocks undo the rows' magnitudes, so that a block's part of the result does not drown in another's."""
+    N, K = 136, 32 * len(fields)
+    c = Grouped(sizes, N, K, epi)
+    r = np.random.default_rng(len(fields))
+    f = np.array(fields)[np.stack([r.permutation(len(fields)) for _ in range(2)])]       # an order of blocks for each group
+    c.codes, c.scales, c.values, bits = [], [], [], []
+    for e in range(2):
+        field = f[e].repeat(32)
+        mant = np.where(r.random((sizes[e], K)) < 0.3, r.integers(0x78, 0x80, (sizes[e], K)), r.integers(1, 0x80, (sizes[e], K)))
+        bits.append(np.where(field < 0, 0, r.integers(0, 2, (sizes[e], K)) << 15 | np.maximum(field, 0) << 7 | mant).astype(np.uint16))
+        codes, scales = mx.encode(r.standard_normal((N, K)) * np.exp2(np.clip(127.0 - field, -120, 120)))
+        c.values.append(_dev(mx.decode(codes, scales, K)))
+        c.codes.append(_dev(codes))
+        c.scales.append(_dev(scales))
+    c.values, c.codes, c.scales = [torch.stack(c.values)], [torch.stack(c.codes)], [torch.stack(c.scales)]
+    c.A = _dev(np.concatenate(bits).view(np.int16)).view(torch.bfloat16)
+    c.run().check()
