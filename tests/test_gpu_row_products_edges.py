@@ -70,3 +70,28 @@ def test_blocks_of_every_magnitude_count_alike(fields, sizes, epi):
     c.values, c.codes, c.scales = [torch.stack(c.values)], [torch.stack(c.codes)], [torch.stack(c.scales)]
     c.A = _dev(np.concatenate(bits).view(np.int16)).view(torch.bfloat16)
     c.run().check()
+
+
+@pytest.mark.parametrize("M", [40, 640])
+def test_gates_far_below_zero_keep_their_share(M):
+    """SiLU(g) = g / (1 + e^-g) beyond the g where e^-g leaves the range of fp32 or of a fast division, beside up values that bring
+    it back. e^g by __expf is within 2 + 1.173 |g| units in the last place, 2^-16 of it for these g, and within 2^-149 where it is
+    subnormal; a product with g that is subnormal within 2^-150 more; the result's rounding 2^-8."""
+    K, N = 64, 24
+    one, other = np.zeros((N, K)), np.zeros((N, K))
+    one[:, 0] = one[:, 1] = 1.0
+    other[:, 32] = 1.0
+    (gc, gs), (uc, us) = mx.encode(one), mx.encode(other)
+    i = np.arange(M) * 640 // M
+    A = torch.zeros((M, K))
+    A[:, 0], A[:, 1], A[:, 32] = torch.from_numpy(-60.0 - i // 16), torch.from_numpy(-(i % 16) / 16.0), 2.0 ** 110     # gates -60 to -99.9
+    out = torch.full((M + 1, N), 77.0, dtype=torch.bfloat16, device="cuda")
+    b = _dev(np.array([0, M], np.int32))
+    L.lsk_gemm_grouped_bf16_mxfp4(L.LSK_EPI_SWIGLU, A.to(torch.bfloat16).cuda(), _dev(gc)[None], _dev(gs)[None], b, 1, out, M, N, K,
+                                  B2_codes=_dev(uc)[None], B2_scales=_dev(us)[None])
+    torch.cuda.synchronize()
+    assert L.lsk_device_error() == 0 and bool((out[M] == 77.0).all())
+    g = (A[:, 0] + A[:, 1]).double().cuda()[:, None]
+    want = g * torch.sigmoid(g) * 2.0 ** 110
+    tol = 2.0 ** -16 * want.abs() + (g.abs() + 1) * 2.0 ** -149 * 2.0 ** 110
+    assert bool(((out[:M].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
