@@ -109,15 +109,18 @@ __device__ __forceinline__ float near_bf16(float v) {
     const float h = __bfloat162float(__float2bfloat16_rn(v));
     return isinf(h) && !isinf(v) ? __bfloat162float(__float2bfloat16_rz(v)) : h;
 }
-constexpr int ROWS_PROD = 0, ROWS_MMA = 1, ROWS_EPI = 2;   // warps; four of the epilogue
+constexpr int ROWS_PROD = 0, ROWS_MMA = 1, ROWS_EPI = 2, ROWS_EPI_WARPS = 4;
+constexpr int ROWS_CHAIN = 16;        // stages that an accumulator takes at most where h has three terms
 
+// ROUNDS: h in three terms from slices too long for its chains.
+template <bool ROUNDS>
 __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) int s_ids[MAX_TILE];
     __shared__ int s_list[MAX_TILE];
     __shared__ int s_warp[ROWS_THREADS / 32];
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(8) uint64_t s_bars[2 * ROWS_MAX_STAGES + 2];
+    __shared__ __align__(8) uint64_t s_bars[2 * ROWS_MAX_STAGES + 4];
     __shared__ volatile int stop;
     if ((int)blockIdx.x >= p.rows_ctas) {
         look_over(p, (int)blockIdx.x - p.rows_ctas, (int)gridDim.x - p.rows_ctas);
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     const uint32_t bars = smem_addr(s_bars);
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (ROWS_MAX_STAGES + s); };
-    const uint32_t acc_full = bars + 8u * 2 * ROWS_MAX_STAGES, red_full = acc_full + 8u;
+    const uint32_t acc_full = bars + 8u * 2 * ROWS_MAX_STAGES, red_full = acc_full + 8u, round_full = acc_full + 16u, round_empty = acc_full + 24u;
     // slices (a cluster) innermost, then runs of columns, slots, runs of rows
     int at = (int)blockIdx.x;
     const int slice = at % p.slices;
@@ -149,6 +152,8 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
         }
         bar_init(acc_full, 1);
         bar_init(red_full, 1);
+        bar_init(round_full, 1);
+        bar_init(round_empty, ROWS_EPI_WARPS);
         bar_init_fence();
         tma_desc_prefetch(&p.map_x);
         tma_desc_prefetch(&p.map_down);
@@ -197,7 +202,9 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     const int k0 = (int)((int64_t)slice * p.k_stages / p.slices), k1 = (int)((int64_t)(slice + 1) * p.k_stages / p.slices);
     // (divisions by numbers that only the launch knows take 150 clocks each: counters and shifts below)
     const int log_cw = p.cw == 16 ? 4 : p.cw == 32 ? 5 : 6;
-    const int chains = min(k1 - k0, p.chains);
+    // Rounds of stages: between two, the epilogue's warps add the accumulators to the sums so far, which lie behind them.
+    const int rounds = ROUNDS && k1 - k0 > p.round ? (k1 - k0 + p.round - 1) / p.round : 1;
+    const int chains = min(k1 - k0 - (rounds - 1) * p.round, p.chains);   // of the last round
     const int own_cols = min(128, p.parts * p.cw - col0), part0 = col0 >> log_cw, parts = own_cols >> log_cw;   // of an adapter
     // the finish: a thread has the same two columns of every row, of an adapter of the gang
     const int log_units = 31 - __clz(own_cols * p.gang) - 1, log_own = 31 - __clz(own_cols), c = (tid & ((1 << log_units) - 1)) * 2;
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
     const int groups = p.run / 8, own_groups = (groups + p.slices - 1) / p.slices;
     const int q = warp & 3, col = 32 * q + lane;   // the epilogue: q the TMEM lane quarter that a warp can read, col the lane's column
     const int rows = min(p.run, p.T - t0 - row0);  // rows that exist (zero and less: none)
-    int it = 0, turn = 0;                          // stages and adapters so far
+    int it = 0, turn = 0, joined = 0;              // stages, adapters and rounds before an adapter's last so far
     bool left = false, came = true;                // everything is sent; everything is here
     int ring = 0;                                  // the place of the next stage, and the parity of its use
     uint32_t parity = 0;
@@ -252,8 +259,19 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             } else if (warp == ROWS_MMA) {
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.run >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
                 const bool one = elect_one();
-                for (int k = k0; k < k1; ++k, step()) {
+                int taken = 0;                     // stages of the round
+                for (int k = k0; k < k1; ++k, ++taken, step()) {
                     const int s = ring;
+                    if (ROUNDS && taken == p.round) {
+                        if (one) mma_commit(round_full);
+                        __syncwarp();
+                        if (!bar_wait_warp(round_empty, (uint32_t)joined++ & 1u, p.err, 12)) {
+                            stop = 1;
+                            break;
+                        }
+                        fence_after_sync();
+                        taken = 0;
+                    }
                     if (!bar_wait_warp(full(s), parity, p.err, 3)) {
                         stop = 1;
                         break;
@@ -263,8 +281,8 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
                         const uint32_t sp = base + s * stage;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16(tmem + (uint32_t)(((k - k0) & (p.chains - 1)) * p.run), operand_desc(sp + 32 * i), operand_desc(sp + down_bytes + 32 * i), idesc,
-                                     k - k0 >= p.chains || i ? 1u : 0u);
+                            mma_bf16(tmem + (uint32_t)((taken & (p.chains - 1)) * p.run), operand_desc(sp + 32 * i), operand_desc(sp + down_bytes + 32 * i), idesc,
+                                     taken >= p.chains || i ? 1u : 0u);
                         mma_commit(empty(s));
                     }
                     __syncwarp();
@@ -292,6 +310,41 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             if (s_ids[row0 + r] == a) return;
             for (int t = 0; t < p.blocks_terms; ++t) to[t * term] = 0;
         });
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16), whole = lanes + (uint32_t)(p.chains * p.run);
+        // eight rows' sums of this lane's column: of the rounds before, of so many accumulators
+        auto sums = [&](int g, bool before, int accumulators, float (&v)[8]) {
+            uint32_t x[8];
+            if (ROUNDS && before) {
+                tmem_load8(whole + 8 * g, x);
+                tmem_load_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[i]);
+            }
+            for (int c = 0; c < accumulators; ++c) {
+                tmem_load8(lanes + (uint32_t)(c * p.run + 8 * g), x);
+                tmem_load_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = c || (ROUNDS && before) ? v[i] + __uint_as_float(x[i]) : __uint_as_float(x[i]);
+            }
+        };
+        if (ROUNDS && any && warp >= ROWS_EPI && warp < ROWS_EPI + ROWS_EPI_WARPS)
+            for (int r = 1; r < rounds; ++r) {
+                if (!bar_wait_warp(round_full, (uint32_t)joined++ & 1u, p.err, 13)) {
+                    stop = 1;
+                    break;
+                }
+                fence_after_sync();
+                if (32 * q < cols)
+                    for (int g = 0; g < groups && 8 * g < rows; ++g) {
+                        float v[8];
+                        sums(g, r > 1, p.chains, v);
+                        tmem_store8(whole + 8 * g, v);
+                    }
+                tmem_store_wait();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) bar_arrive(round_empty);
+            }
         if (any) {
             const bool done = bar_wait_warp(acc_full, (uint32_t)turn & 1u, p.err, 4);   // every warp: nobody is ahead by an adapter
             if (!done) stop = 1;
@@ -306,16 +359,10 @@ __global__ void __launch_bounds__(ROWS_THREADS) lora_rows_kernel(const __grid_co
             fence_after_sync();
             ++turn;
             // every CTA's sums of a row go to the CTA that has it
-            if (warp >= ROWS_EPI && warp < ROWS_EPI + 4 && 32 * q < cols)
+            if (warp >= ROWS_EPI && warp < ROWS_EPI + ROWS_EPI_WARPS && 32 * q < cols)
                 for (int g = 0, owner = 0, l = 0; g < groups && 8 * g < rows; ++g) {
                     float v[8];
-                    for (int c = 0; c < chains; ++c) {
-                        uint32_t x[8];
-                        tmem_load8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c * p.run + 8 * g), x);
-                        tmem_load_wait();
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = c ? v[i] + __uint_as_float(x[i]) : __uint_as_float(x[i]);
-                    }
+                    sums(g, rounds > 1, chains, v);
                     const uint32_t to = smem_addr(red + ((slice * own_groups + l) * 8) * p.block_cols + col);
                     if (col < cols) {
                         if (p.slices == 1) {
@@ -943,6 +990,15 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     p.slices = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_SLICES, (int64_t)p.k_stages * stage / 98304, room / (runs * p.slots)}));
     if (few && runs * p.slots * p.slices <= gemm_num_sms()) p.stages = std::min(ROWS_MAX_STAGES, 131072 / stage);  // an SM to itself
     while (!few && 2 * p.slots <= p.cap && runs * p.slices * 2 * p.slots <= room) p.slots *= 2;
+    // Slices that are long all the same (many rows or adapters, K beyond 8 slices) are taken in rounds where h has three terms, with
+    // half of the accumulators and the sums so far in place of the others. The adapters' part of fp32 results at K = 13824, of its norm
+    // (us beside 5120, 2048 and 1024 weight rows): 128 rows, as many adapters of rank 256, off by 7.8e-6 in one round (524), 1.1e-6
+    // now (570); 4096 rows, 64 of rank 64, 2.0 and 1.2e-6 (1303, 1436); 16384 rows, 2 of rank 16, 7.7 and 1.1e-6 (474, 498).
+    p.round = p.k_stages;
+    if (p.terms == 3 && (p.k_stages + p.slices - 1) / p.slices > ROWS_CHAIN * p.chains) {
+        p.chains /= 2;
+        p.round = ROWS_CHAIN * p.chains;
+    }
     const int groups = p.run / 8, red = p.slices * ((groups + p.slices - 1) / p.slices) * 8 * p.block_cols * 4;
     // not less than 80 KB: a third CTA of an SM would wait for tensor memory
     const int smem = std::max(80 * 1024, 1024 + p.stages * stage + std::max(red, 128 * 128));
@@ -951,8 +1007,10 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     if (rows + looks > 0x7fffffffll) return cudaErrorInvalidValue;
     p.rows_ctas = (int)rows;
     if (!lora_map(&p.map_x, p.x, p.T, p.K, 64, p.run, 0, 0) || !map_down(&p.map_down, p, dual ? 2 : 1)) return cudaErrorInvalidValue;
-    static SmemAllowance allowed;
-    const cudaError_t e = allowed.ensure(reinterpret_cast<const void*>(lora_rows_kernel), smem);
+    const bool rounds = p.round < p.k_stages;
+    auto kern = rounds ? lora_rows_kernel<true> : lora_rows_kernel<false>;
+    static SmemAllowance allowed[2];
+    const cudaError_t e = allowed[rounds].ensure(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = config(dim3((unsigned)(rows + looks)), ROWS_THREADS, smem, s, at, false);
@@ -961,7 +1019,7 @@ cudaError_t launch_rows(LoraArgs& p, bool dual, cudaStream_t s) {
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.numAttrs = p.slices > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, lora_rows_kernel, p);
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int NQ, int PACK>

@@ -144,7 +144,7 @@ struct LoraArgs {
     int64_t tiles;
     // the first kernel's grid
     CUtensorMap map_x, map_down;
-    int run, gang, block_cols, col_runs, k_stages, chains, tmem_cols, stages, slots, slices, rows_ctas;
+    int run, gang, block_cols, col_runs, k_stages, chains, round, tmem_cols, stages, slots, slices, rows_ctas;
     uint32_t* err;
     // in scratch
     int* count;               // [tiles] adapters of a tile

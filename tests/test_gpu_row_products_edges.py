@@ -1,4 +1,4 @@
-"""Products whose weights differ by rows, at the ends of what their arguments may be."""
+"""Products whose weights differ by rows, at the ends of what their arguments may be, and the precision of fp32 results."""
 import numpy as np
 import pytest
 import torch
@@ -7,6 +7,7 @@ from host_offloaded_weight_gb300 import lstream as L
 from oracle import mxfp4 as mx
 from test_gpu_grouped_mxfp4 import Case as Grouped
 from test_gpu_grouped_mxfp4 import _dev
+from test_gpu_lora import Case as Lora
 
 pytestmark = pytest.mark.gpu
 LOW, HIGH = -2 ** 31, 2 ** 31 - 1
@@ -95,3 +96,35 @@ def test_gates_far_below_zero_keep_their_share(M):
     want = g * torch.sigmoid(g) * 2.0 ** 110
     tol = 2.0 ** -16 * want.abs() + (g.abs() + 1) * 2.0 ** -149 * 2.0 ** 110
     assert bool(((out[:M].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
+
+
+# The precision of fp32 results, by norm: a bound on each value as the other tests have it (K 2^-23 of the sum of magnitudes) would let
+# a single long chain of tensor core sums pass, and h in two terms. A tensor core cuts its sums off: a product takes in 16 values of K
+# and loses half of a last bit on average, 2^-25 of the sum so far, always towards zero. A chain of c stages of 64 values is 4 c products,
+# so a result is off by at most 4 c 2^-25 of its norm. Fewer additions in registers than products follow, and the last
+# roundings: 2^-23. (Two terms of h instead of three are off by up to 2^-18 of it.)
+def _cut(products):
+    return products * 2.0 ** -25 + 2.0 ** -23
+
+
+def _error(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("T,K,r,n,stages", [(20, 256, 16, 4, 1), (64, 200, 40, 9, 1), (20, 13824, 32, 8, 16), (128, 13824, 256, 128, 16), (128, 13824, 8, 128, 16),
+                                            (70, 40000, 16, 3, 16), (300, 256, 24, 5, 2), (300, 13824, 16, 3, 16), (4096, 13824, 64, 64, 16),
+                                            (2100, 30000, 136, 40, 16), (16384, 13824, 16, 2, 16)])
+def test_the_adapters_part_alone_has_its_24_bits(T, K, r, n, stages):
+    """h from many slices of K and from few (many rows, many adapters, a long K): chains of 16 stages at most."""
+    c = Lora(T, 136, K, r, n, "resid_only", seed=1)
+    c.w.zero_()
+    c.resid.zero_()
+    c.run()
+    torch.cuda.synchronize()
+    assert L.lsk_device_error() == 0
+    want = torch.zeros((T, 136), dtype=torch.float64, device="cuda")
+    for a in range(n):
+        rows = torch.nonzero(c.ids == a).flatten()
+        want[rows] = float(c.scale[a]) * (c.x[rows].double() @ c.down[a].double().T) @ c.up[a].double().T
+    up = min(3 * -(-r // 16), 4 * 16)             # products of the adapter's own chain
+    assert _error(c.out32[:T], want) <= _cut(4 * stages + up)
