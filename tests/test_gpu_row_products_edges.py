@@ -128,3 +128,18 @@ def test_the_adapters_part_alone_has_its_24_bits(T, K, r, n, stages):
         want[rows] = float(c.scale[a]) * (c.x[rows].double() @ c.down[a].double().T) @ c.up[a].double().T
     up = min(3 * -(-r // 16), 4 * 16)             # products of the adapter's own chain
     assert _error(c.out32[:T], want) <= _cut(4 * stages + up)
+
+
+@pytest.mark.parametrize("epi", ["resid", "resid_only"])
+@pytest.mark.parametrize("T,N,K", [(1, 520, 13824), (16, 136, 5120), (64, 1000, 13824), (128, 264, 5120), (128, 2560, 13824), (129, 264, 5120), (300, 520, 13824),
+                                   (1024, 2056, 5120), (700, 136, 2048), (300, 1024, 1024)])
+def test_the_shared_part_alone_is_summed_in_short_chains(T, N, K, epi):
+    c = Lora(T, N, K, 16, 3, epi, ids=[-1] * T, seed=2)
+    c.resid.zero_()
+    if c.bias is not None:
+        c.bias.zero_()
+    c.run()
+    torch.cuda.synchronize()
+    assert L.lsk_device_error() == 0
+    stages = 4 if T <= 128 else 8 if K <= 2048 else 16
+    assert _error(c.out32[:T], c.x.double() @ c.w.double().T) <= _cut(4 * stages)
