@@ -841,8 +841,12 @@ def lsk_gemm_lora_bf16(epilogue: int, A, B, adapters: LoraAdapters, ids, C_out, 
         _stream(stream)))
 
 
-def _packed(codes, scales, what: str):
-    """Stacked MXFP4 matrices' addresses and the bytes between them."""
+def _packed(codes, scales, N: int, K: int, what: str):
+    """Addresses of stacked MXFP4 matrices of N rows of K values (or more rows) and the bytes between them."""
+    for t, pitch, name in ((codes, (K + 127) // 128 * 64, "_codes"), (scales, (K + 511) // 512 * 16, "_scales")):
+        rows = t.shape[1:]
+        if (rows[1] != pitch or rows[0] < N) if len(rows) == 2 else t.numel() < t.shape[0] * N * pitch:
+            raise ValueError(f"{what + name} of {tuple(rows)} a group are not {N} rows of {pitch} bytes")
     if codes.dtype is _U8 and scales.dtype is _U8 and codes.is_contiguous() and scales.is_contiguous():
         return codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0)
     _bind_types()
@@ -861,13 +865,17 @@ def lsk_gemm_grouped_bf16_mxfp4(epilogue: int, A, B_codes, B_scales, group_bound
     C_out [M, N] bf16, float32 for LSK_EPI_SCALE_F32; all but the groups dense. gather_k > 0: row i is A's row row_table[i] // gather_k."""
     if B_codes.shape[0] < n_groups or (B2_codes is not None and B2_codes.shape[0] < n_groups):
         raise ValueError(f"fewer matrices than {n_groups} groups")
-    bc, bs, cs, ss = _packed(B_codes, B_scales, "B")
+    bc, bs, cs, ss = _packed(B_codes, B_scales, N, K, "B")
     b2c = b2s = 0
     if B2_codes is not None:
-        b2c, b2s, c2, s2 = _packed(B2_codes, B2_scales, "B2")
+        b2c, b2s, c2, s2 = _packed(B2_codes, B2_scales, N, K, "B2")
         if (c2 != cs or s2 != ss) and n_groups > 1:
             raise ValueError("B and B2 need the same distance between groups")
+    if len(A.shape) != 2 or A.shape[1] != K:
+        raise ValueError(f"A of {tuple(A.shape)} has no rows of {K} values")
     f32 = epilogue == LSK_EPI_SCALE_F32
+    if f32 and getattr(row_weight, "dtype", None) is not None and row_weight.numel() < M:
+        raise ValueError(f"row_weight has {row_weight.numel()} values, not {M}")
     try:
         usual = (A.dtype is _BF16 and C_out.dtype is (_F32 if f32 else _BF16) and group_bounds.dtype is _INT32 and A.is_contiguous()
                  and C_out.is_contiguous() and group_bounds.is_contiguous() and group_bounds.numel() > n_groups)
