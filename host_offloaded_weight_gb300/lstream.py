@@ -841,19 +841,25 @@ def lsk_gemm_lora_bf16(epilogue: int, A, B, adapters: LoraAdapters, ids, C_out, 
         _stream(stream)))
 
 
-def _packed(codes, scales, N: int, K: int, what: str):
-    """Addresses of stacked MXFP4 matrices of N rows of K values (or more rows) and the bytes between them."""
-    for t, pitch, name in ((codes, (K + 127) // 128 * 64, "_codes"), (scales, (K + 511) // 512 * 16, "_scales")):
-        rows = t.shape[1:]
-        if (rows[1] != pitch or rows[0] < N) if len(rows) == 2 else t.numel() < t.shape[0] * N * pitch:
-            raise ValueError(f"{what + name} of {tuple(rows)} a group are not {N} rows of {pitch} bytes")
+def _packed(codes, scales, n: int, N: int, K: int, what: str):
+    """Addresses of n or more stacked MXFP4 matrices, each of N rows of K values (or more rows), and the bytes between them."""
+    cp, sp = (K + 127) // 128 * 64, (K + 511) // 512 * 16
     if codes.dtype is _U8 and scales.dtype is _U8 and codes.is_contiguous() and scales.is_contiguous():
-        return codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0)
+        c, s = codes.stride(), scales.stride()
+        if len(c) == len(s) == 3:
+            cs, ss = c[0], s[0]
+            if c[1] == cp and s[1] == sp and cs >= N * cp and ss >= N * sp and codes.numel() >= n * cs and scales.numel() >= n * ss:
+                return codes.data_ptr(), scales.data_ptr(), cs, ss
     _bind_types()
-    for t, name in ((codes, what + "_codes"), (scales, what + "_scales")):
+    for t, pitch, name in ((codes, cp, what + "_codes"), (scales, sp, what + "_scales")):
         if t.itemsize != 1:
             raise TypeError(f"{name} has to be bytes, not {t.dtype}")
         _expert_rows(t, name)
+        if t.shape[0] < n:
+            raise ValueError(f"{name} has fewer matrices than {n} groups")
+        rows = t.shape[1:]
+        if (rows[1] != pitch or rows[0] < N) if len(rows) == 2 else t.numel() < t.shape[0] * N * pitch:
+            raise ValueError(f"{name} of {tuple(rows)} a group are not {N} rows of {pitch} bytes")
     return codes.data_ptr(), scales.data_ptr(), codes.stride(0), scales.stride(0)
 
 
@@ -863,16 +869,15 @@ def lsk_gemm_grouped_bf16_mxfp4(epilogue: int, A, B_codes, B_scales, group_bound
     """Rows sorted by group through the groups' MXFP4 matrices: B_codes [n_groups, N, code pitch] and B_scales [n_groups, N, scale pitch]
     (LSK_EPI_SWIGLU: B2 likewise), A [rows, K] bf16, group_bounds [n_groups + 1] and row_table [M] int32, row_weight [M] float32,
     C_out [M, N] bf16, float32 for LSK_EPI_SCALE_F32; all but the groups dense. gather_k > 0: row i is A's row row_table[i] // gather_k."""
-    if B_codes.shape[0] < n_groups or (B2_codes is not None and B2_codes.shape[0] < n_groups):
-        raise ValueError(f"fewer matrices than {n_groups} groups")
-    bc, bs, cs, ss = _packed(B_codes, B_scales, N, K, "B")
+    bc, bs, cs, ss = _packed(B_codes, B_scales, n_groups, N, K, "B")
     b2c = b2s = 0
     if B2_codes is not None:
-        b2c, b2s, c2, s2 = _packed(B2_codes, B2_scales, N, K, "B2")
+        b2c, b2s, c2, s2 = _packed(B2_codes, B2_scales, n_groups, N, K, "B2")
         if (c2 != cs or s2 != ss) and n_groups > 1:
             raise ValueError("B and B2 need the same distance between groups")
-    if len(A.shape) != 2 or A.shape[1] != K:
-        raise ValueError(f"A of {tuple(A.shape)} has no rows of {K} values")
+    rows = A.shape
+    if len(rows) != 2 or rows[1] != K:
+        raise ValueError(f"A of {tuple(rows)} has no rows of {K} values")
     f32 = epilogue == LSK_EPI_SCALE_F32
     if f32 and getattr(row_weight, "dtype", None) is not None and row_weight.numel() < M:
         raise ValueError(f"row_weight has {row_weight.numel()} values, not {M}")
@@ -887,5 +892,5 @@ def lsk_gemm_grouped_bf16_mxfp4(epilogue: int, A, B_codes, B_scales, group_bound
         _bind_types()
         a, g, c = _values(A, 0, "A"), _ids(group_bounds, "group_bounds", n_groups + 1), _values(C_out, int(f32), "C_out")
     return _check(_lib.lsk_gemm_grouped_bf16_mxfp4(
-        epilogue, a, A.shape[0], bc, bs, b2c, b2s, cs, ss, g, n_groups, 0 if row_table is None else _ids(row_table, "row_table", M),
+        epilogue, a, rows[0], bc, bs, b2c, b2s, cs, ss, g, n_groups, 0 if row_table is None else _ids(row_table, "row_table", M),
         0 if row_weight is None else _values(row_weight, 1, "row_weight"), gather_k, c, M, N, K, _stream(stream)))

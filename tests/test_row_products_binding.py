@@ -41,6 +41,17 @@ def test_tensors_of_other_sizes_are_refused(name, shape):
             _call(epi, n=n, **{name: torch.zeros(shape, dtype=BF16 if name == "A" else U8)})
 
 
+@pytest.mark.parametrize("name,pitch", [("codes", 320), ("scales", 32), ("B2_codes", 320), ("B2_scales", 32)])
+def test_a_matrix_for_each_group(name, pitch):
+    epi = L.LSK_EPI_SWIGLU if name.startswith("B2") else L.LSK_EPI_STORE
+    with pytest.raises(ValueError):
+        _call(epi, **{name: torch.zeros((E - 1, N, pitch), dtype=U8)})
+    assert _call(epi, n=E - 1, **{name: torch.zeros((E - 1, N, pitch), dtype=U8)}) == L.LS_OK
+    one = torch.zeros((1, N + 4, pitch), dtype=U8)[:, :N]           # a stride that says more than there is
+    with pytest.raises(ValueError):
+        _call(epi, **{name: one})
+
+
 def test_a_weight_for_each_row_that_the_table_may_name():
     with pytest.raises(ValueError):
         _call(L.LSK_EPI_SCALE_F32, rows=M, row_weight=torch.zeros(M - 1))
