@@ -143,3 +143,41 @@ def test_the_shared_part_alone_is_summed_in_short_chains(T, N, K, epi):
     assert L.lsk_device_error() == 0
     stages = 4 if T <= 128 else 8 if K <= 2048 else 16
     assert _error(c.out32[:T], c.x.double() @ c.w.double().T) <= _cut(4 * stages)
+
+
+@pytest.mark.parametrize("T,K,r,n", [(70, 40000, 16, 3), (1500, 30000, 136, 40)])
+def test_long_slices_in_flight_captured_and_again_the_same_bits(T, K, r, n):
+    """Calls whose h is summed in rounds: three of them on streams of their own, then two captured ones replayed in turn."""
+    cases = [Lora(T, 200, K, r, n, "resid", seed=s) for s in range(3)]
+    for c in cases:
+        c.run()
+    torch.cuda.synchronize()
+    assert L.lsk_device_error() == 0
+    first = [(c.out.clone(), c.out32.clone()) for c in cases]
+
+    def same():
+        torch.cuda.synchronize()
+        assert L.lsk_device_error() == 0
+        for c, (a, b) in zip(cases, first):
+            assert torch.equal(c.out, a) and torch.equal(c.out32, b)
+            c.out[:T].fill_(0)       # not the row behind the last
+            c.out32[:T].fill_(0)
+
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for c, s in zip(cases, streams):
+            c.run(stream=s)
+    same()
+    graphs = []
+    for c in cases[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[0]):
+            c.run(stream=streams[0])
+        graphs.append(g)
+    cases[2].run()
+    for _ in range(4):
+        for g in graphs:
+            g.replay()
+    same()
