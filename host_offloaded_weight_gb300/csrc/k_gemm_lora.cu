@@ -10,14 +10,16 @@
 // 0 times infinity is NaN, so in a block an adapter with a NaN or an infinity would reach rows of other requests.
 //
 // What bounds it. 16 rows with 14 adapters of rank 16 beside 13824 x 5120: 35 us, the weights alone (ids of no adapter) 31, the floor
-// 22; 64 rows and 24 adapters of rank 32 beside 5120 x 13824, fp32 results too: 51 us, alone 36. What the adapters add is the
-// time of the first kernel, whose loads queue behind the stream of weights (14 us for the 64 rows, 21 MB of `down`; the product
-// starts on the SMs that it leaves), and the stages of `up` at the end (5 us). One row beside 4096 x 1024 takes 14 us, a chain of
-// latencies: ids 1, first load 2.5, sums 1.5, the next kernel's look at them 1.5, `up` 2, results 1.5, and two launches.
+// 22; 64 rows and 24 adapters of rank 32 beside 5120 x 13824, fp32 results too: 50.5 us, alone 36. What the adapters add is the
+// time of the first kernel, whose loads queue behind the stream of weights (14 us for the 64 rows, 21 MB of `down`; its 48 CTAs and the
+// product's 120 have 152 SMs, so 6 of the product's 40 clusters of three start when h is done), and the stages of `up` at the end (5 us).
+// One row beside 4096 x 1024 takes 13.5 us, a chain of latencies: ids 1, first load 2.5, sums 1.5, the next kernel's look at them 1.5,
+// `up` 2, results 1.5, and two launches.
 // Rows of full tiles: 2048 rows gate/up beside 13824 x 5120 take 372 us, lsk_gemm_bf16 in turn with it 341 (20 us the first kernel,
 // 8 the stages of `up`); 4096 rows of 4096 x 1024 with rank 64 45 and 30. The pair kernel starts when h is computed.
 // Tiles of fewer weight rows, so that all SMs have a share of the weights, changed nothing (13824 rows in 144 tiles of 96 in place
-// of 108 of 128: 30.8 us both, and 41 for 35 with adapters, whose kernel then finds no SM free).
+// of 108 of 128: 30.8 us both, and 41 for 35 with adapters, whose kernel then finds no SM free). That is 4.6 TB/s of the weights alone
+// where a copy moves 6.7: what the other 9 us are is not known.
 //
 // Up to 128 rows (gemm_lora_few_kernel, below): the weights are the left operand (128 rows a tile) and the tokens the
 // right one, 16 to 128 columns. Each part of `up` is looked over in shared memory before its product.

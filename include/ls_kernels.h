@@ -283,14 +283,20 @@ typedef struct lsk_lora {
 
 /* lsk_gemm_bf16 with an adapter of its own for each row:
  *   C[t] = epilogue(A[t] B^T + scale_a (A[t] down_a^T) up_a^T),  a = ids_dev[t]
- * and nothing added where ids_dev[t] is not one of 0 .. n-1 (say, -1). All epilogues, arguments and alignments of
- * lsk_gemm_bf16; with LSK_EPI_SWIGLU the gate's and the other projection's parts are added before the SiLU and the product.
+ * and nothing added where ids_dev[t] is not one of 0 .. n-1 (say, -1). All epilogues and alignments of lsk_gemm_bf16, and its
+ * arguments but max_ctas: there is no holding it back to some of the SMs. With LSK_EPI_SWIGLU the gate's and the other projection's
+ * parts are added before the SiLU and the product.
  * Sums are fp32 in a fixed order; A[t] down_a^T, scaled, enters the second product as two bf16 terms (16 bits), with C32
- * as three (24). Rows of one adapter cost least side by side (a tile takes up to 256 rows and pays for each adapter among
- * them). An adapter with a NaN or an infinity makes NaN or infinities of its own rows, wholly or in part; rows of others are
- * as if it were not there. Takes scratch on `stream` from the library's pool (LS_ERR_OOM if refused): 4 to 8 rank bytes, rounded up, for each row of a tile and each
- * adapter that it could hold, min(n, 256) of them. K up to 2^24. LS_ERR_UNSUPPORTED for ranks above 256 or more scratch rows
- * than 2^31. */
+ * as three (24). Tensor cores cut their sums off, so a sum is broken up: after 256 values of K up to 128 rows, and with C32 after 512 or
+ * 1024 above, A[t] down_a^T included. fp32 results are off by 1.2e-6 of their norm at most (K up to 13824; 1.9e-6 where all
+ * products are positive). Without C32 a sum above 128 rows is one chain, as in lsk_gemm_bf16.
+ * Rows of one adapter cost least side by side (a tile takes up to 256 rows and pays for each adapter among them).
+ * An adapter with a NaN or an infinity makes NaN or infinities of its own rows: of all their columns, or, up to 128 rows, of the
+ * columns of those tiles (128 columns, 64 with LSK_EPI_SWIGLU) whose rows of `up` have it. Rows of others are as if it were not there.
+ * Takes scratch on `stream` from the library's pool (LS_ERR_OOM if refused), for resident adapters whether they are in use or not:
+ * M, rounded up to 16, 32, 64, 128 or a multiple of 256, times n (at most as many as a tile has rows, 256), times the rank, rounded up to 16,
+ * 32 or a multiple of 64, times 4 bytes (6 with C32), above 128 rows 6 (8); twice that for LSK_EPI_SWIGLU. 4096 rows beside 256
+ * adapters of rank 64: 0.4 GB, gate and up 0.8. K up to 2^24. LS_ERR_UNSUPPORTED for ranks above 256 or more scratch rows than 2^31. */
 ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A_dev, const void* B_dev, int64_t b_rows, int32_t b2_row_off,
                              const lsk_lora* adapters, const int32_t* ids_dev, const void* bias_dev,
                              const void* resid_dev, int32_t resid_f32, void* C_dev, void* C32_dev, int32_t M, int32_t N,
@@ -305,8 +311,10 @@ ls_status lsk_gemm_lora_bf16(int32_t epilogue, const void* A_dev, const void* B_
  *   LSK_EPI_SCALE_F32  C[row_table[i]] = row_weight[row_table[i]] * a_i B_g^T -> fp32 [M, N]  (entries outside 0 .. M-1 are skipped)
  * M: rows of the table and of C. Groups may be empty; rows of C that belong to no group are left as they were. A's values enter as
  * in lsk_gemm_bf16_mxfp4 (exact down to 2^-13 of the largest of their block of 32, within 2^-22 of that largest below); sums are
- * fp32 in a fixed order, SiLU takes __expf. Any K and N from 1 up where A's rows are 16-byte aligned (K a multiple of 8);
- * bounds outside 0 .. M are cut to it, and a row that bounds out of order give to two groups has the one's or the other's values.
+ * fp32 in a fixed order, each a single chain of K, off by 4e-8 of their norm at K = 768 and 8e-8 at 14336 for values of either sign, by 5e-8
+ * and 1.6e-6 where all products are positive (2.3e-5 at 65536). SiLU takes __expf. Any K and N from 1 up where A's rows are 16-byte
+ * aligned (K a multiple of 8). It takes all SMs, as there is no max_ctas. Bounds outside 0 .. M are cut to it, and a row that bounds out of
+ * order give to two groups has the one's or the other's values.
  * Codes 32-byte aligned, strides of them multiples of 32 bytes; scales, A and strides of
  * scales 16; with one group the strides are not read. n_groups <= 256, M up to 2^30 (LS_ERR_UNSUPPORTED above). Takes scratch on
  * `stream` from the library's pool, 2 M (K + K / 32) bytes and the padding (LS_ERR_OOM if refused). */
