@@ -876,7 +876,7 @@ def lsk_gemm_grouped_bf16_mxfp4(epilogue: int, A, B_codes, B_scales, group_bound
         if (c2 != cs or s2 != ss) and n_groups > 1:
             raise ValueError("B and B2 need the same distance between groups")
     rows = A.shape
-    if (len(rows) != 2 or rows[1] != K) and K % 8 == 0:      # (the library refuses other K)
+    if A.numel() != rows[0] * K and K % 8 == 0:      # (the library refuses other K)
         raise ValueError(f"A of {tuple(rows)} has no rows of {K} values")
     f32 = epilogue == LSK_EPI_SCALE_F32
     if f32 and getattr(row_weight, "dtype", None) is not None and row_weight.numel() < M:

@@ -29,6 +29,7 @@ def test_tensors_of_the_named_sizes_and_larger_ones_are_taken():
     assert _call(codes=torch.zeros((E + 1, N + 2, cp), dtype=U8), scales=torch.zeros((E, N + 5, sp), dtype=U8)) == L.LS_OK
     assert _call(codes=torch.zeros((E, N * cp), dtype=U8), scales=torch.zeros((E, N * sp + 16), dtype=U8)) == L.LS_OK   # blobs
     assert _call(row_weight=torch.zeros(M + 3), A=torch.zeros((1, K), dtype=BF16)) == L.LS_OK
+    assert _call(A=torch.zeros((M, 8, K // 8), dtype=BF16)) == L.LS_OK                                                    # heads side by side
 
 
 @pytest.mark.parametrize("name,shape", [("codes", (E, N, 256)), ("codes", (E, N - 1, 320)), ("codes", (E, N, 384)), ("codes", (E, N * 320 - 32)),
